@@ -322,6 +322,70 @@ spec_status spec_debug_wait_probe(spec_model* m, int64_t budget_cycles, void* st
 spec_status spec_kv_write(spec_model* m, int32_t seq_id, int32_t n_tokens, const uint16_t* k, const uint16_t* v,
                           void* stream);
 
+/* ------------------------------------------------ 4-bit paged KV cache (no model)
+ *
+ * A pool of num_pages pages of 64 tokens, in device memory of the caller: one block
+ * of spec_kv4_block_bytes(head_dim) = 64 * head_dim + 512 bytes per (page, kv head),
+ * [num_pages, n_kv_heads, block], 16-byte aligned.  Against fp16 K/V it is 3.76x
+ * smaller at head_dim 128 and 3.56x at 64.  Per (token, kv head), K and V each, the
+ * values x become
+ *     x' = clamp(x, -65504, 65504), NaN -> -65504 (the library's fp16 saturation)
+ *     m  = fp16 rounded down of min x',   s = fp16 rounded up of (max x' - m) / 15
+ *     c  = floor((x' - m) / s + 1/2) in 0..15, 0 where s = 0
+ * and the cache holds c (4 bits), s and m (fp16) and stands for s * c + m.  (A
+ * quotient less than 2^-20 of its value below a half counts as the half.)  The
+ * order of the bytes inside a block is the library's own: write with spec_kv4_write,
+ * take values out with spec_kv4_read.
+ *
+ * Rows of a call: sequence b owns flat rows row_off[b] .. row_off[b + 1] - 1 (device
+ * [B + 1], non-decreasing, row_off[0] >= 0), or rows_per_seq rows each where row_off
+ * is NULL (total_rows = B * rows_per_seq).  Its rows sit at token positions start[b],
+ * start[b] + 1, ... (device [B]) of page_table[b] (device [B, max_pages], entries in
+ * 0..num_pages-1).  Rows of no sequence are left as they are.  A position past the
+ * page table, or whose page entry is outside the pool (-1: none), has no cell: it is
+ * not written, reads as zeros and is never attended to.
+ * dtype (SPEC_F16 or SPEC_BF16) is the type of the caller's k, v, q and out.  Strides
+ * are elements between consecutive rows (multiples of 8; heads are contiguous within
+ * a row), so views into a fused projection's output can be passed.
+ * No call allocates or keeps state, so calls may run on any streams at once; calls
+ * that write cells another call uses need the caller's ordering.  Two rows of one
+ * write must not map to the same cell.  The streams' device must be current. */
+typedef enum spec_dtype { SPEC_F16 = 0, SPEC_BF16 = 1 } spec_dtype;
+
+/* Bytes of one (page, kv head) block; 0 for an unsupported head_dim. */
+int64_t spec_kv4_block_bytes(int32_t head_dim);
+
+/* Quantise rows k, v [total_rows, n_kv_heads, head_dim] into their cells. */
+spec_status spec_kv4_write(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                           const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* k, const void* v,
+                           int64_t k_stride, int64_t v_stride, void* pool, void* stream);
+
+/* Expand cells to k, v (contiguous [total_rows, n_kv_heads, head_dim]): s * c + m,
+ * rounded once (fp16: at most 65504). */
+spec_status spec_kv4_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                          const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* pool, void* k, void* v,
+                          void* stream);
+
+/* Attention of the verify window over the cache.  q [total_rows, n_heads, head_dim],
+ * out the same, contiguous.  Sequence b's window is its rows (at most W, 1..16; with
+ * row_off NULL W each), whose K/V are already in the cache at positions kv_len[b],
+ * kv_len[b] + 1, ...; row j sees positions < kv_len[b] and the window rows that are
+ * its ancestors (parent_host: HOST [W] as in spec_verify_tree_step, or NULL: the
+ * chain 0..j).  W = 1 is the decode step.  Query head h reads kv head
+ * h / (n_heads / n_kv_heads); scores are scale * (q . k), softmax in fp32, one
+ * rounding of the result (weights are fp16 with fp32 accumulation).  A row that sees
+ * nothing is zeros.  Rows of a sequence beyond W are left as they are.
+ * W * (n_heads / n_kv_heads) <= 64.  max_kv_len: an upper bound of kv_len for the
+ * launch shape, 0: unknown (results do not depend on it beyond the order of the
+ * sums). */
+spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
+                               const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t n_heads,
+                               int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* q, int64_t q_stride,
+                               const int32_t* parent_host, float scale, int32_t max_kv_len, const void* pool,
+                               void* out, void* stream);
+
 /* Timing aid for long contexts: give each sequence (host ids) lens_host[b]
  * cached tokens with pseudo-random bf16 K/V (a hash of seed and position, scaled
  * by `scale`), without running the model.  Attention time does not depend on

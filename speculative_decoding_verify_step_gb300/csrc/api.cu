@@ -1,6 +1,7 @@
 // C ABI of the verify-round library: model arena, tensor maps, the forward
 // schedule, and every entry point declared in spec_verify.h.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -12,6 +13,8 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "kv4.cuh"
+#include "kv4.h"
 #include "sampling.cuh"
 
 namespace spec {
@@ -1275,6 +1278,182 @@ spec_status spec_sync_status(spec_model* m, void* stream) {
   // calls use the single-CTA tensor-core tiles instead.
   if (code == SPEC_ERR_UNSUPPORTED) m->pair_ok = false;
   if (code != 0) return fail((spec_status)code, "device reported status %d", code);
+  return SPEC_OK;
+}
+
+// ------------------------------------------------------------ 4-bit paged KV cache
+}  // extern "C"
+
+namespace {
+
+spec_status kv4_check(int B, int total_rows, int rows_per_seq, const int32_t* row_off, int max_pages, int num_pages,
+                      int Hkv, int hd, int dtype) {
+  if (hd != 64 && hd != 128) return fail(SPEC_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (B < 1 || B > 65535) return fail(SPEC_ERR_INVALID_ARG, "B=%d outside 1..65535", B);
+  if (Hkv < 1 || Hkv > 65535) return fail(SPEC_ERR_INVALID_ARG, "n_kv_heads=%d outside 1..65535", Hkv);
+  if (num_pages < 1 || num_pages > (1 << 24)) return fail(SPEC_ERR_INVALID_ARG, "num_pages=%d outside 1..2^24", num_pages);
+  if (max_pages < 1 || max_pages > (1 << 24)) return fail(SPEC_ERR_INVALID_ARG, "max_pages=%d outside 1..2^24", max_pages);
+  if (dtype != SPEC_F16 && dtype != SPEC_BF16) return fail(SPEC_ERR_INVALID_ARG, "dtype must be SPEC_F16 or SPEC_BF16");
+  if (total_rows < 0 || total_rows > (1 << 30)) return fail(SPEC_ERR_INVALID_ARG, "total_rows=%d outside 0..2^30", total_rows);
+  if (rows_per_seq < 0) return fail(SPEC_ERR_INVALID_ARG, "negative rows per sequence");
+  if (!row_off && (long long)B * rows_per_seq != total_rows)
+    return fail(SPEC_ERR_INVALID_ARG, "total_rows=%d is not B * rows per sequence (%d * %d)", total_rows, B, rows_per_seq);
+  return SPEC_OK;
+}
+
+spec_status kv4_check_ptr(const void* p, const char* name) {
+  if (!p) return fail(SPEC_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & 15u) return fail(SPEC_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  return SPEC_OK;
+}
+
+spec_status kv4_check_stride(long long stride, long long least, const char* name) {
+  if (stride < least || stride % 8)
+    return fail(SPEC_ERR_INVALID_ARG, "%s=%lld must be a multiple of 8 and at least %lld elements", name, stride, least);
+  return SPEC_OK;
+}
+
+Kv4Rows kv4_rows(int B, int rows_per_seq, int total_rows, const int32_t* row_off, const int32_t* start,
+                 const int32_t* page_table, int max_pages, int num_pages) {
+  Kv4Rows r{};
+  r.row_off = row_off;
+  r.start = start;
+  r.page_table = page_table;
+  r.B = B;
+  r.rows_per_seq = rows_per_seq;
+  r.max_pages = max_pages;
+  r.num_pages = num_pages;
+  r.total_rows = total_rows;
+  return r;
+}
+
+// SM count of the current device (asked for once per device).
+cudaError_t current_sm_count(int* out) {
+  static std::atomic<int> counts[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = counts[dev & 63].load(std::memory_order_relaxed);
+  if (n == 0) {
+    e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    counts[dev & 63].store(n, std::memory_order_relaxed);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t spec_kv4_block_bytes(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? kPage * head_dim + 2 * kPage * 4 : 0;
+}
+
+spec_status spec_kv4_write(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                           const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* k, const void* v,
+                           int64_t k_stride, int64_t v_stride, void* pool, void* stream) {
+  if (spec_status s = kv4_check(B, total_rows, rows_per_seq, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype))
+    return s;
+  if (total_rows == 0) return SPEC_OK;
+  if (!start || !page_table) return fail(SPEC_ERR_INVALID_ARG, "start or page_table is NULL");
+  if (spec_status s = kv4_check_ptr(k, "k")) return s;
+  if (spec_status s = kv4_check_ptr(v, "v")) return s;
+  if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
+  if (spec_status s = kv4_check_stride(k_stride, (long long)n_kv_heads * head_dim, "k_stride")) return s;
+  if (spec_status s = kv4_check_stride(v_stride, (long long)n_kv_heads * head_dim, "v_stride")) return s;
+  Kv4WriteParams p{};
+  p.rows = kv4_rows(B, rows_per_seq, total_rows, row_off, start, page_table, max_pages, num_pages);
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.bf16 = dtype == SPEC_BF16;
+  p.k = k;
+  p.v = v;
+  p.row_blk = 1 << 30;  // one block: plain rows
+  p.blk_stride = 0;
+  p.k_row_stride = k_stride;
+  p.v_row_stride = v_stride;
+  p.head_stride = head_dim;
+  p.pool = static_cast<uint8_t*>(pool);
+  CUDA_TRY(launch_kv4_write(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+spec_status spec_kv4_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                          const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* pool, void* k, void* v,
+                          void* stream) {
+  if (spec_status s = kv4_check(B, total_rows, rows_per_seq, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype))
+    return s;
+  if (total_rows == 0) return SPEC_OK;
+  if (!start || !page_table) return fail(SPEC_ERR_INVALID_ARG, "start or page_table is NULL");
+  if (spec_status s = kv4_check_ptr(k, "k")) return s;
+  if (spec_status s = kv4_check_ptr(v, "v")) return s;
+  if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
+  Kv4ReadParams p{};
+  p.rows = kv4_rows(B, rows_per_seq, total_rows, row_off, start, page_table, max_pages, num_pages);
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.bf16 = dtype == SPEC_BF16;
+  p.k = k;
+  p.v = v;
+  p.pool = static_cast<const uint8_t*>(pool);
+  CUDA_TRY(launch_kv4_read(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
+                               const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t n_heads,
+                               int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* q, int64_t q_stride,
+                               const int32_t* parent_host, float scale, int32_t max_kv_len, const void* pool,
+                               void* out, void* stream) {
+  if (W < 1 || W > kMaxWidth) return fail(SPEC_ERR_INVALID_ARG, "width %d outside 1..%d", W, kMaxWidth);
+  if (spec_status s = kv4_check(B, total_rows, W, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype)) return s;
+  if (n_heads < 1 || n_heads % n_kv_heads)
+    return fail(SPEC_ERR_INVALID_ARG, "n_heads=%d must be a multiple of n_kv_heads=%d", n_heads, n_kv_heads);
+  if ((long long)W * (n_heads / n_kv_heads) > 64)
+    return fail(SPEC_ERR_UNSUPPORTED, "width * group size must be <= 64 (%d * %d)", W, n_heads / n_kv_heads);
+  if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID_ARG, "scale is not finite");
+  if (max_kv_len < 0) return fail(SPEC_ERR_INVALID_ARG, "max_kv_len is negative");
+  int depth[16];
+  uint32_t anc[16];
+  if (parent_host) {
+    if (spec_status s = tree_masks(W, parent_host, depth, anc)) return s;
+  } else {
+    chain_masks(W, depth, anc);
+  }
+  if (total_rows == 0) return SPEC_OK;
+  if (!kv_len || !page_table) return fail(SPEC_ERR_INVALID_ARG, "kv_len or page_table is NULL");
+  if (spec_status s = kv4_check_ptr(q, "q")) return s;
+  if (spec_status s = kv4_check_ptr(out, "out")) return s;
+  if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
+  if (spec_status s = kv4_check_stride(q_stride, (long long)n_heads * head_dim, "q_stride")) return s;
+  Kv4AttnParams p{};
+  p.q = q;
+  p.q_row_stride = q_stride;
+  p.out = out;
+  p.bf16 = dtype == SPEC_BF16;
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.page_table = page_table;
+  p.kv_len = kv_len;
+  p.row_begin = row_off;
+  p.B = B;
+  p.W = W;
+  p.total_rows = total_rows;
+  p.Hq = n_heads;
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.table_rows = B;
+  p.scale = scale;
+  for (int j = 0; j < 16; ++j) p.anc[j] = j < W ? anc[j] : 0u;
+  const long long cap = (long long)max_pages * kPage;
+  p.kv_len_hint = (int)std::min<long long>(max_kv_len > 0 ? (long long)max_kv_len + W : cap, cap);
+  CUDA_TRY(current_sm_count(&p.sm_count));
+  CUDA_TRY(launch_kv4_attention(p, static_cast<cudaStream_t>(stream)));
   return SPEC_OK;
 }
 

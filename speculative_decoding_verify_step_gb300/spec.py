@@ -43,7 +43,8 @@ EXPORTS = ["spec_model_create", "spec_model_destroy", "spec_model_set_weight", "
            "spec_accept_greedy", "spec_get_kv_state", "spec_read_kv", "spec_debug_logits", "spec_debug_wait_probe",
            "spec_kv_fill_random", "spec_sync_status", "spec_max_pages_per_seq", "spec_last_launch_count", "spec_last_error",
            "spec_set_profiling", "spec_read_profile", "spec_accept_greedy_noalloc", "spec_verify_ragged",
-           "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write"]
+           "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write",
+           "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention"]
 
 RAGGED_CAP_ACCEPT, RAGGED_COMPACT = 1, 2
 
@@ -91,6 +92,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_set_profiling": (I32, [P, I32]),
         "spec_accept_greedy_noalloc": (I32, [I32, I32, I32, P, P, P, P, P, P]),
         "spec_read_profile": (I32, [P, P, P, P]),
+        "spec_kv4_block_bytes": (I64, [I32]),
+        "spec_kv4_write": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, I64, I64, P, P]),
+        "spec_kv4_read": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, P]),
+        "spec_kv4_attention": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, I32, P, I64, P, F32, I32, P, P,
+                                     P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -433,3 +439,142 @@ def spec_accept_greedy(logits: torch.Tensor, x: Optional[torch.Tensor]):
     _check(lib.spec_accept_greedy(B, W - 1, V, _ptr(lg), _ptr(xx), _ptr(acc), _ptr(com), _ptr(bon), _stream()))
     torch.cuda.current_stream().synchronize()
     return acc, com, bon
+
+
+# ------------------------------------------------------------- 4-bit paged KV cache
+_KV4_DTYPE = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def spec_kv4_pool(num_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """An empty 4-bit KV pool: uint8 [num_pages, n_kv_heads, 64 * head_dim + 512], pages of
+    64 tokens."""
+    block = load_library().spec_kv4_block_bytes(int(head_dim))
+    if block == 0:
+        raise ValueError("head_dim must be 64 or 128")
+    return torch.zeros(num_pages, n_kv_heads, block, dtype=torch.uint8, device=device)
+
+
+def _kv4_geometry(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor, row_off):
+    """Checked (num_pages, n_kv_heads, head_dim, B) of a call's pool and tables."""
+    if pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous() or pool.shape[2] not in (4608, 8704):
+        raise ValueError("pool must be a contiguous uint8 [num_pages, n_kv_heads, 64 * head_dim + 512] tensor "
+                         "(spec_kv4_pool)")
+    B = start.shape[0]
+    for t, shape, what in ((start, (B,), "start / kv_len"), (page_table, (B, page_table.shape[-1]), "page_table")):
+        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape}")
+    if row_off is not None and (row_off.dtype != torch.int32 or tuple(row_off.shape) != (B + 1,)
+                                or not row_off.is_contiguous()):
+        raise ValueError(f"row_off must be a contiguous int32 tensor of shape ({B + 1},)")
+    dev = pool.device
+    if dev.type != "cuda" or start.device != dev or page_table.device != dev or (
+            row_off is not None and row_off.device != dev):
+        raise ValueError("pool, start / kv_len, page_table and row_off must be on one CUDA device")
+    return pool.shape[0], pool.shape[1], (pool.shape[2] - 512) // 64, B
+
+
+def _kv4_rows(x: torch.Tensor, what: str, B: int, heads, hd: int, ragged: bool, dev):
+    """(total_rows, rows_per_seq, row stride) of x: [B, n, heads, hd], or [rows, heads, hd] with row_off.
+    The heads of a row are contiguous; rows may be strided, evenly over all of x."""
+    if x.device != dev or x.dtype not in _KV4_DTYPE:
+        raise ValueError(f"{what} must be fp16 or bf16 on {dev}")
+    lead = 1 if ragged else 2
+    if x.dim() != lead + 2 or x.shape[-1] != hd or (heads is not None and x.shape[-2] != heads) or (
+            not ragged and x.shape[0] != B):
+        want = "[rows, heads, head_dim]" if ragged else "[B, n, heads, head_dim]"
+        raise ValueError(f"{what} must be {want} with head_dim {hd}" + (f" and {heads} heads" if heads else "")
+                         + ("" if ragged else f" and B {B}"))
+    st = x.stride()
+    row = st[lead - 1] if x.shape[lead - 1] > 1 else (st[0] if lead == 2 and x.shape[0] > 1 else x.shape[-2] * hd)
+    if x.numel() and ((st[-1] != 1 and hd > 1) or (st[-2] != hd and x.shape[-2] > 1) or (
+            lead == 2 and x.shape[0] > 1 and x.shape[1] > 1 and st[0] != x.shape[1] * row)):
+        raise ValueError(f"{what}: each row must be contiguous and the rows evenly spaced")
+    if ragged:
+        return x.shape[0], 0, row
+    return x.shape[0] * x.shape[1], x.shape[1], row
+
+
+def _kv4_call(dev, fn, *args):
+    """Call `fn` with the current stream of `dev` (made current for the call where it is not)."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+
+
+def spec_kv4_write(k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor,
+                   pool: torch.Tensor, row_off: Optional[torch.Tensor] = None) -> None:
+    """Quantise K/V rows into the 4-bit cache: k, v [B, n, n_kv_heads, head_dim] at positions
+    start[b] .. start[b] + n - 1 of page_table[b], or packed [rows, n_kv_heads, head_dim]
+    with sequence b's rows row_off[b] .. row_off[b + 1] - 1.  fp16 or bf16."""
+    lib = load_library()
+    P, H, hd, B = _kv4_geometry(pool, start, page_table, row_off)
+    dev, ragged = pool.device, row_off is not None
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have one shape and type")
+    total, n, ks = _kv4_rows(k, "k", B, H, hd, ragged, dev)
+    _, _, vs = _kv4_rows(v, "v", B, H, hd, ragged, dev)
+    _kv4_call(dev, lib.spec_kv4_write, B, n, total, row_off.data_ptr() if ragged else None, start.data_ptr(),
+              page_table.data_ptr(), page_table.shape[1], P, H, hd, _KV4_DTYPE[k.dtype], k.data_ptr(), v.data_ptr(),
+              ks, vs, pool.data_ptr())
+
+
+def spec_kv4_read(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor, n: int,
+                  row_off: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float16, outs=None):
+    """K and V of n tokens per sequence from position start[b] on, as fp16 or bf16
+    [B, n, n_kv_heads, head_dim]; with row_off, n rows in all, [n, n_kv_heads, head_dim].
+    Rows of no sequence are left unwritten.  `outs`: preallocated (k, v)."""
+    lib = load_library()
+    P, H, hd, B = _kv4_geometry(pool, start, page_table, row_off)
+    dev, ragged = pool.device, row_off is not None
+    n = int(n)
+    if dtype not in _KV4_DTYPE:
+        raise ValueError("dtype must be torch.float16 or torch.bfloat16")
+    if n < 0:
+        raise ValueError("n must not be negative")
+    shape = (n, H, hd) if ragged else (B, n, H, hd)
+    if outs is None:
+        outs = (torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev))
+    k, v = outs
+    for t in (k, v):
+        if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"outs must be contiguous {dtype} tensors of shape {shape} on {dev}")
+    _kv4_call(dev, lib.spec_kv4_read, B, 0 if ragged else n, n if ragged else B * n,
+              row_off.data_ptr() if ragged else None, start.data_ptr(), page_table.data_ptr(), page_table.shape[1], P,
+              H, hd, _KV4_DTYPE[dtype], pool.data_ptr(), k.data_ptr(), v.data_ptr())
+    return k, v
+
+
+def spec_kv4_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                       row_off: Optional[torch.Tensor] = None, max_width: Optional[int] = None,
+                       parent: Optional[Sequence[int]] = None, scale: Optional[float] = None, max_kv_len: int = 0,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of verify windows over the 4-bit cache.  q [B, W, n_heads, head_dim], or packed
+    [rows, n_heads, head_dim] with row_off and at most max_width rows per sequence (default:
+    as many as a window may have).  Row j of sequence b sees positions < kv_len[b] and its
+    ancestors in the window, whose K/V sit at kv_len[b] + 0, 1, ... (parent: tree, default the
+    chain).  scale: default head_dim ** -0.5.  max_kv_len: an upper bound of kv_len if known
+    (launch shape only).  Returns q's shape and type; rows of no window are left unwritten."""
+    lib = load_library()
+    P, H, hd, B = _kv4_geometry(pool, kv_len, page_table, row_off)
+    dev, ragged = pool.device, row_off is not None
+    total, W, qs = _kv4_rows(q, "q", B, None, hd, ragged, dev)
+    Hq = q.shape[-2]
+    if ragged:
+        W = max_width if max_width is not None else max(1, min(16, 64 // max(1, Hq // H)))
+    elif max_width is not None and max_width < W:
+        raise ValueError(f"q has {W} rows per sequence, more than max_width {max_width}")
+    par = None
+    if parent is not None:
+        if len(parent) < W:
+            raise ValueError(f"parent must have {W} entries")
+        par = _i32_host(parent)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif out.dtype != q.dtype or out.device != dev or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
+    _kv4_call(dev, lib.spec_kv4_attention, B, W, total, row_off.data_ptr() if ragged else None, kv_len.data_ptr(),
+              page_table.data_ptr(), page_table.shape[1], P, Hq, H, hd, _KV4_DTYPE[q.dtype], q.data_ptr(), qs, par,
+              float(hd ** -0.5 if scale is None else scale), int(max_kv_len), pool.data_ptr(), out.data_ptr())
+    return out
