@@ -379,12 +379,18 @@ spec_status spec_kv4_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
  * nothing is zeros.  Rows of a sequence beyond W are left as they are.
  * W * (n_heads / n_kv_heads) <= 64.  max_kv_len: an upper bound of kv_len for the
  * launch shape, 0: unknown (results do not depend on it beyond the order of the
- * sums). */
+ * sums).  workspace: device memory of spec_kv4_attention_workspace() bytes for the same
+ * arguments (0: none needed, may be NULL; -1: a shape the call refuses), 16-byte aligned,
+ * for the partial results of sequences that several SMs share; it holds nothing between
+ * calls, and calls that may overlap need one each.  A device-side wait that runs out (about
+ * 2 s) leaves NaN rows. */
+int64_t spec_kv4_attention_workspace(int32_t B, int32_t W, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                     int32_t max_pages, int32_t max_kv_len);
 spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
                                const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t n_heads,
                                int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* q, int64_t q_stride,
                                const int32_t* parent_host, float scale, int32_t max_kv_len, const void* pool,
-                               void* out, void* stream);
+                               void* out, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Timing aid for long contexts: give each sequence (host ids) lens_host[b]
  * cached tokens with pseudo-random bf16 K/V (a hash of seed and position, scaled

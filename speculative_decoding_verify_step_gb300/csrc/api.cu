@@ -1327,6 +1327,12 @@ Kv4Rows kv4_rows(int B, int rows_per_seq, int total_rows, const int32_t* row_off
   return r;
 }
 
+// Upper bound of a sequence's cached and window tokens, for the launch shape.
+int kv4_len_hint(int max_pages, int max_kv_len, int W) {
+  const long long cap = std::min<long long>((long long)max_pages * kPage, 0x40000000ll);
+  return (int)std::min<long long>(max_kv_len > 0 ? (long long)max_kv_len + W : cap, cap);
+}
+
 // SM count of the current device (asked for once per device).
 cudaError_t current_sm_count(int* out) {
   static std::atomic<int> counts[64];
@@ -1404,17 +1410,30 @@ spec_status spec_kv4_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
   return SPEC_OK;
 }
 
+int64_t spec_kv4_attention_workspace(int32_t B, int32_t W, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                     int32_t max_pages, int32_t max_kv_len) {
+  if (B < 1 || W < 1 || W > kMaxWidth || n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads || max_pages < 1 ||
+      max_kv_len < 0 || (long long)W * (n_heads / n_kv_heads) > 64 || (head_dim != 64 && head_dim != 128))
+    return -1;
+  int sms = 0;
+  if (current_sm_count(&sms) != cudaSuccess) return -1;
+  return kv4_attention_workspace(B, n_kv_heads, W * (n_heads / n_kv_heads), head_dim,
+                                 kv4_len_hint(max_pages, max_kv_len, W), sms);
+}
+
 spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
                                const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t n_heads,
                                int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* q, int64_t q_stride,
                                const int32_t* parent_host, float scale, int32_t max_kv_len, const void* pool,
-                               void* out, void* stream) {
+                               void* out, void* workspace, int64_t workspace_bytes, void* stream) {
   if (W < 1 || W > kMaxWidth) return fail(SPEC_ERR_INVALID_ARG, "width %d outside 1..%d", W, kMaxWidth);
   if (spec_status s = kv4_check(B, total_rows, W, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype)) return s;
   if (n_heads < 1 || n_heads % n_kv_heads)
     return fail(SPEC_ERR_INVALID_ARG, "n_heads=%d must be a multiple of n_kv_heads=%d", n_heads, n_kv_heads);
   if ((long long)W * (n_heads / n_kv_heads) > 64)
     return fail(SPEC_ERR_UNSUPPORTED, "width * group size must be <= 64 (%d * %d)", W, n_heads / n_kv_heads);
+  if ((long long)B * n_kv_heads * max_pages > (1 << 30))
+    return fail(SPEC_ERR_UNSUPPORTED, "B * n_kv_heads * max_pages must be at most 2^30");
   if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID_ARG, "scale is not finite");
   if (max_kv_len < 0) return fail(SPEC_ERR_INVALID_ARG, "max_kv_len is negative");
   int depth[16];
@@ -1450,9 +1469,15 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
   p.table_rows = B;
   p.scale = scale;
   for (int j = 0; j < 16; ++j) p.anc[j] = j < W ? anc[j] : 0u;
-  const long long cap = (long long)max_pages * kPage;
-  p.kv_len_hint = (int)std::min<long long>(max_kv_len > 0 ? (long long)max_kv_len + W : cap, cap);
+  p.kv_len_hint = kv4_len_hint(max_pages, max_kv_len, W);
+  const int group_rows = W * (n_heads / n_kv_heads);
+  if (kv4_attention_workspace(B, n_kv_heads, group_rows, head_dim, p.kv_len_hint, 1) > 0)
+    if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
   CUDA_TRY(current_sm_count(&p.sm_count));
+  const long long need = kv4_attention_workspace(B, n_kv_heads, group_rows, head_dim, p.kv_len_hint, p.sm_count);
+  if (workspace_bytes < need)
+    return fail(SPEC_ERR_INVALID_ARG, "workspace_bytes=%lld, %lld needed", (long long)workspace_bytes, need);
+  p.workspace = static_cast<float*>(workspace);
   CUDA_TRY(launch_kv4_attention(p, static_cast<cudaStream_t>(stream)));
   return SPEC_OK;
 }

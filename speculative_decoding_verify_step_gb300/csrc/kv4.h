@@ -51,7 +51,6 @@ struct Kv4AttnParams {
   const int32_t* kv_len;       // [B] cached tokens before the window
   const int32_t* row_begin;    // [B] (or [B + 1]) first flat row of sequence b; null: b * W
   const int32_t* row_count;    // [B] rows of sequence b; null: row_begin[b + 1] - row_begin[b], or W
-  const int32_t* seq_order;    // [B] batch index of the z-th CTA group; null: z
   int B, W, total_rows, Hq, Hkv, hd;
   int max_pages, num_pages, table_rows;
   int sm_count, kv_len_hint;   // launch shape only
@@ -61,9 +60,12 @@ struct Kv4AttnParams {
   // before the predecessor let this kernel launch, so only q and the window's K/V
   // are waited for.  0: everything is.
   int early;
-  int row_tiles, stages;       // set by the launcher
+  int stages, slots, cluster;  // ring depth, CTAs resident at once, CTAs of a cluster: set by the launcher
+  float* workspace;            // kv4_attention_workspace bytes
   int* status;
 };
+// Bytes of workspace for windows of `rows` query rows per kv head (W * group size).
+long long kv4_attention_workspace(int B, int Hkv, int rows, int hd, int kv_len_hint, int sm_count);
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, cudaStream_t st);
 
 }  // namespace spec

@@ -26,22 +26,48 @@
 //   O = sum (P s)_fp16 c - 7.5 R + sum P (m + 7.5 s),
 // which leaves only the rounding of the weights of c - 7.5.  Everything else is fp32.
 //
-// One CTA of four warps per (sequence, kv head, split of its pages); the splits of a
-// sequence are a thread-block cluster that merges its partials through distributed
-// shared memory.  A page of one kv head is one block (8704 bytes at head_dim 128)
-// and one bulk copy into the ring of its warp team; a team is 1, 2 or 4 warps that
-// take different 16-token steps of a page (short caches) or different query rows
-// (wide windows).
-#include <cooperative_groups.h>
+// Work split.  A group is a sequence and a kv head.  Long groups are cut into pieces of
+// about equal length, as many as the GPU holds CTAs; a CTA takes one piece.  A group of
+// one piece is finished there; the others leave partials (unnormalised O, running
+// maximum and sum per row) in the workspace, and a second kernel merges them.  Short
+// caches need neither: the CTAs of a group are one thread-block cluster and merge
+// through distributed shared memory.  (One list of all pages cut into exactly equal
+// shares was slower: a share that crosses from one group into the next pays the
+// prologue and the epilogue twice.)
+//
+// A page of one kv head is one block (8704 bytes at head_dim 128) and one bulk copy
+// into the CTA's ring.  A team of TW warps works on a page: with TW = 1 each of the
+// four warps has pages of its own, with TW = 4 each takes 16 of the page's 64 tokens
+// for S and the softmax and a quarter of the dims for the PV product, the weights
+// passing through shared memory.  Either way every code is unpacked once per CTA.  A
+// team of four keeps a warp's accumulators small (8 registers per 8 rows, against 32),
+// so wide windows fit, and has a page's result sooner; one warp needs no barriers.
+// Measured (head_dim 128, 8 kv heads): one row tile, 2 x 65520 tokens 35 against 43 us;
+// two, 8 x 32768 tokens 78 against 88; three, 64 x 512-2048 tokens 69 against 66.  In a
+// team the scores of the next page are computed before the barrier that releases this
+// page's weights: one barrier per page.
+//
+// What bounds it.  mma.sync runs at 8 cycles per m16n8k16 and SM quarter here and shares
+// its pipe with the fp32 instructions; AND and shift take 2 cycles, exp2 and movmatrix 4
+// (measured).  Per page and 16 query rows that is 272 + 75 cycles of the first pipe, 209
+// of the integer pipe and 48 of the special functions; HBM delivers a page per SM in
+// 390.  The pipes overlap little at two warps per SM quarter, so 16 rows run at about
+// 600 cycles a page and 8 rows at about 400, next to the memory's rate.  (More CTAs per
+// SM with spilled registers, half pages, and packed fp32 pairs -- 3 cycles each -- were
+// all slower.)
+//
+// The running maximum moves only when a score passes it by more than 2^8: the
+// barrier (or vote) carries that question, and the exchange of maxima and the
+// rescaling of the accumulators are a rare branch.  Weights are then at most 2^8
+// times 2^4 (the same slack for the scale of V), far below fp16's largest.
 #include <math.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "kv4.cuh"
 #include "kv4.h"
 #include "launch.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace spec {
 
@@ -49,7 +75,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxStages = 12;  // pages in flight per CTA
+constexpr int kMaxStages = 24;        // pages of a CTA's ring
+constexpr float kNoMax = -1e30f;      // running maximum of a row that has seen no token
+constexpr float kSlack = 8.f;         // how far (log2) a score may pass the running maximum
 
 SPEC_DEVICE_INLINE float ex2(float x) {
   float y;
@@ -57,11 +85,40 @@ SPEC_DEVICE_INLINE float ex2(float x) {
   return y;
 }
 
+// D(16x8 fp32) += A(16x16 f16, row) * B(16x8 f16, col).  Not volatile: the compiler may
+// order independent products, whose latency (21 cycles, 8 cycles apart) would
+// otherwise show between two into one accumulator.
+SPEC_DEVICE_INLINE void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with D = A * B.
+SPEC_DEVICE_INLINE void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                             uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // 8 x 8 transpose of 16-bit elements across the warp.
 SPEC_DEVICE_INLINE uint32_t movmatrix_trans(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Barrier of a team (one warp or the CTA), and the same with an OR.
+template <int TW>
+SPEC_DEVICE_INLINE void team_sync() {
+  if (TW == 1) __syncwarp();
+  else __syncthreads();
+}
+template <int TW>
+SPEC_DEVICE_INLINE bool team_any(bool x) {
+  return TW == 1 ? __any_sync(0xffffffffu, x) : __syncthreads_or(x);
 }
 
 SPEC_DEVICE_INLINE void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -71,221 +128,402 @@ SPEC_DEVICE_INLINE void bulk_load(void* dst, const void* src, uint32_t bytes, ui
                : "memory");
 }
 
-template <int HD>
-struct Cfg {
-  static constexpr int kBlock = kPage * HD + 2 * kPage * 4;
-  static constexpr int kQTile = (HD / 32) * 512;  // query fragments of 8 rows
-  static constexpr int kMaxTiles = 8;             // 64 query rows
-  // two CTAs per SM: 228 KB less 1 KB of system use and this kernel's static arrays each
-  static constexpr int kSmemBudget = 112 * 1024;
-  static constexpr int stages(int tiles) {
-    const int n = (kSmemBudget - tiles * kQTile) / kBlock;
-    return n < kMaxStages ? n : kMaxStages;
+// Window geometry of sequence b, from the call's tables.
+struct Kv4Seq {
+  int sid, row0, Wb, L, n_keys, pages;
+};
+SPEC_DEVICE_INLINE Kv4Seq kv4_seq(const Kv4AttnParams& p, int b) {
+  Kv4Seq s;
+  s.sid = p.seq_ids ? p.seq_ids[b] : b;
+  s.row0 = p.row_begin ? p.row_begin[b] : b * p.W;
+  s.Wb = p.row_count ? p.row_count[b] : p.row_begin ? p.row_begin[b + 1] - s.row0 : p.W;
+  s.row0 = max(0, min(s.row0, p.total_rows));
+  s.Wb = max(0, min(min(s.Wb, p.W), p.total_rows - s.row0));
+  const int cap = p.max_pages * kPage;
+  s.L = max(0, min(p.kv_len[b], cap));
+  s.n_keys = s.sid >= 0 && s.sid < p.table_rows && s.Wb > 0 ? min(s.L + s.Wb, cap) : 0;
+  s.pages = (s.n_keys + kPage - 1) / kPage;
+  return s;
+}
+
+// How the groups are cut into pieces, one CTA each.  All pieces of a call have about
+// `target` pages; a group of that many or fewer is one piece.
+struct Kv4Plan {
+  int target, total;  // total: pieces of all groups
+};
+SPEC_DEVICE_INLINE int kv4_pieces(int pages, int target) { return (pages + target - 1) / target; }
+
+// Sequence `lane` of the first 32 (every warp starts with it: most batches need no other).
+SPEC_DEVICE_INLINE Kv4Seq kv4_first_seqs(const Kv4AttnParams& p) {
+  const int lane = threadIdx.x & 31;
+  Kv4Seq s{};
+  if (lane < p.B) s = kv4_seq(p, lane);
+  return s;
+}
+SPEC_DEVICE_INLINE Kv4Seq kv4_seq_at(const Kv4AttnParams& p, const Kv4Seq& mine, int b) {
+  if (b >= 32) return kv4_seq(p, b);
+  Kv4Seq s;
+  s.sid = __shfl_sync(0xffffffffu, mine.sid, b);
+  s.row0 = __shfl_sync(0xffffffffu, mine.row0, b);
+  s.Wb = __shfl_sync(0xffffffffu, mine.Wb, b);
+  s.L = __shfl_sync(0xffffffffu, mine.L, b);
+  s.n_keys = __shfl_sync(0xffffffffu, mine.n_keys, b);
+  s.pages = __shfl_sync(0xffffffffu, mine.pages, b);
+  return s;
+}
+// With fewer groups than slots (CTAs the GPU holds at once) the pieces fit the slots: every
+// group has at most pages / target + 1.  With more, a group is cut only if it is longer
+// than a slot's share of all pages.
+SPEC_DEVICE_INLINE Kv4Plan kv4_plan(const Kv4AttnParams& p, const Kv4Seq& mine) {
+  const int lane = threadIdx.x & 31;
+  int n = mine.pages;
+  for (int b = lane + 32; b < p.B; b += 32) n += kv4_seq(p, b).pages;
+  n = warp_sum(n) * p.Hkv;
+  const int groups = p.B * p.Hkv;
+  const int share = groups < p.slots ? p.slots - groups : p.slots;
+  Kv4Plan r;
+  r.target = max(1, (n + share - 1) / share);
+  int k = kv4_pieces(mine.pages, r.target);
+  for (int b = lane + 32; b < p.B; b += 32) k += kv4_pieces(kv4_seq(p, b).pages, r.target);
+  r.total = warp_sum(k) * p.Hkv;
+  return r;
+}
+// The sequence that holds piece x (below the total; per sequence all pieces of head 0, then
+// head 1, ...), and the pieces before it: of all sequences, and of those cut in two or more.
+SPEC_DEVICE_INLINE int kv4_find_piece(const Kv4AttnParams& p, const Kv4Seq& mine, int target, int x, int& before,
+                                      int& before_cut) {
+  const int lane = threadIdx.x & 31;
+  int base = 0, base_cut = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int pages = b0 == 0 ? mine.pages : b0 + lane < p.B ? kv4_seq(p, b0 + lane).pages : 0;
+    const int n = kv4_pieces(pages, target) * p.Hkv, nc = n > p.Hkv ? n : 0;
+    int incl = n, incl_cut = nc;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, incl_cut, o);
+      if (lane >= o) incl += u, incl_cut += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, base + incl > x);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      before = base + __shfl_sync(0xffffffffu, incl - n, l);
+      before_cut = base_cut + __shfl_sync(0xffffffffu, incl_cut - nc, l);
+      return b0 + l;
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+    base_cut += __shfl_sync(0xffffffffu, incl_cut, 31);
   }
+  before = base, before_cut = base_cut;
+  return p.B;
+}
+
+// Partial i of the workspace (pieces of cut groups, in order): rows x hd of O, then the rows'
+// maxima and sums.
+SPEC_DEVICE_INLINE float* kv4_partial(float* ws, int i, int rows, int hd) {
+  return ws + (long long)i * rows * (hd + 2);
+}
+
+// Four output values of a row: o / l in the caller's type; a row that sees no token is zeros.
+SPEC_DEVICE_INLINE void store_row4(const Kv4AttnParams& p, int row, int head, int hd, int d4, float4 o, float l) {
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint2 w;
+  if (p.bf16) {
+    w.x = kv4_pack2<true>(o.x * inv, o.y * inv);
+    w.y = kv4_pack2<true>(o.z * inv, o.w * inv);
+  } else {
+    w = pack_act4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((long long)row * p.Hq + head) * hd + d4 * 4) = w;
+}
+
+// V words of 16-token step t for a lane whose chunk starts at v: NPIECE pieces of tokens
+// {2c, 2c+1} (x0) and {2c+8, 2c+9} (x1).
+template <int HD, int NPIECE>
+SPEC_DEVICE_INLINE void kv4_v_words(const uint8_t* v, int t, uint32_t (&x0)[NPIECE], uint32_t (&x1)[NPIECE]) {
+  const uint8_t* a = v + t * (HD == 128 ? 1024 : 512);
+  const uint8_t* d = a + (HD == 128 ? 512 : 8);
+  if constexpr (HD == 64 && NPIECE == 2) {
+    const uint4 w = *reinterpret_cast<const uint4*>(a);
+    x0[0] = w.x, x0[1] = w.y, x1[0] = w.z, x1[1] = w.w;
+  } else if constexpr (NPIECE == 4) {
+    const uint4 w = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(d);
+    x0[0] = w.x, x0[1] = w.y, x0[2] = w.z, x0[3] = w.w;
+    x1[0] = y.x, x1[1] = y.y, x1[2] = y.z, x1[3] = y.w;
+  } else if constexpr (NPIECE == 2) {
+    const uint2 w = *reinterpret_cast<const uint2*>(a), y = *reinterpret_cast<const uint2*>(d);
+    x0[0] = w.x, x0[1] = w.y;
+    x1[0] = y.x, x1[1] = y.y;
+  } else {
+    x0[0] = *reinterpret_cast<const uint32_t*>(a);
+    x1[0] = *reinterpret_cast<const uint32_t*>(d);
+  }
+}
+
+// HD: head_dim; NT: tiles of 8 query rows; TW: warps of a team.
+template <int HD, int NT, int TW>
+struct Cfg {
+  static constexpr int kPieces = HD / 32 >= TW ? HD / 32 / TW : 1;  // V words of a token pair per warp
+  static constexpr int kTeams = kWarps / TW;
+  static constexpr int kBlock = kPage * HD + 2 * kPage * 4;    // bytes of a page of one kv head: a stage
+  // CTAs per SM by the registers of a warp
+  static constexpr int kRegs = NT * (HD / 4 / TW + 8 + 16 / TW) + (TW == 1 ? 90 : 70);
+  static constexpr int kCtas = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : 2;
+  static constexpr int kQ = NT * (HD / 32) * 512;              // query fragments
+  static constexpr int kP = TW == 1 ? 0 : 2 * NT * 1024;       // weights of two pages
+  static constexpr int kFixed = kQ + kP;
+  static constexpr int kStatic = NT * 8 * 4 * (5 + 2 * kWarps + kTeams) + 512;  // static shared memory, at most
+  // Ring depth with `ctas` CTAs on an SM: 228 KB, 1 KB of system use per CTA.  A multiple
+  // of the teams, so that the pages of one stage are one team's, in order: a team that
+  // waited for a stage's next page while another team's was still in flight would take
+  // the phase before for its own.
+  static constexpr int stages(int ctas) {
+    const int n = (233472 / ctas - 1024 - kStatic - kFixed) / kBlock;
+    return (n < kMaxStages ? n : kMaxStages) / kTeams * kTeams;
+  }
+  static_assert(kCtas <= (NT <= 3 ? 4 : 3), "workspace");
+  // a team refills a stage two of its pages late and computes scores one page ahead
+  static_assert(TW == 1 || TW == kWarps, "a team is one warp or the CTA");
+  static_assert(stages(kCtas) >= (TW == 1 ? 2 : 4) * kTeams, "ring");
+  static_assert(kTeams * NT * 8 * HD * 4 <= stages(kCtas) * kBlock, "the teams' partials reuse the ring");
 };
 
 // Query row r of the CTA is window row r / grp, head r % grp of the group.
-// HD: head_dim; NT: tiles of 8 query rows per warp; KG: warps that share a page's keys.
-template <int HD, int NT, int KG>
-__global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const __grid_constant__ Kv4AttnParams p) {
-  using C = Cfg<HD>;
-  constexpr int MT = 4 / KG;        // 16-token steps of a page per warp
-  constexpr int WORDS = HD / 32;    // 32-bit words of K codes per lane and token
-  constexpr int DM = HD / 16;       // 16-row tiles of the PV product
+// CL: a group's pieces are the CTAs of one thread-block cluster (gridDim.x / (B Hkv) of them,
+// possibly one), merged through distributed shared memory.
+template <int HD, int NT, int TW, bool CL>
+__global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
+    kv4_attention_kernel(const __grid_constant__ Kv4AttnParams p) {
+  using C = Cfg<HD, NT, TW>;
+  constexpr int WORDS = HD / 32;     // 32-bit words of K codes per lane and token
+  constexpr int MT = 4 / TW;         // 16-token steps of a page per warp (S and softmax)
+  constexpr int PW = WORDS * 2 / TW; // 16-row tiles of the PV product per warp
+  constexpr int TEAMS = C::kTeams;
+  constexpr int ROWS = NT * 8;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
-  __shared__ float s_sumq[64], s_f[64];
+  uint8_t* const ring = smem;
+  const int S = p.stages;            // ring depth
+  uint8_t* const qfrag = smem + S * C::kBlock;
+  __shared__ uint64_t full[kMaxStages];
+  __shared__ float4 s_row[ROWS / 2];          // rows 2i, 2i + 1: sums of q, factors to exp2 units
+  __shared__ float2 s_max[TEAMS][ROWS / 2];   // running maxima
+  __shared__ float s_red[kWarps][ROWS], s_red2[kWarps][ROWS];
+  __shared__ float s_m[CL ? ROWS : 1], s_l[CL ? ROWS : 1];
+  __shared__ uint32_t s_smax[kWarps];
   __shared__ uint32_t s_anc[16];
-  __shared__ float s_m[64], s_l[64];
-  __shared__ float part_m[kWarps * 32], part_l[kWarps * 32];
   __shared__ int s_fail;
-  cg::cluster_group cluster = cg::this_cluster();
 
-  const int rank = blockIdx.x, CS = gridDim.x, kvh = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int team = warp / TW, tw = warp % TW;
   const int g = lane >> 2, c = lane & 3;
-  const int NG = p.row_tiles / NT;          // row groups (row_tiles is a multiple of NT)
-  const int TW = KG * NG;                   // warps of a team
-  const int teams = kWarps / TW;
-  const int team = warp / TW, kg = warp % KG, ng = (warp % TW) / KG;
-  const int S = p.stages;                   // ring depth of a team
   const int grp = p.Hq / p.Hkv;
+  uint8_t* const pfrag = qfrag + C::kQ;
 
-  pdl_launch_dependents();
+  // the merge kernel reads the call's tables before its own wait, so it may only start
+  // once they are complete
   if (!p.early) pdl_wait();
-  const int b = p.seq_order ? p.seq_order[blockIdx.z] : blockIdx.z;
-  const int sid = p.seq_ids ? p.seq_ids[b] : b;
-  int row0 = p.row_begin ? p.row_begin[b] : b * p.W;
-  int Wb = p.row_count ? p.row_count[b] : p.row_begin ? p.row_begin[b + 1] - row0 : p.W;
-  row0 = max(0, min(row0, p.total_rows));
-  Wb = max(0, min(min(Wb, p.W), p.total_rows - row0));
-  const bool sid_ok = sid >= 0 && sid < p.table_rows;
-  const int cap = p.max_pages * kPage;
-  const int L = max(0, min(p.kv_len[b], cap));
-  const int n_keys = sid_ok && Wb > 0 ? min(L + Wb, cap) : 0;
-  const int rows = Wb * grp;
-  const int n_pages = (n_keys + kPage - 1) / kPage;
-  const int pps = (n_pages + CS - 1) / CS;
-  const int pg0 = min(rank * pps, n_pages);
-  const int npg = min(pg0 + pps, n_pages) - pg0;
-  const int n_it = npg > team ? (npg - team + teams - 1) / teams : 0;  // pages of this team
-
-  uint8_t* const ring = smem + team * S * C::kBlock;
-  uint64_t* const fullb = full + team * S;
-  uint64_t* const emptyb = empty + team * S;
-  uint8_t* const qfrag = smem + kWarps / TW * S * C::kBlock;
+  pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int s = 0; s < teams * S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], TW);
-    }
+    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
     s_fail = 0;
     fence_barrier_init();
   }
   if (threadIdx.x < 16) s_anc[threadIdx.x] = p.anc[threadIdx.x];
+
+  if (threadIdx.x < ROWS / 2)
+#pragma unroll
+    for (int i = 0; i < TEAMS; ++i) s_max[i][threadIdx.x] = make_float2(kNoMax, kNoMax);
+
+  int kvh, piece, pieces, slot = 0;
+  Kv4Seq seq;
+  if constexpr (CL) {
+    pieces = p.cluster;
+    piece = blockIdx.x % pieces;
+    const int group = blockIdx.x / pieces;
+    kvh = group % p.Hkv;
+    seq = kv4_seq(p, group / p.Hkv);
+  } else {
+    const Kv4Seq mine = kv4_first_seqs(p);
+    const Kv4Plan plan = kv4_plan(p, mine);
+    if ((int)blockIdx.x >= plan.total) return;
+    int before, before_cut;
+    const int b = kv4_find_piece(p, mine, plan.target, blockIdx.x, before, before_cut);
+    seq = kv4_seq_at(p, mine, b);
+    pieces = kv4_pieces(seq.pages, plan.target);
+    kvh = (blockIdx.x - before) / pieces;
+    piece = (blockIdx.x - before) % pieces;
+    slot = before_cut + (blockIdx.x - before);
+  }
+  const int pg0 = (int)((long long)seq.pages * piece / pieces);
+  const int npg = (int)((long long)seq.pages * (piece + 1) / pieces) - pg0;
+  const int L = seq.L, n_keys = seq.n_keys, Wb = seq.Wb, row0 = seq.row0, rows = seq.Wb * grp;
+  const int key_base = pg0 * kPage;
+  bool failed = false;
   __syncthreads();
 
-  // Page numbers of iterations [i0, i0 + 32) and the 32 after them, one per lane.
-  const int32_t* table = p.page_table + (long long)(sid_ok ? sid : 0) * p.max_pages;
-  auto page_at = [&](int i) {
-    const int pg = i < n_it ? table[pg0 + i * teams + team] : -1;
+  // Page numbers of the piece's pages [base, base + 32) and the 32 after them, one per
+  // lane, and which of the first 32 are there.
+  const int32_t* table = p.page_table + (long long)seq.sid * p.max_pages + pg0;
+  auto page_at = [&](int j) {
+    const int pg = j < npg ? table[j] : -1;
     return pg < p.num_pages ? pg : -1;
   };
   int pid0 = page_at(lane), pid1 = page_at(32 + lane);
+  uint32_t there = __ballot_sync(0xffffffffu, pid0 >= 0);
   int base = 0;
-  auto pid = [&](int i) {  // base <= i < base + 64, the same in all lanes
-    const int a = __shfl_sync(0xffffffffu, pid0, i & 31), d = __shfl_sync(0xffffffffu, pid1, i & 31);
-    return i - base < 32 ? a : d;
-  };
-  // Start the copy of iteration i's block (an absent page completes its phase empty).
-  auto issue = [&](int i, int s) {
-    const int pg = pid(i);
+  // Start the copy of page j into stage s (an absent page completes its phase empty); j is
+  // in [base, base + 64), a whole warp calls it.
+  auto issue = [&](int j, int s) {
+    const int pg = __shfl_sync(0xffffffffu, j - base < 32 ? pid0 : pid1, j & 31);
     if (lane == 0) {
       if (pg >= 0) {
-        mbar_arrive_expect_tx(&fullb[s], C::kBlock);
-        bulk_load(ring + s * C::kBlock, p.pool + ((long long)pg * p.Hkv + kvh) * C::kBlock, C::kBlock, &fullb[s]);
+        mbar_arrive_expect_tx(&full[s], C::kBlock);
+        bulk_load(ring + s * C::kBlock, p.pool + ((long long)pg * p.Hkv + kvh) * C::kBlock, C::kBlock, &full[s]);
       } else {
-        mbar_arrive(&fullb[s]);
+        mbar_arrive(&full[s]);
       }
     }
   };
-  const bool leader = warp % TW == 0;
-  // Before pdl_wait only pages without window slots may be read.
   int issued = 0;
-  if (leader) {
-    for (; issued < min(S, n_it); ++issued) {
-      if (p.early && (pg0 + issued * teams + team + 1) * kPage > L) break;
+  if (warp == 0) {
+    // before pdl_wait only pages without window slots may be read
+    for (; issued < min(S, npg); ++issued) {
+      if (p.early && key_base + (issued + 1) * kPage > L) break;
       issue(issued, issued);
     }
   }
   if (p.early) pdl_wait();
-  if (leader)
-    for (; issued < min(S, n_it); ++issued) issue(issued, issued);
+  if (warp == 0)
+    for (; issued < min(S, npg); ++issued) issue(issued, issued);
 
   // Queries: each row is scaled by a power of two (largest element in [2^14, 2^15)),
   // so the factor 1/16 of the odd columns costs no precision; the sum of the scaled
-  // row and the factor back to exp2 units are kept per row.  One warp per row.
+  // row and the factor back to exp2 units are kept per row.  One warp per row, four
+  // rows at a time.
   {
     constexpr int PER = HD / 32;  // elements of a lane
-    for (int r = warp; r < p.row_tiles * 8; r += kWarps) {
-      float x[PER];
+    constexpr int RB = NT == 1 ? 2 : 4;
+    for (int r0 = warp; r0 < ROWS; r0 += RB * kWarps) {
+      uint32_t raw[RB][PER / 2];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) x[i] = 0.f;
-      if (r < rows) {
-        const uint16_t* qr = static_cast<const uint16_t*>(p.q) + (row0 + r / grp) * p.q_row_stride +
-                             (long long)(kvh * grp + r % grp) * HD + lane * PER;
-        const uint32_t* q2 = reinterpret_cast<const uint32_t*>(qr);
+      for (int k = 0; k < RB; ++k) {
+        const int r = r0 + k * kWarps;
 #pragma unroll
-        for (int i = 0; i < PER / 2; ++i) {
-          const float2 f = p.bf16 ? kv4_unpack2<true>(q2[i]) : kv4_unpack2<false>(q2[i]);
-          x[2 * i] = kv4_sat(f.x);
-          x[2 * i + 1] = kv4_sat(f.y);
+        for (int i = 0; i < PER / 2; ++i) raw[k][i] = 0;
+        if (r < rows) {
+          const uint16_t* qr = static_cast<const uint16_t*>(p.q) + (row0 + r / grp) * p.q_row_stride +
+                               (long long)(kvh * grp + r % grp) * HD + lane * PER;
+          if constexpr (PER == 4) {
+            const uint2 w = *reinterpret_cast<const uint2*>(qr);
+            raw[k][0] = w.x, raw[k][1] = w.y;
+          } else {
+            raw[k][0] = *reinterpret_cast<const uint32_t*>(qr);
+          }
         }
       }
-      float mx = 0.f;
+      float x[RB][PER], mx[RB], sum[RB];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) mx = fmaxf(mx, fabsf(x[i]));
-      mx = warp_max(mx);
-      // 2^sh with 2^14 <= mx 2^sh < 2^15; rows below 2^-40 count as zeros
-      const int sh = mx > 9.1e-13f ? 14 - (int)((__float_as_uint(mx) >> 23) - 127u) : 0;
-      const float up = __uint_as_float((uint32_t)(127 + sh) << 23);
-      float sum = 0.f;
+      for (int k = 0; k < RB; ++k) {
+        mx[k] = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        x[i] *= p.scale < 0.f ? -up : up;
-        sum += x[i];
+        for (int i = 0; i < PER / 2; ++i) {
+          const float2 f = p.bf16 ? kv4_unpack2<true>(raw[k][i]) : kv4_unpack2<false>(raw[k][i]);
+          x[k][2 * i] = kv4_sat(f.x);
+          x[k][2 * i + 1] = kv4_sat(f.y);
+          mx[k] = fmaxf(mx[k], fmaxf(fabsf(x[k][2 * i]), fabsf(x[k][2 * i + 1])));
+        }
       }
-      sum = warp_sum(sum);
-      if (lane == 0) {
-        s_sumq[r] = sum * 5.9604644775390625e-8f;  // in the units of the code products (2^-24)
-        s_f[r] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * 16777216.f * __uint_as_float((uint32_t)(127 - sh) << 23),
-                       1e-30f);
-      }
-      // fragment of lane (r % 8, cc), word w: halves (d0, d4) (d1, d5)/16 (d2, d6) (d3, d7)/16
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int d = lane * PER + i;
-        const int cc = d / (HD / 4), w = (d % (HD / 4)) / 8, n = d % 8;
-        __half* dst = reinterpret_cast<__half*>(qfrag + (r >> 3) * C::kQTile + (w * 32 + (r & 7) * 4 + cc) * 16);
-        dst[(n & 3) * 2 + (n >> 2)] = __float2half_rn((n & 1) ? x[i] * 0.0625f : x[i]);
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < RB; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+      int sh[RB];
+#pragma unroll
+      for (int k = 0; k < RB; ++k) {
+        // 2^sh with 2^14 <= mx 2^sh < 2^15; rows below 2^-40 count as zeros
+        sh[k] = mx[k] > 9.1e-13f ? 14 - (int)((__float_as_uint(mx[k]) >> 23) - 127u) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + sh[k]) << 23);
+        sum[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          x[k][i] *= p.scale < 0.f ? -up : up;
+          sum[k] += x[k][i];
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < RB; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+#pragma unroll
+      for (int k = 0; k < RB; ++k) {
+        const int r = r0 + k * kWarps;
+        if (r >= ROWS) break;
+        if (lane == 0) {
+          float* row = reinterpret_cast<float*>(&s_row[r >> 1]) + (r & 1);
+          row[0] = sum[k] * 5.9604644775390625e-8f;  // in the units of the code products (2^-24)
+          row[2] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * 16777216.f *
+                             __uint_as_float((uint32_t)(127 - sh[k]) << 23),
+                         1e-30f);
+        }
+        // fragment of lane (r % 8, cc), word w: halves (d0, d4) (d1, d5)/16 (d2, d6) (d3, d7)/16
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const int d = lane * PER + i;
+          const int cc = d / (HD / 4), w = (d % (HD / 4)) / 8, n = d % 8;
+          __half* dst =
+              reinterpret_cast<__half*>(qfrag + (((r >> 3) * WORDS + w) * 32 + (r & 7) * 4 + cc) * 16);
+          dst[(n & 3) * 2 + (n >> 2)] = __float2half_rn((n & 1) ? x[k][i] * 0.0625f : x[k][i]);
+        }
       }
     }
   }
   __syncthreads();
 
-  float acc[NT][DM][4], accr[NT][4];
-  float mrow[NT][2], lrow[NT][2], zrow[NT][2], sq[NT][2], fr[NT][2];
+  float acc[NT][PW][4], accr[NT][4];        // codes^T . weights, and the weights' sums
+  float lrow[NT][2], zrow[NT][2];           // rows 2c, 2c + 1
+  float sc[NT][MT][4];                      // scores / factor: tokens g, g + 8 of a step; rows 2c, 2c + 1
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-    for (int t = 0; t < DM; ++t) acc[nt][t][0] = acc[nt][t][1] = acc[nt][t][2] = acc[nt][t][3] = 0.f;
+    for (int t = 0; t < PW; ++t) acc[nt][t][0] = acc[nt][t][1] = acc[nt][t][2] = acc[nt][t][3] = 0.f;
     accr[nt][0] = accr[nt][1] = accr[nt][2] = accr[nt][3] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = (ng * NT + nt) * 8 + 2 * c + e;
-      mrow[nt][e] = -INFINITY;
-      lrow[nt][e] = zrow[nt][e] = 0.f;
-      sq[nt][e] = s_sumq[r];
-      fr[nt][e] = s_f[r];
-    }
+    lrow[nt][0] = lrow[nt][1] = zrow[nt][0] = zrow[nt][1] = 0.f;
   }
-  uint32_t smax = 0;      // largest V scale so far (its word), and 2^-exponent of it
-  float inv_e = 1.f;
+  uint32_t vw[2 * MT];                      // V parameter words of the lane's tokens
+  uint32_t s_lim = 1;                       // V scales (fp16 bits) below this keep 2^-e
+  float inv_e = 1.f;                        // 2^-e: the weights are P s 2^-e
 
-  int s = 0;
-  uint32_t par = 0;
-  for (int i = 0; i < n_it; ++i) {
-    if (i - base == 32) {
-      base = i;
+  const int kk = tw * MT * 16 + g;          // this lane's first token in a page
+  // Scores of page j (in stage s, phase parity par) into sc; returns whether a score or a
+  // scale passes its limit.
+  auto scores = [&](int j, int s, uint32_t par) -> bool {
+    if (j - base >= 32) {
+      base += 32;
       pid0 = pid1;
+      there = __ballot_sync(0xffffffffu, pid0 >= 0);
       pid1 = page_at(base + 32 + lane);
     }
-    const int pg = pid(i);
-    if (!mbar_wait(&fullb[s], par, p.status)) {
+    // a wait that runs out is the warp's last: it goes on without data, so that the
+    // CTA's barriers stay whole, and its rows come out as NaN
+    if (!failed && !mbar_wait(&full[s], par, p.status)) {
+      failed = true;
       s_fail = 1;
-      break;
     }
-    if (pg >= 0) {
-      const uint8_t* st = ring + s * C::kBlock;
-      const int key0 = (pg0 + i * teams + team) * kPage;
-      const bool masked = key0 + kPage > L;
-
-      // parameter words of this lane's tokens: 16-token step t, tokens g and g + 8
-      uint32_t kw[2 * MT], vw[2 * MT];
-      const uint32_t* kpar = reinterpret_cast<const uint32_t*>(st + kPage * HD);
+    const uint8_t* st = ring + s * C::kBlock;
+    const uint32_t* kpar = reinterpret_cast<const uint32_t*>(st + kPage * HD) + kk;
+    uint32_t kw[2 * MT];
 #pragma unroll
-      for (int t = 0; t < 2 * MT; ++t) {
-        const int k = (kg * MT + (t >> 1)) * 16 + (t & 1) * 8 + g;
-        kw[t] = kpar[k];
-        vw[t] = kpar[kPage + k];
-        if (masked && key0 + k >= n_keys) kw[t] = vw[t] = 0;  // never written: may hold anything
-      }
-      // K codes
-      uint32_t kc[2 * MT][WORDS];
+    for (int t = 0; t < 2 * MT; ++t) {
+      kw[t] = kpar[8 * t];
+      vw[t] = kpar[kPage + 8 * t];
+    }
+    // two steps at a time: enough independent products to cover their latency
+    constexpr int HB = MT < 2 ? 1 : 2;
 #pragma unroll
-      for (int t = 0; t < 2 * MT; ++t) {
-        const int k = (kg * MT + (t >> 1)) * 16 + (t & 1) * 8 + g;
-        const uint8_t* a = st + k * (HD / 2) + c * (HD / 8);
+    for (int h = 0; h < MT; h += HB) {
+      uint32_t kc[2 * HB][WORDS];
+#pragma unroll
+      for (int t = 0; t < 2 * HB; ++t) {
+        const uint8_t* a = st + (kk + 16 * h + 8 * t) * (HD / 2) + c * (HD / 8);
         if constexpr (WORDS == 4) {
           const uint4 v = *reinterpret_cast<const uint4*>(a);
           kc[t][0] = v.x, kc[t][1] = v.y, kc[t][2] = v.z, kc[t][3] = v.w;
@@ -294,347 +532,579 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_attention_kernel(const __grid
           kc[t][0] = v.x, kc[t][1] = v.y;
         }
       }
-      // S = codes . q, then s (.) + m sum(q)
-      float sc[NT][MT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) sc[nt][t][0] = sc[nt][t][1] = sc[nt][t][2] = sc[nt][t][3] = 0.f;
 #pragma unroll
       for (int w = 0; w < WORDS; ++w) {
-        uint4 qf[NT];
+        uint4 q[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-          qf[nt] = *reinterpret_cast<const uint4*>(qfrag + (ng * NT + nt) * C::kQTile + (w * 32 + lane) * 16);
+          q[nt] = *reinterpret_cast<const uint4*>(qfrag + ((nt * WORDS + w) * 32 + lane) * 16);
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
+        for (int t = 0; t < HB; ++t) {
           const uint32_t x0 = kc[2 * t][w], x1 = kc[2 * t + 1][w];
-          const uint32_t y0 = x0 >> 8, y1 = x1 >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(sc[nt][t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, qf[nt].x,
-                          qf[nt].y);
-            mma_f16_16816(sc[nt][t], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, qf[nt].z,
-                          qf[nt].w);
-          }
-        }
-      }
-      // largest V scale: 2^-E keeps P s below 2 and, for the larger scales, normal
-      float rescale_e = 1.f;
-      {
-        uint32_t mx = 0;
-#pragma unroll
-        for (int t = 0; t < 2 * MT; ++t) mx = max(mx, vw[t]);
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        if ((mx >> 16) > smax) {
-          smax = mx >> 16;
-          const uint32_t e = __float_as_uint(__half2float(__ushort_as_half((unsigned short)smax))) >> 23;
-          const float now = __uint_as_float((254u - e) << 23);
-          rescale_e = now / inv_e;
-          inv_e = now;
-        }
-      }
-      float vs[2 * MT], vz[2 * MT];
-#pragma unroll
-      for (int t = 0; t < 2 * MT; ++t) {
-        const float2 kmv = __half22float2(*reinterpret_cast<const __half2*>(&kw[t]));
-        const float2 vmv = __half22float2(*reinterpret_cast<const __half2*>(&vw[t]));
-        vs[t] = vmv.y * inv_e;
-        vz[t] = fmaf(7.5f, vmv.y, vmv.x);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = sc[nt][t >> 1][(t & 1) * 2 + e];
-            x = fmaf(kmv.y, x, kmv.x * sq[nt][e]);
-          }
-      }
-      if (masked) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = (ng * NT + nt) * 8 + 2 * c + e;
-            const uint32_t anc = r < rows ? s_anc[r / grp] & ((1u << Wb) - 1u) : 0u;
-#pragma unroll
-            for (int t = 0; t < 2 * MT; ++t) {
-              const int w = key0 + (kg * MT + (t >> 1)) * 16 + (t & 1) * 8 + g - L;
-              const bool vis = w < 0 || (w < 16 && ((anc >> w) & 1u) && w + L < n_keys);
-              if (!vis) sc[nt][t >> 1][(t & 1) * 2 + e] = -INFINITY;
-            }
-          }
-      }
-      // running maximum and sum; weights into fp16 B fragments
-      uint32_t pb[NT][2 * MT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = sc[nt][0][e];
-#pragma unroll
-          for (int t = 1; t < 2 * MT; ++t) mx = fmaxf(mx, sc[nt][t >> 1][(t & 1) * 2 + e]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float now = fmaxf(mrow[nt][e], mx * fr[nt][e]);
-          alpha[e] = mrow[nt][e] == now ? 1.f : ex2(mrow[nt][e] - now);
-          mrow[nt][e] = now;
-        }
-        const float off0 = mrow[nt][0] == -INFINITY ? 0.f : mrow[nt][0];
-        const float off1 = mrow[nt][1] == -INFINITY ? 0.f : mrow[nt][1];
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f) || rescale_e != 1.f) {
-          const float a0 = alpha[0] * rescale_e, a1 = alpha[1] * rescale_e;
-#pragma unroll
-          for (int t = 0; t < DM; ++t) {
-            acc[nt][t][0] *= a0;
-            acc[nt][t][1] *= a1;
-            acc[nt][t][2] *= a0;
-            acc[nt][t][3] *= a1;
-          }
-          accr[nt][0] *= a0;
-          accr[nt][1] *= a1;
-          lrow[nt][0] *= alpha[0];
-          lrow[nt][1] *= alpha[1];
-          zrow[nt][0] *= alpha[0];
-          zrow[nt][1] *= alpha[1];
-        }
-#pragma unroll
-        for (int t = 0; t < 2 * MT; ++t) {
-          const float p0 = ex2(fmaf(sc[nt][t >> 1][(t & 1) * 2], fr[nt][0], -off0));
-          const float p1 = ex2(fmaf(sc[nt][t >> 1][(t & 1) * 2 + 1], fr[nt][1], -off1));
-          lrow[nt][0] += p0;
-          lrow[nt][1] += p1;
-          zrow[nt][0] = fmaf(p0, vz[t], zrow[nt][0]);
-          zrow[nt][1] = fmaf(p1, vz[t], zrow[nt][1]);
-          pb[nt][t] = movmatrix_trans(pack_f16x2(p0 * vs[t], p1 * vs[t]));
-        }
-      }
-      // O^T += codes^T . weights
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int step = kg * MT + t;
-        const uint8_t* vbase = st + kPage * HD / 2 + ((g ^ (2 * c)) << 4);
-        uint32_t lo[HD / 32], hi[HD / 32];  // pieces of tokens {2c, 2c+1} and {2c+8, 2c+9}
-        if constexpr (HD == 128) {
-          const uint4 a = *reinterpret_cast<const uint4*>(vbase + (step * 8 + c) * 128);
-          const uint4 d = *reinterpret_cast<const uint4*>(vbase + (step * 8 + 4 + c) * 128);
-          lo[0] = a.x, lo[1] = a.y, lo[2] = a.z, lo[3] = a.w;
-          hi[0] = d.x, hi[1] = d.y, hi[2] = d.z, hi[3] = d.w;
-        } else {
-          const uint4 a = *reinterpret_cast<const uint4*>(vbase + (step * 4 + c) * 128);
-          lo[0] = a.x, lo[1] = a.y;
-          hi[0] = a.z, hi[1] = a.w;
-        }
-#pragma unroll
-        for (int w = 0; w < HD / 32; ++w) {
-          const uint32_t x0 = lo[w], x1 = hi[w], y0 = x0 >> 8, y1 = x1 >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(acc[nt][2 * w], x0 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x000f000fu, x1 & 0x00f000f0u,
-                          pb[nt][2 * t], pb[nt][2 * t + 1]);
-            mma_f16_16816(acc[nt][2 * w + 1], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u,
-                          pb[nt][2 * t], pb[nt][2 * t + 1]);
+            if (w == 0)
+              mma0(sc[nt][h + t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, q[nt].x,
+                   q[nt].y);
+            else
+              mma(sc[nt][h + t], x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u, q[nt].x,
+                  q[nt].y);
           }
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_f16_16816(accr[nt], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[nt][2 * t], pb[nt][2 * t + 1]);
+        for (int t = 0; t < HB; ++t) {
+          const uint32_t y0 = kc[2 * t][w] >> 8, y1 = kc[2 * t + 1][w] >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma(sc[nt][h + t], y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u, q[nt].z,
+                q[nt].w);
+        }
       }
     }
-    // The stage is refilled through the async proxy: order this warp's reads before it.
-    fence_proxy_async();
-    __syncwarp();
-    if (TW == 1) {
-      if (i + S < n_it) issue(i + S, s);
-    } else {
-      if (lane == 0) mbar_arrive(&emptyb[s]);
-      // the team's first warp refills the stage of the page before, which the others
-      // have usually left by now
-      if (leader && i > 0 && i - 1 + S < n_it) {
-        const int ps = s == 0 ? S - 1 : s - 1;
-        const uint32_t pp = s == 0 ? par ^ 1u : par;
-        if (!mbar_wait(&emptyb[ps], pp, p.status)) {
-          s_fail = 1;
-          break;
-        }
-        issue(i - 1 + S, ps);
-      }
+    const int key0 = key_base + j * kPage;
+    const bool here = (there >> (j & 31)) & 1u;
+    const bool masked = key0 + kPage > L || !here;
+    if (masked) {
+      const int end = here ? n_keys : 0;
+#pragma unroll
+      for (int t = 0; t < 2 * MT; ++t)
+        if (key0 + kk + 8 * t >= end) kw[t] = vw[t] = 0;  // never written: may hold anything
     }
-    if (++s == S) {
-      s = 0;
-      par ^= 1u;
+    float km[2 * MT], ks[2 * MT];
+    uint32_t smax = 0;
+#pragma unroll
+    for (int t = 0; t < 2 * MT; ++t) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&kw[t]));
+      km[t] = f.x;
+      ks[t] = f.y;
+      smax = max(smax, vw[t]);
     }
-  }
-  __syncthreads();
-  if (s_fail && threadIdx.x < teams * S) {
-    // a wait ran out: give copies still in flight the same time to land before the
-    // CTA's shared memory is given up
-    (void)mbar_wait(&full[threadIdx.x], 0, nullptr);
-    (void)mbar_wait(&full[threadIdx.x], 1, nullptr);
-  }
-
-  // Partials of every warp (the ring is drained): out-of-loop order is
-  // [key partial][row][HD], with NP = kWarps / NG partials per row.
-  const int NP = kWarps / NG;
-  const int n_rows8 = p.row_tiles * 8;
-  float* part_o = reinterpret_cast<float*>(smem);
-  {
-    const int np = team * KG + kg;
-    const float e_up = 1.f / inv_e;
+    bool over = (smax >> 16) >= s_lim;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      const float4 row = s_row[nt * 4 + c];
+      const float2 top = s_max[team][nt * 4 + c];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = lrow[nt][e], z = zrow[nt][e];
+      for (int t = 0; t < 2 * MT; ++t) {
+        float* x = &sc[nt][t >> 1][(t & 1) * 2];
+        x[0] = fmaf(ks[t], x[0], km[t] * row.x);
+        x[1] = fmaf(ks[t], x[1], km[t] * row.y);
+      }
+      if (masked) {
+        // window slots are seen by their descendants only; slots past the window by nobody
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          l += __shfl_xor_sync(0xffffffffu, l, o);
-          z += __shfl_xor_sync(0xffffffffu, z, o);
-        }
-        const int r = (ng * NT + nt) * 8 + 2 * c + e;
-        const float bias = z - 7.5f * e_up * accr[nt][e];
-        float* o = part_o + ((long long)np * n_rows8 + r) * HD + g * (HD / 8);
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + 2 * c + e;
+          const uint32_t anc = r < rows && here ? s_anc[r / grp] & ((1u << Wb) - 1u) : 0u;
 #pragma unroll
-        for (int t = 0; t < DM; t += 2)
-          *reinterpret_cast<float4*>(o + 2 * t) =
-              make_float4(fmaf(acc[nt][t][e], e_up * 16777216.f, bias), fmaf(acc[nt][t][2 + e], e_up * 1048576.f, bias),
-                          fmaf(acc[nt][t + 1][e], e_up * 16777216.f, bias),
-                          fmaf(acc[nt][t + 1][2 + e], e_up * 1048576.f, bias));
-        if (g == 0) {
-          part_m[np * n_rows8 + r] = mrow[nt][e];
-          part_l[np * n_rows8 + r] = l;
+          for (int t = 0; t < 2 * MT; ++t) {
+            const int w = key0 + kk + 8 * t - L;
+            const bool vis = w < 0 ? here : w < 16 && ((anc >> w) & 1u) && w + L < n_keys;
+            if (!vis) sc[nt][t >> 1][(t & 1) * 2 + e] = -INFINITY;
+          }
         }
       }
+      float m0 = sc[nt][0][0], m1 = sc[nt][0][1];
+#pragma unroll
+      for (int t = 1; t < 2 * MT; ++t) {
+        m0 = fmaxf(m0, sc[nt][t >> 1][(t & 1) * 2]);
+        m1 = fmaxf(m1, sc[nt][t >> 1][(t & 1) * 2 + 1]);
+      }
+      over |= fmaf(m0, row.z, -top.x) > kSlack || fmaf(m1, row.w, -top.y) > kSlack;
+    }
+    return over;
+  };
+
+  // Move the running maxima (and 2^-e) to what this page's scores and scales ask for and
+  // rescale the accumulators.
+  auto raise_max = [&] {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float4 row = s_row[nt * 4 + c];
+      float m0 = sc[nt][0][0], m1 = sc[nt][0][1];
+#pragma unroll
+      for (int t = 1; t < 2 * MT; ++t) {
+        m0 = fmaxf(m0, sc[nt][t >> 1][(t & 1) * 2]);
+        m1 = fmaxf(m1, sc[nt][t >> 1][(t & 1) * 2 + 1]);
+      }
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+        m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+      }
+      if (g == 0) {
+        s_red[warp][nt * 8 + 2 * c] = m0 * row.z;
+        s_red[warp][nt * 8 + 2 * c + 1] = m1 * row.w;
+      }
+    }
+    uint32_t smax = 0;
+#pragma unroll
+    for (int t = 0; t < 2 * MT; ++t) smax = max(smax, vw[t]);
+    smax = __reduce_max_sync(0xffffffffu, smax) >> 16;
+    if (lane == 0) s_smax[warp] = smax;
+    team_sync<TW>();
+#pragma unroll
+    for (int w = 0; w < TW; ++w) smax = max(smax, s_smax[team * TW + w]);
+    float re = 1.f;
+    if (smax >= s_lim) {
+      const uint32_t e = __float_as_uint(__half2float(__ushort_as_half((unsigned short)smax))) >> 23;
+      const float now = __uint_as_float((254u - e) << 23);
+      re = now / inv_e;
+      inv_e = now;
+      // the limit is 2^4 times the power of two at or below smax
+      s_lim = __half_as_ushort(__float2half_rn(fminf(__uint_as_float((e + 4u) << 23), 65504.f)));
+      if (s_lim == 0x7bffu) s_lim = 0x7c00u;
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 old = s_max[team][nt * 4 + c];
+      float2 now = old;
+#pragma unroll
+      for (int w = 0; w < TW; ++w) {
+        now.x = fmaxf(now.x, s_red[team * TW + w][nt * 8 + 2 * c]);
+        now.y = fmaxf(now.y, s_red[team * TW + w][nt * 8 + 2 * c + 1]);
+      }
+      const float a0 = ex2(old.x - now.x), a1 = ex2(old.y - now.y);
+#pragma unroll
+      for (int t = 0; t < PW; ++t) {
+        acc[nt][t][0] *= a0 * re;
+        acc[nt][t][1] *= a1 * re;
+        acc[nt][t][2] *= a0 * re;
+        acc[nt][t][3] *= a1 * re;
+      }
+      accr[nt][0] *= a0 * re;
+      accr[nt][1] *= a1 * re;
+      lrow[nt][0] *= a0;
+      lrow[nt][1] *= a1;
+      zrow[nt][0] *= a0;
+      zrow[nt][1] *= a1;
+    }
+    team_sync<TW>();
+    for (int r = tw * 32 + lane; r < ROWS; r += TW * 32) {
+      float* top = reinterpret_cast<float*>(s_max[team]) + r;
+      float m = *top;
+#pragma unroll
+      for (int w = 0; w < TW; ++w) m = fmaxf(m, s_red[team * TW + w][r]);
+      *top = m;
+    }
+    team_sync<TW>();
+  };
+
+  // Weights of 16-token step t of the page whose scores are in sc, as B fragments pb.
+  uint32_t pb[NT][2 * MT];
+  auto weights = [&](int t) {
+    float vs[2], vz[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&vw[2 * t + u]));
+      vs[u] = f.y * inv_e;
+      vz[u] = fmaf(7.5f, f.y, f.x);
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const float4 row = s_row[nt * 4 + c];
+      const float2 top = s_max[team][nt * 4 + c];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float* x = &sc[nt][t][u * 2];
+        const float w0 = ex2(fmaf(x[0], row.z, -top.x)), w1 = ex2(fmaf(x[1], row.w, -top.y));
+        lrow[nt][0] += w0;
+        lrow[nt][1] += w1;
+        zrow[nt][0] = fmaf(w0, vz[u], zrow[nt][0]);
+        zrow[nt][1] = fmaf(w1, vz[u], zrow[nt][1]);
+        pb[nt][2 * t + u] = movmatrix_trans(pack_f16x2(w0 * vs[u], w1 * vs[u]));
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+      mma(accr[nt], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[nt][2 * t], pb[nt][2 * t + 1]);
+  };
+
+  // Pieces (words of a token pair) of this lane: which of a chunk's words it takes varies
+  // with g, so that the 32 lanes of a narrow load hit all banks (any dim may be any row
+  // of the product).
+  constexpr int NPIECE = C::kPieces;
+  int piece0 = 0;  // first of them
+  if (TW == kWarps) piece0 = HD == 128 ? tw ^ (g >> 1) : (tw >> 1) ^ ((g >> 1) & 1);
+  const int v_off = kPage * HD / 2 + c * 128 + ((g ^ (2 * c)) << 4) + piece0 * 4;
+  // PV product of the 16-token step t of the page whose V codes (of this lane) start at v.
+  auto pv_step = [&](const uint8_t* v, int t, const uint32_t (&b)[NT][2]) {
+    uint32_t x0[NPIECE], x1[NPIECE];  // tokens {2c, 2c+1} and {2c+8, 2c+9}
+    kv4_v_words<HD, NPIECE>(v, t, x0, x1);
+    if (PW == 1 && (tw & 1)) x0[0] >>= 8, x1[0] >>= 8;  // head_dim 64, team of four: half of a piece's dims
+#pragma unroll
+    for (int w = 0; w < NPIECE; ++w) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        mma(acc[nt][(2 * w) % PW], x0[w] & 0x000f000fu, x0[w] & 0x00f000f0u, x1[w] & 0x000f000fu, x1[w] & 0x00f000f0u,
+            b[nt][0], b[nt][1]);
+      if (PW > 1) {
+        const uint32_t y0 = x0[w] >> 8, y1 = x1[w] >> 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          mma(acc[nt][(2 * w + 1) % PW], y0 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x000f000fu, y1 & 0x00f000f0u,
+              b[nt][0], b[nt][1]);
+      }
+    }
+  };
+
+  // The team's pages: team, team + TEAMS, ...; page j is in stage j % S.
+  int s = team, ps = 0;   // stages of the team's current page and of the one before
+  uint32_t par = 0;
+  auto advance = [&] {
+    ps = s;
+    s += TEAMS;
+    if (s >= S) {
+      s -= S;
+      par ^= 1u;
+    }
+  };
+  if constexpr (TW == 1) {
+    for (int j = team; j < npg; j += TEAMS) {
+      if (team_any<1>(scores(j, s, par))) raise_max();
+      // the weights of a step are computed beside the products of the step before: the
+      // exp2 and transposes then run under the tensor cores
+      const uint8_t* v = ring + s * C::kBlock + v_off;
+      weights(0);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (t + 1 < MT) weights(t + 1);
+        uint32_t b[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) b[nt][0] = pb[nt][2 * t], b[nt][1] = pb[nt][2 * t + 1];
+        pv_step(v, t, b);
+      }
+      __syncwarp();
+      fence_proxy_async();  // the stage was read through the generic proxy
+      if (j + S < npg) issue(j + S, s);
+      advance();
+    }
+  } else {
+    bool over = npg > 0 && scores(0, s, par);
+    uint8_t* pf0 = pfrag + lane * 16;  // weights: [page parity][nt][step / 2][lane][step % 2], 8 bytes each
+    for (int j = 0;; ++j) {
+      // after this barrier the weights of page j - 1 are stored, and every warp has left
+      // the PV product of page j - 2
+      const bool any = team_any<TW>(over);
+      if (j > 0) {
+        if (warp == 0 && j > 1 && j - 2 + S < npg) {
+          fence_proxy_async();  // the stage was read through the generic proxy
+          issue(j - 2 + S, ps == 0 ? S - 1 : ps - 1);
+        }
+        const uint8_t* v = ring + ps * C::kBlock + v_off;
+        const uint8_t* pf = pf0 + ((j - 1) & 1) * (NT * 1024);
+#pragma unroll
+        for (int t2 = 0; t2 < 2; ++t2) {
+          uint4 pw[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) pw[nt] = *reinterpret_cast<const uint4*>(pf + (nt * 2 + t2) * 512);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t b[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) b[nt][0] = u ? pw[nt].z : pw[nt].x, b[nt][1] = u ? pw[nt].w : pw[nt].y;
+            pv_step(v, t2 * 2 + u, b);
+          }
+        }
+      }
+      if (j >= npg) break;
+      if (any) raise_max();
+      weights(0);
+      uint8_t* pf = pf0 + (j & 1) * (NT * 1024) + (tw >> 1) * 512 + (tw & 1) * 8;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) *reinterpret_cast<uint2*>(pf + nt * 1024) = make_uint2(pb[nt][0], pb[nt][1]);
+      advance();
+      over = j + 1 < npg && scores(j + 1, s, par);
     }
   }
+  if (failed) {
+    // give copies still in flight the same time to land before the
+    // CTA's shared memory is given up
+    (void)mbar_wait(&full[lane % S], 0, nullptr);
+    (void)mbar_wait(&full[lane % S], 1, nullptr);
+  }
   __syncthreads();
-  // merge the CTA's partials into the first; out = sum_i 2^(m_i - M) o_i, the same for l
-  constexpr int V4 = HD / 4;
-  for (int it = threadIdx.x; it < rows * V4; it += kThreads) {
-    const int r = it / V4, d4 = it % V4;
-    float M = -INFINITY;
-    for (int i = 0; i < NP; ++i) M = fmaxf(M, part_m[i * n_rows8 + r]);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-    for (int i = 0; i < NP; ++i) {
-      const float m = part_m[i * n_rows8 + r];
-      const float w = m == -INFINITY ? 0.f : ex2(m - M);
-      const float4 x = *reinterpret_cast<const float4*>(part_o + ((long long)i * n_rows8 + r) * HD + d4 * 4);
-      if (w != 0.f) {
+  // The teams' partials: sums over the team's tokens, then O, in the ring's place.
+  const float e_up = 1.f / inv_e;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float2 l = make_float2(lrow[nt][0], lrow[nt][1]), z = make_float2(zrow[nt][0], zrow[nt][1]);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l.x += __shfl_xor_sync(0xffffffffu, l.x, o);
+      l.y += __shfl_xor_sync(0xffffffffu, l.y, o);
+      z.x += __shfl_xor_sync(0xffffffffu, z.x, o);
+      z.y += __shfl_xor_sync(0xffffffffu, z.y, o);
+    }
+    if (g == 0) {
+      s_red[warp][nt * 8 + 2 * c] = l.x;
+      s_red[warp][nt * 8 + 2 * c + 1] = l.y;
+      s_red2[warp][nt * 8 + 2 * c] = z.x - 7.5f * e_up * accr[nt][0];
+      s_red2[warp][nt * 8 + 2 * c + 1] = z.y - 7.5f * e_up * accr[nt][1];
+    }
+  }
+  team_sync<TW>();
+  float* const part = reinterpret_cast<float*>(ring);  // [TEAMS][ROWS][HD]
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int r = nt * 8 + 2 * c + e;
+      float bias = 0.f;
+#pragma unroll
+      for (int w = 0; w < TW; ++w) bias += s_red2[team * TW + w][r];
+      const float u0 = e_up * 16777216.f, u1 = e_up * 1048576.f;
+      float* o = part + (team * ROWS + r) * HD + g * (HD / 8) + piece0 * 4;
+      if constexpr (PW == 1)
+        *reinterpret_cast<float2*>(o + (tw & 1) * 2) =
+            make_float2(fmaf(acc[nt][0][e], u0, bias), fmaf(acc[nt][0][2 + e], u1, bias));
+      else
+#pragma unroll
+        for (int w = 0; w < PW / 2; ++w)
+          *reinterpret_cast<float4*>(o + w * 4) =
+              make_float4(fmaf(acc[nt][2 * w][e], u0, bias), fmaf(acc[nt][2 * w][2 + e], u1, bias),
+                          fmaf(acc[nt][(2 * w + 1) % PW][e], u0, bias), fmaf(acc[nt][(2 * w + 1) % PW][2 + e], u1, bias));
+    }
+  __syncthreads();
+  // the CTA's: sum_i 2^(m_i - M) o_i over the teams; normalised and rounded where the
+  // group is whole, else left in the workspace
+  {
+    constexpr int V4 = HD / 4;
+    const bool whole = pieces == 1;
+    float* const ws = CL ? nullptr : kv4_partial(p.workspace, slot, ROWS, HD);
+    for (int it = threadIdx.x; it < rows * V4; it += kThreads) {
+      const int r = it / V4, d4 = it % V4;
+      float m[TEAMS], M = kNoMax, l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < TEAMS; ++i) {
+        m[i] = reinterpret_cast<const float*>(s_max[i])[r];
+        M = fmaxf(M, m[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < TEAMS; ++i) {
+        const float w = TEAMS == 1 ? 1.f : ex2(m[i] - M);
+        const float4 x = *reinterpret_cast<const float4*>(part + (i * ROWS + r) * HD + d4 * 4);
         o.x = fmaf(w, x.x, o.x);
         o.y = fmaf(w, x.y, o.y);
         o.z = fmaf(w, x.z, o.z);
         o.w = fmaf(w, x.w, o.w);
-        l = fmaf(w, part_l[i * n_rows8 + r], l);
-      }
-    }
-    *reinterpret_cast<float4*>(part_o + (long long)r * HD + d4 * 4) = o;
-    if (d4 == 0) {
-      s_m[r] = M;
-      s_l[r] = l;
-    }
-  }
-  if (CS > 1) cluster.sync();
-  else __syncthreads();
-  // the cluster's CTAs share the rows
-  if (!s_fail) {
-    const uint32_t o_base = smem_u32(part_o), m_base = smem_u32(s_m), l_base = smem_u32(s_l);
-    const int n_my = rows > rank ? (rows - rank + CS - 1) / CS : 0;
-    for (int it = threadIdx.x; it < n_my * V4; it += kThreads) {
-      const int r = rank + it / V4 * CS, d4 = it % V4;
-      float M = -INFINITY;
-      float ms[16], ls[16];
-      float4 os[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (i < CS) {
-          ms[i] = ld_dsmem_f32(mapa_u32(m_base + r * 4, i));
-          ls[i] = ld_dsmem_f32(mapa_u32(l_base + r * 4, i));
-          os[i] = ld_dsmem_f4(mapa_u32(o_base + (r * HD + d4 * 4) * 4, i));
+        for (int k = 0; k < TW; ++k) l = fmaf(w, s_red[i * TW + k][r], l);
+      }
+      if (s_fail) o = make_float4(NAN, NAN, NAN, NAN), l = 1.f;  // a wait ran out
+      if (whole) {
+        store_row4(p, row0 + r / grp, kvh * grp + r % grp, HD, d4, o, l);
+      } else if (CL) {  // the first team's place; each item reads and writes its own four values
+        *reinterpret_cast<float4*>(part + r * HD + d4 * 4) = o;
+        if (d4 == 0) {
+          s_m[r] = M;
+          s_l[r] = l;
         }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < CS) M = fmaxf(M, ms[i]);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (i < CS && ms[i] != -INFINITY) {
-          const float w = ex2(ms[i] - M);
-          l = fmaf(w, ls[i], l);
-          o.x = fmaf(w, os[i].x, o.x);
-          o.y = fmaf(w, os[i].y, o.y);
-          o.z = fmaf(w, os[i].z, o.z);
-          o.w = fmaf(w, os[i].w, o.w);
-        }
-      }
-      const float inv = l > 0.f ? 1.f / l : 0.f;  // a row that sees no token is zeros
-      uint2 w2;
-      if (p.bf16) {
-        w2.x = kv4_pack2<true>(o.x * inv, o.y * inv);
-        w2.y = kv4_pack2<true>(o.z * inv, o.w * inv);
       } else {
-        w2 = pack_act4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        *reinterpret_cast<float4*>(ws + r * HD + d4 * 4) = o;
+        if (d4 == 0) {
+          ws[ROWS * HD + r] = M;
+          ws[ROWS * HD + ROWS + r] = l;
+        }
       }
-      uint16_t* dst = static_cast<uint16_t*>(p.out) +
-                      ((long long)(row0 + r / grp) * p.Hq + kvh * grp + r % grp) * HD + d4 * 4;
-      *reinterpret_cast<uint2*>(dst) = w2;
+    }
+    if constexpr (CL) {
+      if (pieces > 1) {
+        cluster_arrive();
+        cluster_wait();
+        // the cluster's CTAs share the rows; all remote loads of a row are in flight together
+        const uint32_t o_base = smem_u32(part), m_base = smem_u32(s_m), l_base = smem_u32(s_l);
+        const int n_my = rows > piece ? (rows - piece + pieces - 1) / pieces : 0;
+        for (int it = threadIdx.x; it < n_my * V4; it += kThreads) {
+          const int r = piece + it / V4 * pieces, d4 = it % V4;
+          float M = kNoMax, ms[16], ls[16];
+          float4 os[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (i < pieces) {
+              ms[i] = ld_dsmem_f32(mapa_u32(m_base + r * 4, i));
+              ls[i] = ld_dsmem_f32(mapa_u32(l_base + r * 4, i));
+              os[i] = ld_dsmem_f4(mapa_u32(o_base + (r * HD + d4 * 4) * 4, i));
+              M = fmaxf(M, ms[i]);
+            }
+          }
+          float l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (i < pieces) {
+              const float w = ex2(ms[i] - M);
+              l = fmaf(w, ls[i], l);
+              o.x = fmaf(w, os[i].x, o.x);
+              o.y = fmaf(w, os[i].y, o.y);
+              o.z = fmaf(w, os[i].z, o.z);
+              o.w = fmaf(w, os[i].w, o.w);
+            }
+          }
+          store_row4(p, row0 + r / grp, kvh * grp + r % grp, HD, d4, o, l);
+        }
+        __syncwarp();
+        cluster_arrive();  // keep this CTA's shared memory until every CTA has read it
+        cluster_wait();
+      }
     }
   }
-  if (CS > 1) cluster.sync();  // keep this CTA's shared memory until every CTA has read it
+}
+
+// Merge the partials of one cut group: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// grid (chunks of 128 float4 of a group's rows, Hkv, B).
+template <int HD>
+__global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4AttnParams p, int ws_rows) {
+  constexpr int V4 = HD / 4;
+  const int b = blockIdx.z, kvh = blockIdx.y, grp = p.Hq / p.Hkv;
+  const Kv4Seq mine = kv4_first_seqs(p);
+  const Kv4Seq seq = kv4_seq_at(p, mine, b);
+  const Kv4Plan plan = kv4_plan(p, mine);
+  const int n = kv4_pieces(seq.pages, plan.target);
+  int before_cut = 0;  // partials of the sequences before this one
+  for (int i = threadIdx.x & 31; i < b; i += 32) {
+    const int k = kv4_pieces(i < 32 ? mine.pages : kv4_seq(p, i).pages, plan.target);
+    if (k > 1) before_cut += k;
+  }
+  const int i0 = warp_sum(before_cut) * p.Hkv + kvh * n;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (n < 2) return;  // one CTA finished the group
+  const int it = blockIdx.x * 128 + threadIdx.x;
+  const int r = it / V4, d4 = it % V4;
+  if (r >= seq.Wb * grp) return;
+  float M = kNoMax, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int NB = 8;  // partials whose loads are in flight together
+  for (int k0 = 0; k0 < n; k0 += NB) {
+    float ms[NB], ls[NB];
+    float4 os[NB];
+    float mb = M;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const float* ws = kv4_partial(p.workspace, i0 + min(k0 + k, n - 1), ws_rows, HD);
+      os[k] = *reinterpret_cast<const float4*>(ws + r * HD + d4 * 4);
+      ms[k] = ws[ws_rows * HD + r];
+      ls[k] = ws[ws_rows * HD + ws_rows + r];
+      mb = fmaxf(mb, ms[k]);
+    }
+    const float a = ex2(M - mb);
+    M = mb;
+    l *= a;
+    o.x *= a, o.y *= a, o.z *= a, o.w *= a;
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+      if (k0 + k < n) {
+        const float w = ex2(ms[k] - M);
+        l = fmaf(w, ls[k], l);
+        o.x = fmaf(w, os[k].x, o.x);
+        o.y = fmaf(w, os[k].y, o.y);
+        o.z = fmaf(w, os[k].z, o.z);
+        o.w = fmaf(w, os[k].w, o.w);
+      }
+  }
+  store_row4(p, seq.row0 + r / grp, kvh * grp + r % grp, HD, d4, o, l);
 }
 
 // Function attributes are per device: one bit per device once they are set there.
 template <typename K>
-cudaError_t configure(K kernel, int smem, std::atomic<uint64_t>& done) {
+cudaError_t configure(K kernel, int smem, bool cluster, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (done.load(std::memory_order_acquire) >> (dev & 63) & 1ull) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess && cluster) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) done.fetch_or(1ull << (dev & 63), std::memory_order_release);
   return e;
 }
 
-template <int HD, int NT, int KG>
-cudaError_t launch_kg(Kv4AttnParams p, int ng, int cs, cudaStream_t st) {
-  using C = Cfg<HD>;
-  const int teams = kWarps / (KG * ng);
-  p.row_tiles = NT * ng;
-  p.stages = C::stages(p.row_tiles) / teams;
-  const int smem = teams * p.stages * C::kBlock + p.row_tiles * C::kQTile;
+// Pages of a group, at most.
+int hint_pages(const Kv4AttnParams& p) { return (p.kv_len_hint + kPage - 1) / kPage; }
+
+// Short caches: the CTAs of a group as one cluster, where all clusters fit the GPU at once (14 of
+// 16 CTAs, 36 of 8, 74 of 4 and 152 of 2 do with two CTAs per SM) and a CTA gets four pages at
+// most.  No workspace and no second launch: 7.0 against 8.2 us at 1024 tokens, one sequence of 8
+// kv heads.  0: not short.
+int cluster_size(int B, int Hkv, int pages) {
+  const long long groups = (long long)B * Hkv;
+  if (pages <= 4 && groups <= (1 << 30)) return 1;
+  const struct { int cs, fit; } sizes[] = {{2, 152}, {4, 74}, {8, 36}, {16, 14}};
+  for (const auto& s : sizes)
+    if (groups <= s.fit && pages <= 4 * s.cs) {
+      int cs = s.cs;  // the widest that fits: fewer pages for each CTA
+      for (const auto& w : sizes)
+        if (w.cs > cs && groups <= w.fit && pages >= w.cs) cs = w.cs;
+      return cs;
+    }
+  return 0;
+}
+
+template <int HD, int NT>
+cudaError_t launch_cluster(Kv4AttnParams p, int cs, cudaStream_t st) {
+  using C = Cfg<HD, NT, kWarps>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = configure(kv4_attention_kernel<HD, NT, KG>, C::kSmemBudget, done);
+  p.stages = C::stages(2);
+  const int smem = C::kFixed + p.stages * C::kBlock;
+  cudaError_t e = configure(kv4_attention_kernel<HD, NT, kWarps, true>, smem, true, done);
   if (e != cudaSuccess) return e;
-  return launch_k_cluster(kv4_attention_kernel<HD, NT, KG>, dim3(cs, p.Hkv, p.B), dim3(kThreads),
-                          smem, st, dim3(cs, 1, 1), p);
+  p.cluster = cs;
+  return launch_k_cluster(kv4_attention_kernel<HD, NT, kWarps, true>, dim3(p.B * p.Hkv * cs), dim3(kThreads), smem, st,
+                          dim3(cs, 1, 1), p);
+}
+
+template <int HD, int NT, int TW>
+cudaError_t launch_pieces(Kv4AttnParams p, cudaStream_t st) {
+  using C = Cfg<HD, NT, TW>;
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = configure(kv4_attention_kernel<HD, NT, TW, false>, C::kFixed + C::stages(1) * C::kBlock, false, done);
+  if (e != cudaSuccess) return e;
+  const int pages = hint_pages(p);
+  const long long groups = (long long)p.B * p.Hkv;
+  const long long most = std::min<long long>(groups * pages, (long long)C::kCtas * p.sm_count);
+  const int occ = (int)std::min<long long>(C::kCtas, (std::max(most, groups) + p.sm_count - 1) / p.sm_count);
+  p.slots = occ * p.sm_count;
+  p.stages = C::stages(occ);
+  const long long ctas = groups < p.slots ? std::min<long long>(p.slots, groups * pages) : groups + p.slots;
+  if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
+  e = launch_k(kv4_attention_kernel<HD, NT, TW, false>, dim3((unsigned)ctas), dim3(kThreads),
+               C::kFixed + p.stages * C::kBlock, st, p);
+  if (e != cudaSuccess) return e;
+  const int chunks = (p.W * (p.Hq / p.Hkv) * (HD / 4) + 127) / 128;
+  return launch_k(kv4_merge_kernel<HD>, dim3(chunks, p.Hkv, p.B), dim3(128), 0, st, p, NT * 8);
+}
+
+template <int HD, int NT>
+cudaError_t launch_nt(const Kv4AttnParams& p, cudaStream_t st) {
+  if (const int cs = cluster_size(p.B, p.Hkv, hint_pages(p))) return launch_cluster<HD, NT>(p, cs, st);
+  return launch_pieces<HD, NT, (NT <= 2 ? 1 : kWarps)>(p, st);
 }
 
 template <int HD>
 cudaError_t launch_hd(const Kv4AttnParams& p, cudaStream_t st) {
-  const int tiles = (p.W * (p.Hq / p.Hkv) + 7) / 8;
-  if (tiles < 1 || tiles > Cfg<HD>::kMaxTiles) return cudaErrorInvalidValue;
-  // The widest cluster whose grid fits two CTAs per SM.
-  int cs = 16;
-  while (cs > 1 && p.B * p.Hkv * cs > 2 * p.sm_count) cs >>= 1;
-  const int pages = (p.kv_len_hint + kPage - 1) / kPage;
-  const int per_cta = (pages + cs - 1) / cs;
-  const bool few = per_cta < 8;  // too few pages for four independent teams
-  switch (tiles) {
-    case 1: return few ? launch_kg<HD, 1, 4>(p, 1, cs, st) : launch_kg<HD, 1, 1>(p, 1, cs, st);
-    case 2: return few ? launch_kg<HD, 2, 4>(p, 1, cs, st) : launch_kg<HD, 2, 1>(p, 1, cs, st);
-    case 3: return few ? launch_kg<HD, 3, 4>(p, 1, cs, st) : launch_kg<HD, 3, 1>(p, 1, cs, st);
-    case 4: return few ? launch_kg<HD, 2, 2>(p, 2, cs, st) : launch_kg<HD, 2, 1>(p, 2, cs, st);
-    case 5:
-    case 6: return few ? launch_kg<HD, 3, 2>(p, 2, cs, st) : launch_kg<HD, 3, 1>(p, 2, cs, st);
-    default: return launch_kg<HD, 2, 1>(p, 4, cs, st);
+  switch ((p.W * (p.Hq / p.Hkv) + 7) / 8) {
+    case 1: return launch_nt<HD, 1>(p, st);
+    case 2: return launch_nt<HD, 2>(p, st);
+    case 3: return launch_nt<HD, 3>(p, st);
+    case 4: return launch_nt<HD, 4>(p, st);
+    case 5: return launch_nt<HD, 5>(p, st);
+    case 6: return launch_nt<HD, 6>(p, st);
+    case 7: return launch_nt<HD, 7>(p, st);
+    case 8: return launch_nt<HD, 8>(p, st);
+    default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
+
+// The partials of cut groups: at most two for each slot of the largest grid (4 CTAs per SM, 3
+// from four row tiles on).
+long long kv4_attention_workspace(int B, int Hkv, int rows, int hd, int kv_len_hint, int sm_count) {
+  if (cluster_size(B, Hkv, (kv_len_hint + kPage - 1) / kPage)) return 0;
+  const int nt = (rows + 7) / 8;
+  return 2ll * (nt <= 3 ? 4 : 3) * sm_count * nt * 8 * (hd + 2) * 4;
+}
 
 cudaError_t launch_kv4_attention(const Kv4AttnParams& p, cudaStream_t st) {
   return p.hd == 128 ? launch_hd<128>(p, st) : launch_hd<64>(p, st);

@@ -44,7 +44,7 @@ EXPORTS = ["spec_model_create", "spec_model_destroy", "spec_model_set_weight", "
            "spec_kv_fill_random", "spec_sync_status", "spec_max_pages_per_seq", "spec_last_launch_count", "spec_last_error",
            "spec_set_profiling", "spec_read_profile", "spec_accept_greedy_noalloc", "spec_verify_ragged",
            "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write",
-           "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention"]
+           "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention", "spec_kv4_attention_workspace"]
 
 RAGGED_CAP_ACCEPT, RAGGED_COMPACT = 1, 2
 
@@ -96,7 +96,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_kv4_write": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, I64, I64, P, P]),
         "spec_kv4_read": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, P]),
         "spec_kv4_attention": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, I32, P, I64, P, F32, I32, P, P,
-                                     P]),
+                                     P, I64, P]),
+        "spec_kv4_attention_workspace": (I64, [I32, I32, I32, I32, I32, I32, I32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -454,23 +455,31 @@ def spec_kv4_pool(num_pages: int, n_kv_heads: int, head_dim: int, device="cuda")
     return torch.zeros(num_pages, n_kv_heads, block, dtype=torch.uint8, device=device)
 
 
+_KV4_HEAD_DIM = {4608: 64, 8704: 128}  # by the bytes of a (page, kv head) block
+_KV4_WORKSPACE = {}  # bytes by device index and the arguments of spec_kv4_attention_workspace
+
+
 def _kv4_geometry(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor, row_off):
-    """Checked (num_pages, n_kv_heads, head_dim, B) of a call's pool and tables."""
-    if pool.dtype != torch.uint8 or pool.dim() != 3 or not pool.is_contiguous() or pool.shape[2] not in (4608, 8704):
+    """Checked (num_pages, n_kv_heads, head_dim, B, max_pages) of a call's pool and tables."""
+    ps, ts, i32 = pool.shape, page_table.shape, torch.int32
+    hd = _KV4_HEAD_DIM.get(ps[-1]) if len(ps) == 3 else None
+    if hd is None or pool.dtype is not torch.uint8 or not pool.is_contiguous():
         raise ValueError("pool must be a contiguous uint8 [num_pages, n_kv_heads, 64 * head_dim + 512] tensor "
                          "(spec_kv4_pool)")
-    B = start.shape[0]
-    for t, shape, what in ((start, (B,), "start / kv_len"), (page_table, (B, page_table.shape[-1]), "page_table")):
-        if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape}")
-    if row_off is not None and (row_off.dtype != torch.int32 or tuple(row_off.shape) != (B + 1,)
-                                or not row_off.is_contiguous()):
-        raise ValueError(f"row_off must be a contiguous int32 tensor of shape ({B + 1},)")
+    B = start.numel()
+    if start.dtype is not i32 or start.dim() != 1 or not start.is_contiguous():
+        raise ValueError("start / kv_len must be a contiguous int32 tensor of shape (B,)")
+    if page_table.dtype is not i32 or len(ts) != 2 or ts[0] != B or not page_table.is_contiguous():
+        raise ValueError(f"page_table must be a contiguous int32 tensor of shape ({B}, max_pages)")
     dev = pool.device
-    if dev.type != "cuda" or start.device != dev or page_table.device != dev or (
-            row_off is not None and row_off.device != dev):
+    same = start.device == dev and page_table.device == dev
+    if row_off is not None:
+        if row_off.dtype is not i32 or row_off.dim() != 1 or row_off.numel() != B + 1 or not row_off.is_contiguous():
+            raise ValueError(f"row_off must be a contiguous int32 tensor of shape ({B + 1},)")
+        same = same and row_off.device == dev
+    if not same or not pool.is_cuda:
         raise ValueError("pool, start / kv_len, page_table and row_off must be on one CUDA device")
-    return pool.shape[0], pool.shape[1], (pool.shape[2] - 512) // 64, B
+    return ps[0], ps[1], hd, B, ts[1]
 
 
 def _kv4_rows(x: torch.Tensor, what: str, B: int, heads, hd: int, ragged: bool, dev):
@@ -478,29 +487,31 @@ def _kv4_rows(x: torch.Tensor, what: str, B: int, heads, hd: int, ragged: bool, 
     The heads of a row are contiguous; rows may be strided, evenly over all of x."""
     if x.device != dev or x.dtype not in _KV4_DTYPE:
         raise ValueError(f"{what} must be fp16 or bf16 on {dev}")
+    xs = x.shape
     lead = 1 if ragged else 2
-    if x.dim() != lead + 2 or x.shape[-1] != hd or (heads is not None and x.shape[-2] != heads) or (
-            not ragged and x.shape[0] != B):
+    if len(xs) != lead + 2 or xs[-1] != hd or (heads is not None and xs[-2] != heads) or (not ragged and xs[0] != B):
         want = "[rows, heads, head_dim]" if ragged else "[B, n, heads, head_dim]"
         raise ValueError(f"{what} must be {want} with head_dim {hd}" + (f" and {heads} heads" if heads else "")
                          + ("" if ragged else f" and B {B}"))
+    total, n = (xs[0], 0) if ragged else (xs[0] * xs[1], xs[1])
+    if x.is_contiguous():
+        return total, n, xs[-2] * hd
     st = x.stride()
-    row = st[lead - 1] if x.shape[lead - 1] > 1 else (st[0] if lead == 2 and x.shape[0] > 1 else x.shape[-2] * hd)
-    if x.numel() and ((st[-1] != 1 and hd > 1) or (st[-2] != hd and x.shape[-2] > 1) or (
-            lead == 2 and x.shape[0] > 1 and x.shape[1] > 1 and st[0] != x.shape[1] * row)):
+    row = st[lead - 1] if xs[lead - 1] > 1 else (st[0] if lead == 2 and xs[0] > 1 else xs[-2] * hd)
+    if total and (st[-1] != 1 or (st[-2] != hd and xs[-2] > 1) or (
+            lead == 2 and xs[0] > 1 and xs[1] > 1 and st[0] != xs[1] * row)):
         raise ValueError(f"{what}: each row must be contiguous and the rows evenly spaced")
-    if ragged:
-        return x.shape[0], 0, row
-    return x.shape[0] * x.shape[1], x.shape[1], row
+    return total, n, row
 
 
 def _kv4_call(dev, fn, *args):
     """Call `fn` with the current stream of `dev` (made current for the call where it is not)."""
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        _check(fn(*args, torch._C._cuda_getCurrentRawStream(i)))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, torch.cuda.current_stream(dev).cuda_stream))
+            _check(fn(*args, torch._C._cuda_getCurrentRawStream(i)))
 
 
 def spec_kv4_write(k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor,
@@ -508,15 +519,15 @@ def spec_kv4_write(k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, page_t
     """Quantise K/V rows into the 4-bit cache: k, v [B, n, n_kv_heads, head_dim] at positions
     start[b] .. start[b] + n - 1 of page_table[b], or packed [rows, n_kv_heads, head_dim]
     with sequence b's rows row_off[b] .. row_off[b + 1] - 1.  fp16 or bf16."""
-    lib = load_library()
-    P, H, hd, B = _kv4_geometry(pool, start, page_table, row_off)
+    lib = _lib or load_library()
+    P, H, hd, B, width = _kv4_geometry(pool, start, page_table, row_off)
     dev, ragged = pool.device, row_off is not None
     if k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v must have one shape and type")
     total, n, ks = _kv4_rows(k, "k", B, H, hd, ragged, dev)
     _, _, vs = _kv4_rows(v, "v", B, H, hd, ragged, dev)
     _kv4_call(dev, lib.spec_kv4_write, B, n, total, row_off.data_ptr() if ragged else None, start.data_ptr(),
-              page_table.data_ptr(), page_table.shape[1], P, H, hd, _KV4_DTYPE[k.dtype], k.data_ptr(), v.data_ptr(),
+              page_table.data_ptr(), width, P, H, hd, _KV4_DTYPE[k.dtype], k.data_ptr(), v.data_ptr(),
               ks, vs, pool.data_ptr())
 
 
@@ -525,8 +536,8 @@ def spec_kv4_read(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Ten
     """K and V of n tokens per sequence from position start[b] on, as fp16 or bf16
     [B, n, n_kv_heads, head_dim]; with row_off, n rows in all, [n, n_kv_heads, head_dim].
     Rows of no sequence are left unwritten.  `outs`: preallocated (k, v)."""
-    lib = load_library()
-    P, H, hd, B = _kv4_geometry(pool, start, page_table, row_off)
+    lib = _lib or load_library()
+    P, H, hd, B, width = _kv4_geometry(pool, start, page_table, row_off)
     dev, ragged = pool.device, row_off is not None
     n = int(n)
     if dtype not in _KV4_DTYPE:
@@ -541,7 +552,7 @@ def spec_kv4_read(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Ten
         if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
             raise ValueError(f"outs must be contiguous {dtype} tensors of shape {shape} on {dev}")
     _kv4_call(dev, lib.spec_kv4_read, B, 0 if ragged else n, n if ragged else B * n,
-              row_off.data_ptr() if ragged else None, start.data_ptr(), page_table.data_ptr(), page_table.shape[1], P,
+              row_off.data_ptr() if ragged else None, start.data_ptr(), page_table.data_ptr(), width, P,
               H, hd, _KV4_DTYPE[dtype], pool.data_ptr(), k.data_ptr(), v.data_ptr())
     return k, v
 
@@ -556,8 +567,8 @@ def spec_kv4_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
     ancestors in the window, whose K/V sit at kv_len[b] + 0, 1, ... (parent: tree, default the
     chain).  scale: default head_dim ** -0.5.  max_kv_len: an upper bound of kv_len if known
     (launch shape only).  Returns q's shape and type; rows of no window are left unwritten."""
-    lib = load_library()
-    P, H, hd, B = _kv4_geometry(pool, kv_len, page_table, row_off)
+    lib = _lib or load_library()
+    P, H, hd, B, width = _kv4_geometry(pool, kv_len, page_table, row_off)
     dev, ragged = pool.device, row_off is not None
     total, W, qs = _kv4_rows(q, "q", B, None, hd, ragged, dev)
     Hq = q.shape[-2]
@@ -571,10 +582,19 @@ def spec_kv4_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
             raise ValueError(f"parent must have {W} entries")
         par = _i32_host(parent)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != q.dtype or out.device != dev or out.shape != q.shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
+    key = (dev.index, B, W, Hq, H, hd, width, max_kv_len)
+    size = _KV4_WORKSPACE.get(key)
+    if size is None:
+        if len(_KV4_WORKSPACE) > 4096:
+            _KV4_WORKSPACE.clear()
+        with torch.cuda.device(dev):
+            size = _KV4_WORKSPACE[key] = lib.spec_kv4_attention_workspace(*key[1:])
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
     _kv4_call(dev, lib.spec_kv4_attention, B, W, total, row_off.data_ptr() if ragged else None, kv_len.data_ptr(),
-              page_table.data_ptr(), page_table.shape[1], P, Hq, H, hd, _KV4_DTYPE[q.dtype], q.data_ptr(), qs, par,
-              float(hd ** -0.5 if scale is None else scale), int(max_kv_len), pool.data_ptr(), out.data_ptr())
+              page_table.data_ptr(), width, P, Hq, H, hd, _KV4_DTYPE[q.dtype], q.data_ptr(), qs, par,
+              hd ** -0.5 if scale is None else scale, max_kv_len, pool.data_ptr(), out.data_ptr(),
+              None if ws is None else ws.data_ptr(), size)
     return out

@@ -74,11 +74,12 @@ def _read(spec, **kw):
 
 def _attend(spec, **kw):
     a = dict(B=2, n=3, total=6, row_off=None, start=4096, table=4096, max_pages=4, num_pages=8, Hq=4, H=2, hd=64,
-             dtype=0, q=4096, qs=256, parent=None, scale=0.125, hint=0, pool=4096, out=4096)
+             dtype=0, q=4096, qs=256, parent=None, scale=0.125, hint=0, pool=4096, out=4096, ws=4096, ws_bytes=1 << 40)
     a.update(kw)
     return spec._lib.spec_kv4_attention(a["B"], a["n"], a["total"], a["row_off"], a["start"], a["table"],
                                         a["max_pages"], a["num_pages"], a["Hq"], a["H"], a["hd"], a["dtype"], a["q"],
-                                        a["qs"], a["parent"], a["scale"], a["hint"], a["pool"], a["out"], None)
+                                        a["qs"], a["parent"], a["scale"], a["hint"], a["pool"], a["out"], a["ws"],
+                                        a["ws_bytes"], None)
 
 
 COMMON = [(dict(hd=96), 7), (dict(hd=0), 7), (dict(B=0, total=0), 1), (dict(B=65536, total=65536 * 3), 1),
@@ -109,7 +110,7 @@ def test_read_refusals(spec, kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(n=0, total=0), 1), (dict(n=17, total=34), 1), (dict(Hq=5), 1), (dict(Hq=0), 1), (dict(q=None), 1),
     (dict(out=None), 1), (dict(q=4104), 1), (dict(out=4104), 1), (dict(qs=248), 1), (dict(qs=260), 1),
-    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(hint=-1), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(hint=-1), 1), (dict(ws=None, max_pages=4096), 1), (dict(ws=4100, max_pages=4096), 1),
     (dict(n=9, total=18, Hq=16), 7),                                  # 9 rows x 8 heads of a group
     (dict(parent=(ctypes.c_int32 * 3)(0, 0, 1)), 1), (dict(parent=(ctypes.c_int32 * 3)(-1, 1, 0)), 1)])
 def test_attention_refusals(spec, kw, status):
