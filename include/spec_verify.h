@@ -106,6 +106,16 @@ typedef struct spec_model spec_model; /* opaque; owned by the library */
  * start empty.  Returns SPEC_ERR_UNSUPPORTED_DEVICE on anything but sm_103. */
 spec_status spec_model_create(const spec_config* cfg, spec_model** out);
 
+/* The same with a choice of KV cache.  SPEC_KV_F16 is spec_model_create's cache.
+ * SPEC_KV_INT4 holds K and V in 4 bits with a scale and an offset per token and kv head
+ * (the cells of spec_kv4_write below): 3.76x less memory and cache traffic at head_dim
+ * 128, 3.56x at 64.  Every call of this header works on either; a window's K and V are
+ * quantised as they are written, so its rows attend to the held values and a verify
+ * round sees what decode steps would have left.  Against an fp16 cache the logits move by
+ * the 4-bit rounding. */
+typedef enum spec_kv_format { SPEC_KV_F16 = 0, SPEC_KV_INT4 = 1 } spec_kv_format;
+spec_status spec_model_create_kv(const spec_config* cfg, int32_t kv_format, spec_model** out);
+
 /* Free everything the model owns.  Synchronises the device first.  NULL is a no-op. */
 void spec_model_destroy(spec_model* m);
 
@@ -293,8 +303,8 @@ spec_status spec_accept_greedy_noalloc(int32_t B, int32_t gamma, int32_t V, cons
 spec_status spec_get_kv_state(spec_model* m, int32_t n, const int32_t* seq_ids_host, int32_t* seq_len_host,
                               int32_t* page_table_host);
 
-/* Synchronous host copy of cached K and V (fp16 bits: the cache is fp16) of one
- * sequence, slots [t0, t0+n), layer `layer`: k_host and v_host are
+/* Synchronous host copy of cached K and V (fp16 bits; of a 4-bit cache, the values it
+ * holds rounded to fp16) of one sequence, slots [t0, t0+n), layer `layer`: k_host and v_host are
  * [n, n_kv_heads, head_dim] uint16. */
 spec_status spec_read_kv(spec_model* m, int32_t layer, int32_t seq_id, int32_t t0, int32_t n,
                          uint16_t* k_host, uint16_t* v_host);
@@ -315,7 +325,7 @@ spec_status spec_debug_wait_probe(spec_model* m, int64_t budget_cycles, void* st
  * are the caller's: k, v device [n_layers, n_tokens, n_kv_heads, head_dim] fp16
  * bits (the cache's format), 16-byte aligned.  The sequence is emptied first,
  * then gets pages for n_tokens slots (lowest free first) and the values copied
- * in; its length becomes n_tokens, so the next call's row 0 is the pending
+ * in (quantised, if the cache is held in 4 bits); its length becomes n_tokens, so the next call's row 0 is the pending
  * token at position n_tokens.  Lets a test start the model and a reference
  * from one cache without a prefill.  An exhausted pool sets SPEC_ERR_CAPACITY
  * in the status word (length 0).  Synchronises `stream`. */
@@ -394,7 +404,7 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
 
 /* Timing aid for long contexts: give each sequence (host ids) lens_host[b]
  * cached tokens with pseudo-random bf16 K/V (a hash of seed and position, scaled
- * by `scale`), without running the model.  Attention time does not depend on
+ * by `scale`; quantised, if the cache is held in 4 bits), without running the model.  Attention time does not depend on
  * the values. */
 spec_status spec_kv_fill_random(spec_model* m, int32_t n, const int32_t* seq_ids_host, const int32_t* lens_host,
                                 uint64_t seed, float scale, void* stream);

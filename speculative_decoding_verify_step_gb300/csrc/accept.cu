@@ -29,6 +29,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "kv4.cuh"
 #include "kvstate.cuh"
 #include "launch.cuh"
 #include "sampling.cuh"
@@ -431,7 +432,16 @@ SPEC_DEVICE_INLINE void commit_tree_path(const TreeParams& p, int b, const int* 
     if (src_t / kPage < p.max_pages) {
       const int src_pg = p.page_table[(long long)s * p.max_pages + src_t / kPage];
       const int dst_pg = p.page_table[(long long)s * p.max_pages + dst_t / kPage];
-      if (src_pg >= 0 && dst_pg >= 0 && src_t != dst_t) {
+      if (src_pg >= 0 && dst_pg >= 0 && src_t != dst_t && p.kv4_pool) {
+        for (int r = threadIdx.x; r < p.n_layers * p.Hkv; r += blockDim.x) {
+          const int kvh = r % p.Hkv;
+          const long long layer0 = (long long)(r / p.Hkv) * p.num_pages;
+          uint8_t* src = p.kv4_pool + ((layer0 + src_pg) * p.Hkv + kvh) * kv4_block_bytes(p.hd);
+          uint8_t* dst = p.kv4_pool + ((layer0 + dst_pg) * p.Hkv + kvh) * kv4_block_bytes(p.hd);
+          if (p.hd == 128) kv4_move_token<128>(src, src_t % kPage, dst, dst_t % kPage);
+          else kv4_move_token<64>(src, src_t % kPage, dst, dst_t % kPage);
+        }
+      } else if (src_pg >= 0 && dst_pg >= 0 && src_t != dst_t) {
         for (int r = threadIdx.x; r < per_tok; r += blockDim.x) {
           const int vec = r % vec_per_head;
           const int kvh = (r / vec_per_head) % p.Hkv;

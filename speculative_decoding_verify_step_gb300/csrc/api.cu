@@ -110,6 +110,14 @@ struct spec_model {
   // KV pool: [layer][page][kv head][64][head_dim] for K and for V
   act_t *kpool = nullptr, *vpool = nullptr;
   CUtensorMap tm_k, tm_v;
+  // 4-bit cache (kpool and vpool then only stage one forward's window rows, row r as
+  // slot r): [layer][page][kv head][block]
+  bool kv4 = false;
+  uint8_t* kv4_pool = nullptr;
+  long long kv4_layer = 0;        // bytes of a layer
+  int32_t* stage_slot = nullptr;  // [M_max] 0, 1, 2, ..
+  float* kv4_ws = nullptr;        // partial results of split sequences
+  int stage_pages = 0;
   // sequence state
   int32_t *seq_len = nullptr, *seq_npages = nullptr, *page_table = nullptr;
   uint32_t* free_bits = nullptr;
@@ -294,7 +302,8 @@ spec_status forward(spec_model* m, int B, int W, const int32_t* seq_ids, const i
   const double wb_qkv = 2.0 * m->qkv_n * d, wb_o = 2.0 * d * m->q_dim, wb_gu = 4.0 * F * d, wb_dn = 2.0 * d * F;
   // K/V bytes of one attention launch: the host-side bound on the cached lengths
   const long long bound = std::min<long long>(max_len_bound(m) + W, c.max_seq_len);
-  const double kv_bytes = 2.0 * 2.0 * hd * Hkv * (double)B * (double)bound;
+  const double tok_bytes = m->kv4 ? (double)kv4_block_bytes(hd) / kPage : 2.0 * 2.0 * hd;  // K and V of one kv head
+  const double kv_bytes = tok_bytes * Hkv * (double)B * (double)bound;
   // While a short-context attention runs, HBM has room for about kAttnL2Budget
   // bytes beyond the attention's own K/V: that much of the O projection's and
   // then the gate/up projection's weights is prefetched into L2 (none once the
@@ -309,6 +318,47 @@ spec_status forward(spec_model* m, int B, int W, const int32_t* seq_ids, const i
   const double pf = prefetch ? std::max(0.0, kAttnL2Budget - kv_bytes) : 0.0;
   const unsigned long long pf_o = (unsigned long long)std::min(pf, wb_o - (double)q_o) & ~15ull;
   const unsigned long long pf_gu = (unsigned long long)std::max(0.0, std::min(pf - (double)pf_o, wb_gu)) & ~15ull;
+  // 4-bit cache: the window's K and V, staged by the QKV projection, are quantised into
+  // their cells, then attended to with the rest
+  Kv4WriteParams kw{};
+  Kv4AttnParams ka{};
+  if (m->kv4) {
+    kw.rows.row_slot = m->row_slot;
+    kw.rows.num_pages = c.num_pages;
+    kw.rows.total_rows = M;
+    kw.Hkv = Hkv;
+    kw.hd = hd;
+    kw.k = m->kpool;
+    kw.v = m->vpool;
+    kw.row_blk = kPage;
+    kw.blk_stride = (long long)Hkv * kPage * hd;
+    kw.k_row_stride = kw.v_row_stride = hd;
+    kw.head_stride = (long long)kPage * hd;
+    ka.q = m->qrot;
+    ka.q_row_stride = m->q_dim;
+    ka.out = m->attn_out;
+    ka.page_table = m->page_table;
+    ka.seq_ids = seq_ids;
+    ka.kv_len = m->seq_start;
+    ka.row_begin = m->seq_rowoff;
+    ka.row_count = m->seq_wlen;
+    ka.B = B;
+    ka.W = W;
+    ka.total_rows = M;
+    ka.Hq = Hq;
+    ka.Hkv = Hkv;
+    ka.hd = hd;
+    ka.max_pages = m->max_pages;
+    ka.num_pages = c.num_pages;
+    ka.table_rows = c.max_batch;
+    ka.sm_count = m->sm_count;
+    ka.kv_len_hint = ap.kv_len_hint;
+    ka.scale = 1.f / std::sqrt((float)hd);
+    for (int j = 0; j < 16; ++j) ka.anc[j] = ap.anc[j];
+    ka.early = 1;
+    ka.workspace = m->kv4_ws;
+    ka.status = m->status;
+  }
   for (int l = 0; l < c.n_layers; ++l) {
     auto& Ly = m->layers[l];
     ap.l2_next[0] = reinterpret_cast<const char*>(Ly.wo) + q_o;
@@ -326,18 +376,29 @@ spec_status forward(spec_model* m, int B, int W, const int32_t* seq_ids, const i
       e.Hkv = Hkv;
       e.hd = hd;
       e.row_pos = m->row_pos;
-      e.row_slot = m->row_slot;
+      e.row_slot = m->kv4 ? m->stage_slot : m->row_slot;
       e.rope_cos = m->rope_cos;
       e.rope_sin = m->rope_sin;
       e.q_out = m->qrot;
-      e.kpool = m->kpool + l * layer_elems;
-      e.vpool = m->vpool + l * layer_elems;
+      e.kpool = m->kv4 ? m->kpool : m->kpool + l * layer_elems;
+      e.vpool = m->kv4 ? m->vpool : m->vpool + l * layer_elems;
       e.l2_next = Ly.wo;
       e.l2_next_bytes = q_o;
       CUDA_TRY(profiled(m, 0, wb_qkv, st, [&] { return launch_gemm_epi(kEpiQKV, &Ly.tm_qkv, tmx_xn, BM, e, st); }));
     }
-    ap.layer_row0 = l * c.num_pages * Hkv * kPage;
-    CUDA_TRY(profiled(m, 5, kv_bytes, st, [&] { return launch_attention(&m->tm_k, &m->tm_v, ap, st); }));
+    if (m->kv4) {
+      kw.pool = m->kv4_pool + l * m->kv4_layer;
+      ka.pool = kw.pool;
+      CUDA_TRY(launch_kv4_write(kw, st));
+      for (int i = 0; i < 2; ++i) {
+        ka.l2_next[i] = ap.l2_next[i];
+        ka.l2_next_bytes[i] = ap.l2_next_bytes[i];
+      }
+      CUDA_TRY(profiled(m, 5, kv_bytes, st, [&] { return launch_kv4_attention(ka, st); }));
+    } else {
+      ap.layer_row0 = l * c.num_pages * Hkv * kPage;
+      CUDA_TRY(profiled(m, 5, kv_bytes, st, [&] { return launch_attention(&m->tm_k, &m->tm_v, ap, st); }));
+    }
     {
       EpiParams e = base;
       e.N = d;
@@ -529,6 +590,20 @@ void bump_bounds(spec_model* m, int W) {
   for (auto& v : m->host_len_bound) v = std::min<long long>(v + W, m->cfg.max_seq_len);
 }
 
+Kv4Rows kv4_rows(int B, int rows_per_seq, int total_rows, const int32_t* row_off, const int32_t* start,
+                 const int32_t* page_table, int max_pages, int num_pages) {
+  Kv4Rows r{};
+  r.row_off = row_off;
+  r.start = start;
+  r.page_table = page_table;
+  r.B = B;
+  r.rows_per_seq = rows_per_seq;
+  r.max_pages = max_pages;
+  r.num_pages = num_pages;
+  r.total_rows = total_rows;
+  return r;
+}
+
 }  // namespace
 
 // =============================================================================== C ABI
@@ -541,8 +616,13 @@ int32_t spec_max_pages_per_seq(const spec_model* m) { return m ? m->max_pages : 
 int32_t spec_last_launch_count(const spec_model* m) { return m ? m->last_launches : 0; }
 
 spec_status spec_model_create(const spec_config* cfg, spec_model** out) {
+  return spec_model_create_kv(cfg, SPEC_KV_F16, out);
+}
+
+spec_status spec_model_create_kv(const spec_config* cfg, int32_t kv_format, spec_model** out) {
   if (!cfg || !out) return fail(SPEC_ERR_INVALID_ARG, "NULL argument");
   *out = nullptr;
+  if (kv_format != SPEC_KV_F16 && kv_format != SPEC_KV_INT4) return fail(SPEC_ERR_INVALID_ARG, "unknown kv_format %d", kv_format);
   spec_status s = validate_cfg(*cfg);
   if (s != SPEC_OK) return s;
   int dev = 0;
@@ -595,7 +675,20 @@ spec_status spec_model_create(const spec_config* cfg, spec_model** out) {
     ALLOC(Ly.attn_norm, d);
     ALLOC(Ly.ffn_norm, d);
   }
-  const size_t kv_elems = (size_t)c.n_layers * c.num_pages * c.n_kv_heads * kPage * hd;
+  m->kv4 = kv_format == SPEC_KV_INT4;
+  m->stage_pages = (M_max + kPage - 1) / kPage;
+  const size_t kv_elems =
+      (size_t)(m->kv4 ? m->stage_pages : c.n_layers * (size_t)c.num_pages) * c.n_kv_heads * kPage * hd;
+  if (m->kv4) {
+    m->kv4_layer = (long long)c.num_pages * c.n_kv_heads * kv4_block_bytes(hd);
+    const int rows = c.max_width * (c.n_heads / c.n_kv_heads);
+    long long ws = 16;
+    for (int r = 8; r <= (rows + 7) / 8 * 8; r += 8)  // no batch or length needs more
+      ws = std::max(ws, kv4_attention_workspace(1 << 20, 1, r, hd, 1 << 20, m->sm_count));
+    ALLOC(m->kv4_pool, (size_t)c.n_layers * m->kv4_layer);
+    ALLOC(m->kv4_ws, (size_t)ws / 4);
+    ALLOC(m->stage_slot, M_max);
+  }
   ALLOC(m->kpool, kv_elems);
   ALLOC(m->vpool, kv_elems);
   ALLOC(m->seq_len, c.max_batch);
@@ -650,6 +743,12 @@ spec_status spec_model_create(const spec_config* cfg, spec_model** out) {
     cudaError_t e2 = cudaMemcpy(m->rope_sin, sn.data(), sn.size() * 4, cudaMemcpyHostToDevice);
     if (e1 != cudaSuccess || e2 != cudaSuccess) return bail(fail(SPEC_ERR_CUDA, "rope table upload failed"));
   }
+  if (m->kv4) {
+    std::vector<int32_t> id(M_max);
+    for (int i = 0; i < M_max; ++i) id[i] = i;
+    if (cudaMemcpy(m->stage_slot, id.data(), (size_t)M_max * 4, cudaMemcpyHostToDevice) != cudaSuccess)
+      return bail(fail(SPEC_ERR_CUDA, "stage slot upload failed"));
+  }
   // gains default to 1
   {
     std::vector<float> ones(d, 1.f);
@@ -673,7 +772,7 @@ spec_status spec_model_create(const spec_config* cfg, spec_model** out) {
     ok &= make_map(&m->tm_attn[i], m->attn_out, m->q_dim, m->M_alloc, 64, kBMs[i]);
     ok &= make_map(&m->tm_act[i], m->act, F, m->M_alloc, 64, kBMs[i]);
   }
-  const uint64_t kv_rows = (uint64_t)c.n_layers * c.num_pages * c.n_kv_heads * kPage;
+  const uint64_t kv_rows = kv_elems / hd;
   for (int i = 0; i < kPairBoxes; ++i) {
     ok &= make_map(&m->tm_xn2[i], m->xn, d, m->M_alloc, 64, 8 * (i + 1));
     ok &= make_map(&m->tm_attn2[i], m->attn_out, m->q_dim, m->M_alloc, 64, 8 * (i + 1));
@@ -873,6 +972,7 @@ TreeParams tree_params(spec_model* m, int B, int n_nodes, const int32_t* seq_ids
   tp.max_batch = m->cfg.max_batch;
   tp.kpool = m->kpool;
   tp.vpool = m->vpool;
+  tp.kv4_pool = m->kv4_pool;
   tp.n_layers = m->cfg.n_layers;
   tp.num_pages = m->cfg.num_pages;
   tp.Hkv = m->cfg.n_kv_heads;
@@ -1156,6 +1256,30 @@ spec_status spec_read_kv(spec_model* m, int32_t layer, int32_t seq_id, int32_t t
   CUDA_TRY(cudaMemcpy(pt.data(), m->page_table + (size_t)seq_id * m->max_pages, m->max_pages * 4,
                       cudaMemcpyDeviceToHost));
   const int hd = c.head_dim, Hkv = c.n_kv_heads;
+  if (m->kv4) {
+    for (int t = t0; t < t0 + n; ++t)
+      if (pt[t / kPage] < 0) return fail(SPEC_ERR_INVALID_ARG, "slot %d has no page", t);
+    // expanded into the staging buffers, as many tokens at a time as they hold
+    const int step = m->stage_pages * kPage;
+    for (int d = 0; d < n; d += step) {
+      const int cnt = std::min(step, n - d), at = t0 + d;
+      CUDA_TRY(cudaMemcpy(m->scratch_lens, &at, 4, cudaMemcpyHostToDevice));
+      Kv4ReadParams rp{};
+      rp.rows = kv4_rows(1, cnt, cnt, nullptr, m->scratch_lens, m->page_table + (size_t)seq_id * m->max_pages,
+                         m->max_pages, c.num_pages);
+      rp.Hkv = Hkv;
+      rp.hd = hd;
+      rp.k = m->kpool;
+      rp.v = m->vpool;
+      rp.pool = m->kv4_pool + layer * m->kv4_layer;
+      CUDA_TRY(launch_kv4_read(rp, nullptr));
+      CUDA_TRY(cudaDeviceSynchronize());
+      const size_t elems = (size_t)Hkv * hd;
+      CUDA_TRY(cudaMemcpy(k_host + d * elems, m->kpool, cnt * elems * 2, cudaMemcpyDeviceToHost));
+      CUDA_TRY(cudaMemcpy(v_host + d * elems, m->vpool, cnt * elems * 2, cudaMemcpyDeviceToHost));
+    }
+    return SPEC_OK;
+  }
   for (int t = t0; t < t0 + n; ++t) {
     const int pg = pt[t / kPage];
     if (pg < 0) return fail(SPEC_ERR_INVALID_ARG, "slot %d has no page", t);
@@ -1199,9 +1323,14 @@ spec_status spec_kv_fill_random(spec_model* m, int32_t n, const int32_t* seq_ids
   CUDA_TRY(launch_seq_reset(rp, st));
   CUDA_TRY(launch_alloc_to_len(m->scratch_ids, m->scratch_lens, n, 0, m->seq_len, m->seq_npages, m->page_table,
                                m->free_bits, m->max_pages, m->cfg.num_pages, m->cfg.max_batch, m->status, st));
-  CUDA_TRY(launch_kv_fill_pages(m->kpool, m->vpool, m->page_table, m->seq_npages, m->max_pages, m->scratch_ids, n,
-                                m->cfg.n_layers, m->cfg.num_pages, m->cfg.n_kv_heads, m->cfg.head_dim, seed, scale,
-                                st));
+  if (m->kv4)
+    CUDA_TRY(launch_kv4_fill_pages(m->kv4_pool, m->kv4_layer, m->page_table, m->seq_npages, m->max_pages,
+                                   m->scratch_ids, n, m->cfg.n_layers, m->cfg.num_pages, m->cfg.n_kv_heads,
+                                   m->cfg.head_dim, seed, scale, st));
+  else
+    CUDA_TRY(launch_kv_fill_pages(m->kpool, m->vpool, m->page_table, m->seq_npages, m->max_pages, m->scratch_ids, n,
+                                  m->cfg.n_layers, m->cfg.num_pages, m->cfg.n_kv_heads, m->cfg.head_dim, seed, scale,
+                                  st));
   CUDA_TRY(cudaStreamSynchronize(st));
   for (int i = 0; i < n; ++i) m->host_len_bound[seq_ids_host[i]] = lens_host[i];
   return SPEC_OK;
@@ -1224,9 +1353,28 @@ spec_status spec_kv_write(spec_model* m, int32_t seq_id, int32_t n_tokens, const
   CUDA_TRY(launch_seq_reset(rp, st));
   CUDA_TRY(launch_alloc_to_len(m->scratch_ids, m->scratch_lens, 1, 0, m->seq_len, m->seq_npages, m->page_table,
                                m->free_bits, m->max_pages, c.num_pages, c.max_batch, m->status, st));
-  CUDA_TRY(launch_kv_write(m->kpool, m->vpool, m->page_table, m->max_pages, seq_id, n_tokens,
-                           reinterpret_cast<const act_t*>(k), reinterpret_cast<const act_t*>(v), c.n_layers,
-                           c.num_pages, c.n_kv_heads, c.head_dim, st));
+  if (m->kv4) {
+    const long long elems = (long long)n_tokens * m->kv_dim;
+    CUDA_TRY(cudaMemsetAsync(m->scratch_lens, 0, 4, st));  // from position 0 on
+    for (int l = 0; l < c.n_layers; ++l) {
+      Kv4WriteParams p{};
+      p.rows = kv4_rows(1, n_tokens, n_tokens, nullptr, m->scratch_lens, m->page_table + (size_t)seq_id * m->max_pages,
+                        m->max_pages, c.num_pages);
+      p.Hkv = c.n_kv_heads;
+      p.hd = c.head_dim;
+      p.k = k + l * elems;
+      p.v = v + l * elems;
+      p.row_blk = 1 << 30;
+      p.k_row_stride = p.v_row_stride = m->kv_dim;
+      p.head_stride = c.head_dim;
+      p.pool = m->kv4_pool + l * m->kv4_layer;
+      CUDA_TRY(launch_kv4_write(p, st));
+    }
+  } else {
+    CUDA_TRY(launch_kv_write(m->kpool, m->vpool, m->page_table, m->max_pages, seq_id, n_tokens,
+                             reinterpret_cast<const act_t*>(k), reinterpret_cast<const act_t*>(v), c.n_layers,
+                             c.num_pages, c.n_kv_heads, c.head_dim, st));
+  }
   CUDA_TRY(cudaStreamSynchronize(st));  // ids and lens are host buffers
   m->host_len_bound[seq_id] = n_tokens;
   return SPEC_OK;
@@ -1311,20 +1459,6 @@ spec_status kv4_check_stride(long long stride, long long least, const char* name
   if (stride < least || stride % 8)
     return fail(SPEC_ERR_INVALID_ARG, "%s=%lld must be a multiple of 8 and at least %lld elements", name, stride, least);
   return SPEC_OK;
-}
-
-Kv4Rows kv4_rows(int B, int rows_per_seq, int total_rows, const int32_t* row_off, const int32_t* start,
-                 const int32_t* page_table, int max_pages, int num_pages) {
-  Kv4Rows r{};
-  r.row_off = row_off;
-  r.start = start;
-  r.page_table = page_table;
-  r.B = B;
-  r.rows_per_seq = rows_per_seq;
-  r.max_pages = max_pages;
-  r.num_pages = num_pages;
-  r.total_rows = total_rows;
-  return r;
 }
 
 // Upper bound of a sequence's cached and window tokens, for the launch shape.

@@ -242,6 +242,7 @@ struct TreeParams {
   int max_pages, max_batch;
   __half* kpool;
   __half* vpool;
+  uint8_t* kv4_pool;         // the 4-bit cache instead of kpool / vpool, or null
   int n_layers, num_pages, Hkv, hd;
   int* status;
   // sampled trees: q [B, N, V] (children of node v drawn i.i.d. from q[b, v]; null:

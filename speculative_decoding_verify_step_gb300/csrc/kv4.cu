@@ -9,6 +9,7 @@
 // s up and m down keeps every quotient inside [0, 15], so no code needs a clamp.
 #include "kv4.cuh"
 #include "kv4.h"
+#include "kvstate.cuh"
 #include "launch.cuh"
 
 namespace spec {
@@ -78,6 +79,16 @@ SPEC_DEVICE_INLINE uint32_t kv4_quantise(const float (&x)[8], uint32_t& par) {
   return w;
 }
 
+// Store a thread's codes and its token's parameters in the token's cell.
+template <int HD>
+SPEC_DEVICE_INLINE void kv4_store(uint8_t* block, int t, int j8, const uint32_t (&code)[2], const uint32_t (&par)[2]) {
+  reinterpret_cast<uint32_t*>(block + t * (HD / 2))[j8] = code[0];
+  uint8_t* v = block + kPage * HD / 2;
+  *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) = (uint16_t)code[1];
+  *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) = (uint16_t)(code[1] >> 16);
+  if (j8 < 2) reinterpret_cast<uint32_t*>(block + kPage * HD)[j8 * kPage + t] = j8 ? par[1] : par[0];
+}
+
 // One token and kv head per hd / 8 threads, eight dims of K and of V each.  The
 // warp's tokens are neighbouring rows of one head, so a token pair's V pieces meet
 // in one 128-byte row of the block.
@@ -118,11 +129,40 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
   if (slot < 0) return;
   uint8_t* block = p.pool + ((slot / kPage) * p.Hkv + h) * (long long)kv4_block_bytes(HD);
   const int t = (int)(slot % kPage);
-  reinterpret_cast<uint32_t*>(block + t * (HD / 2))[j8] = code[0];
-  uint8_t* v = block + kPage * HD / 2;
-  *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) = (uint16_t)code[1];
-  *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) = (uint16_t)(code[1] >> 16);
-  if (j8 < 2) reinterpret_cast<uint32_t*>(block + kPage * HD)[j8 * kPage + t] = par[j8];
+  kv4_store<HD>(block, t, j8, code, par);
+}
+
+// Pseudo-random cells.  grid (pages, n_layers, n); each block fills one page of one layer.
+template <int HD>
+__global__ void kv4_fill_kernel(uint8_t* pool, long long layer_bytes, const int32_t* page_table,
+                                const int32_t* seq_npages, int max_pages, const int32_t* seq_ids, int num_pages, int Hkv,
+                                uint64_t seed, float scale) {
+  constexpr int kLanes = HD / 8;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int s = seq_ids[blockIdx.z];
+  const int layer = blockIdx.y, pi = blockIdx.x;
+  if (pi >= seq_npages[s]) return;
+  const int pg = page_table[(long long)s * max_pages + pi];
+  if (pg < 0) return;
+  const int j8 = threadIdx.x % kLanes;
+  for (int e = threadIdx.x / kLanes; e < Hkv * kPage; e += blockDim.x / kLanes) {
+    const int h = e / kPage, t = e % kPage;
+    const long long base = ((((long long)layer * num_pages + pg) * Hkv + h) * kPage + t) * HD + j8 * 8;
+    float x[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint64_t w = splitmix64(seed ^ (uint64_t)(base + i) * 0x2545F4914F6CDD1Dull);
+      x[0][i] = ((float)(uint32_t)(w & 0xffffffu) * (1.0f / 16777216.0f) * 2.f - 1.f) * scale;
+      x[1][i] = ((float)(uint32_t)((w >> 32) & 0xffffffu) * (1.0f / 16777216.0f) * 2.f - 1.f) * scale;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) x[kv][i] = __half2float(to_act(x[kv][i]));
+    }
+    uint32_t code[2], par[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) code[kv] = kv4_quantise<kLanes>(x[kv], par[kv]);
+    kv4_store<HD>(pool + layer * layer_bytes + ((long long)pg * Hkv + h) * kv4_block_bytes(HD), t, j8, code, par);
+  }
 }
 
 // Two fp32 to fp16, finite: s is rounded up, so 15 s + m can pass 65504 by 16.
@@ -190,6 +230,13 @@ cudaError_t launch_rows(K kernel, const P& p, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_kv4_fill_pages(uint8_t* pool, long long layer_bytes, const int32_t* page_table,
+                                  const int32_t* seq_npages, int max_pages, const int32_t* seq_ids, int n, int n_layers,
+                                  int num_pages, int Hkv, int hd, uint64_t seed, float scale, cudaStream_t st) {
+  return launch_k(hd == 128 ? kv4_fill_kernel<128> : kv4_fill_kernel<64>, dim3(max_pages, n_layers, n), dim3(256), 0, st,
+                  pool, layer_bytes, page_table, seq_npages, max_pages, seq_ids, num_pages, Hkv, seed, scale);
+}
 
 cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t st) {
   if (p.hd == 128)

@@ -27,7 +27,7 @@
 
 namespace spec {
 
-SPEC_DEVICE_INLINE constexpr int kv4_block_bytes(int hd) { return kPage * hd + 2 * kPage * 4; }
+__host__ __device__ constexpr int kv4_block_bytes(int hd) { return kPage * hd + 2 * kPage * 4; }
 
 // Byte offset, from the V codes of a block, of the piece with dims d .. d + 3 (d a
 // multiple of 4) of token t.
@@ -41,6 +41,24 @@ SPEC_DEVICE_INLINE int kv4_v_piece(int t, int d) {
   }
   const int blk = (t >> 4) * 4 + ((t & 7) >> 1);  // chunk = tokens {2n, 2n+1}, {2n+8, 2n+9} x 2 pieces
   return blk * 128 + ((g ^ (2 * (blk & 3))) << 4) + ((t >> 3) & 1) * 8 + piece * 4 + (t & 1) * 2;
+}
+
+// Copy one token's cell from block `src`, token ts, to block `dst`, token td.
+template <int HD>
+SPEC_DEVICE_INLINE void kv4_move_token(const uint8_t* src, int ts, uint8_t* dst, int td) {
+#pragma unroll
+  for (int i = 0; i < HD / 32; ++i)
+    reinterpret_cast<uint4*>(dst + td * (HD / 2))[i] = reinterpret_cast<const uint4*>(src + ts * (HD / 2))[i];
+  const uint8_t* vs = src + kPage * HD / 2;
+  uint8_t* vd = dst + kPage * HD / 2;
+#pragma unroll 8
+  for (int d = 0; d < HD; d += 4)
+    *reinterpret_cast<uint16_t*>(vd + kv4_v_piece<HD>(td, d)) =
+        *reinterpret_cast<const uint16_t*>(vs + kv4_v_piece<HD>(ts, d));
+  const uint32_t* ps = reinterpret_cast<const uint32_t*>(src + kPage * HD);
+  uint32_t* pd = reinterpret_cast<uint32_t*>(dst + kPage * HD);
+  pd[td] = ps[ts];
+  pd[kPage + td] = ps[kPage + ts];
 }
 
 // fp32 in fp16's range to fp16, towards -infinity / +infinity.

@@ -29,6 +29,11 @@ struct Kv4WriteParams {
   long long blk_stride, k_row_stride, v_row_stride, head_stride;
   uint8_t* pool;
 };
+// Pseudo-random cells (the hash of the fp16 cache's fill) on every page of the listed sequences,
+// all layers; layer l's pool is pool + l * layer_bytes.
+cudaError_t launch_kv4_fill_pages(uint8_t* pool, long long layer_bytes, const int32_t* page_table,
+                                  const int32_t* seq_npages, int max_pages, const int32_t* seq_ids, int n, int n_layers,
+                                  int num_pages, int Hkv, int hd, uint64_t seed, float scale, cudaStream_t st);
 cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t st);
 
 struct Kv4ReadParams {
@@ -62,6 +67,10 @@ struct Kv4AttnParams {
   int early;
   int stages, slots, cluster;  // ring depth, CTAs resident at once, CTAs of a cluster: set by the launcher
   float* workspace;            // kv4_attention_workspace bytes
+  // Weights of the projections that follow, brought into L2 once the queries are
+  // there; split evenly over the CTAs.  Null / 0: none.
+  const void* l2_next[2];
+  unsigned long long l2_next_bytes[2];  // multiples of 16
   int* status;
 };
 // Bytes of workspace for windows of `rows` query rows per kv head (W * group size).

@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   } else {
     const Kv4Seq mine = kv4_first_seqs(p);
     const Kv4Plan plan = kv4_plan(p, mine);
-    if ((int)blockIdx.x >= plan.total) return;
+    if ((int)blockIdx.x >= plan.total) {
+      if (p.early) pdl_wait();  // the grid's end stands for the predecessor's, too
+      return;
+    }
     int before, before_cut;
     const int b = kv4_find_piece(p, mine, plan.target, blockIdx.x, before, before_cut);
     seq = kv4_seq_at(p, mine, b);
@@ -394,6 +397,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   if (p.early) pdl_wait();
   if (warp == 0)
     for (; issued < min(S, npg); ++issued) issue(issued, issued);
+  if (threadIdx.x == kThreads - 1) {
+    l2_prefetch_share(p.l2_next[0], p.l2_next_bytes[0]);
+    l2_prefetch_share(p.l2_next[1], p.l2_next_bytes[1]);
+  }
 
   // Queries: each row is scaled by a power of two (largest element in [2^14, 2^15)),
   // so the factor 1/16 of the odd columns costs no precision; the sum of the scaled

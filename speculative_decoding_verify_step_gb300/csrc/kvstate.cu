@@ -235,13 +235,6 @@ __global__ void __launch_bounds__(32) alloc_to_len_kernel(const int32_t* seq_ids
   }
 }
 
-SPEC_DEVICE_INLINE uint64_t splitmix64(uint64_t x) {
-  x += 0x9E3779B97F4A7C15ull;
-  x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
-  x = (x ^ (x >> 27)) * 0x94D049BB133111EBull;
-  return x ^ (x >> 31);
-}
-
 // Fill K and V of every allocated page of the listed sequences, all layers.
 // grid: (pages, n_layers, n); each block writes one (layer, page) of one sequence.
 __global__ void kv_fill_kernel(act_t* kpool, act_t* vpool, const int32_t* page_table,

@@ -78,4 +78,12 @@ SPEC_DEVICE_INLINE void truncate_seq(int s, int new_len, int32_t* seq_len, int32
   seq_len[s] = new_len;
 }
 
+// Hash of the pseudo-random cache fills.
+SPEC_DEVICE_INLINE uint64_t splitmix64(uint64_t x) {
+  x += 0x9E3779B97F4A7C15ull;
+  x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
+  x = (x ^ (x >> 27)) * 0x94D049BB133111EBull;
+  return x ^ (x >> 31);
+}
+
 }  // namespace spec

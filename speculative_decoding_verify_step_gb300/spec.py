@@ -44,7 +44,8 @@ EXPORTS = ["spec_model_create", "spec_model_destroy", "spec_model_set_weight", "
            "spec_kv_fill_random", "spec_sync_status", "spec_max_pages_per_seq", "spec_last_launch_count", "spec_last_error",
            "spec_set_profiling", "spec_read_profile", "spec_accept_greedy_noalloc", "spec_verify_ragged",
            "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write",
-           "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention", "spec_kv4_attention_workspace"]
+           "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention", "spec_kv4_attention_workspace",
+           "spec_model_create_kv"]
 
 RAGGED_CAP_ACCEPT, RAGGED_COMPACT = 1, 2
 
@@ -65,6 +66,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     P, I32, I64, F32, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_uint64
     sig = {
         "spec_model_create": (I32, [ctypes.POINTER(spec_config), ctypes.POINTER(P)]),
+        "spec_model_create_kv": (I32, [ctypes.POINTER(spec_config), I32, ctypes.POINTER(P)]),
         "spec_model_destroy": (None, [P]),
         "spec_model_set_weight": (I32, [P, I32, I32, P, I64, P]),
         "spec_seq_reset": (I32, [P, I32, P, P]),
@@ -148,18 +150,27 @@ def _opt_dev(t, device, dtype):
     return t.to(device=device, dtype=dtype).contiguous()
 
 
-class SpecModel:
-    """Owns one spec_model handle.  Method names follow the C ABI without the prefix."""
+KV_FORMATS = {"fp16": 0, "int4": 1}
 
-    def __init__(self, dims, *, max_batch: int, max_width: int, max_seq_len: int, num_pages: int):
+
+class SpecModel:
+    """Owns one spec_model handle.  Method names follow the C ABI without the prefix.
+    kv_format "int4" holds the KV cache in 4 bits (a scale and an offset per token and kv
+    head): 3.6 to 3.8 times the cached tokens in the same memory."""
+
+    def __init__(self, dims, *, max_batch: int, max_width: int, max_seq_len: int, num_pages: int,
+                 kv_format: str = "fp16"):
+        if kv_format not in KV_FORMATS:
+            raise ValueError(f"kv_format must be one of {sorted(KV_FORMATS)}")
         lib = load_library()
         self.dims = dims
         cfg = spec_config(dims.n_layers, dims.d_model, dims.n_heads, dims.n_kv_heads, dims.head_dim, dims.ffn_dim,
                           dims.vocab, dims.rms_eps, dims.rope_theta, 64, max_batch, max_width, max_seq_len, num_pages)
         self.cfg = cfg
         h = ctypes.c_void_p()
-        _check(lib.spec_model_create(ctypes.byref(cfg), ctypes.byref(h)))
+        _check(lib.spec_model_create_kv(ctypes.byref(cfg), KV_FORMATS[kv_format], ctypes.byref(h)))
         self.handle = h
+        self.kv_format = kv_format
         self.device = torch.device("cuda", torch.cuda.current_device())
         self.max_pages = lib.spec_max_pages_per_seq(h)
 
@@ -297,7 +308,8 @@ class SpecModel:
 
     def kv_write(self, seq_id: int, k: torch.Tensor, v: torch.Tensor):
         """Give sequence seq_id the cached K/V k, v: [n_layers, n_tokens, n_kv_heads,
-        head_dim] (converted to fp16, the cache's format); its length becomes n_tokens."""
+        head_dim] (converted to fp16; quantised, if kv_format is "int4"); its length becomes
+        n_tokens."""
         want = (self.dims.n_layers, k.shape[1], self.dims.n_kv_heads, self.dims.head_dim)
         if tuple(k.shape) != want or tuple(v.shape) != want:
             raise ValueError(f"k, v must be {want}")

@@ -161,3 +161,15 @@ def test_binding_row_geometry(spec):
                 torch.zeros(10, 2, 64).half()):
         with pytest.raises(ValueError):
             rows(bad)
+
+
+def test_model_refuses_an_unknown_cache_format(spec):
+    from speculative_decoding_verify_step_gb300 import synth
+    d = synth.TINY
+    cfg = spec.spec_config(d.n_layers, d.d_model, d.n_heads, d.n_kv_heads, d.head_dim, d.ffn_dim, d.vocab, d.rms_eps,
+                           d.rope_theta, 64, 2, 4, 256, 8)
+    h = ctypes.c_void_p()
+    assert spec._lib.spec_model_create_kv(ctypes.byref(cfg), 2, ctypes.byref(h)) == 1 and not h.value
+    assert spec._lib.spec_model_create_kv(None, 1, ctypes.byref(h)) == 1
+    with pytest.raises(ValueError):
+        spec.SpecModel(d, max_batch=2, max_width=4, max_seq_len=256, num_pages=8, kv_format="int3")
