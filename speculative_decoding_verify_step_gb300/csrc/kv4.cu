@@ -18,10 +18,10 @@ namespace {
 
 // Physical slot of flat row r; -1: no slot given, position past the page table, or a
 // page outside the pool; -2: a row of no sequence.
-SPEC_DEVICE_INLINE long long kv4_slot(const Kv4Rows& a, int r) {
+SPEC_DEVICE_INLINE int kv4_slot(const Kv4Rows& a, int r) {
   if (a.row_slot) {
     const int s = a.row_slot[r];
-    return s >= 0 && s < (long long)a.num_pages * kPage ? s : -1;
+    return s >= 0 && s < a.num_pages * kPage ? s : -1;
   }
   int b, j;
   if (a.row_off) {
@@ -41,95 +41,249 @@ SPEC_DEVICE_INLINE long long kv4_slot(const Kv4Rows& a, int r) {
   const long long t = (long long)a.start[b] + j;
   if (t < 0 || t >= (long long)a.max_pages * kPage) return -1;
   const int pg = a.page_table[(long long)b * a.max_pages + (int)(t / kPage)];
-  if (pg < 0 || pg >= a.num_pages) return -1;
-  return (long long)pg * kPage + (int)(t % kPage);
+  return pg >= 0 && pg < a.num_pages ? pg * kPage + (int)(t % kPage) : -1;
 }
 
-// Codes of the 8 values of this thread; LANES neighbouring threads hold the token's
-// vector.  Returns the 8 codes as one word (value i in nibble i) and the parameters.
-template <int LANES>
-SPEC_DEVICE_INLINE uint32_t kv4_quantise(const float (&x)[8], uint32_t& par) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-#pragma unroll
-  for (int o = LANES / 2; o > 0; o >>= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
+// Offset m, scale s and the factor of the quotients of a vector with the given extremes.
+// The code of x is floor((x - m) / s + 1/2): the sum (x - m) * inv + 1.5 * 2^23 rounds to
+// the nearest whole number in the float's last bits.  inv is 1/s raised by 2^-20 of
+// itself, so an exact half (about one value in a thousand: x, m and s have 11 bits)
+// always goes up, whichever way 1/s was rounded.
+SPEC_DEVICE_INLINE uint32_t kv4_params(float lo, float hi, float& m, float& inv) {
   const __half mh = kv4_half_down(lo);
-  const float m = __half2float(mh);
+  m = __half2float(mh);
   const __half sh = kv4_half_up(__fdiv_rn(__fsub_rn(hi, m), 15.f));
   const float s = __half2float(sh);
-  // (x - m) / s + 1/2, floored: the sum (x - m) * inv + 1.5 * 2^23 rounds to the
-  // nearest whole number in the float's last bits.  inv is 1/s raised by 2^-20 of
-  // itself, so an exact half (about one value in a thousand: x, m and s have 11
-  // bits) always goes up, whichever way 1/s was rounded.
-  const float inv = s > 0.f ? __fmul_rn(__frcp_rn(s), 1.f + 9.5367431640625e-7f) : 0.f;
+  inv = s > 0.f ? __fmul_rn(__frcp_rn(s), 1.f + 9.5367431640625e-7f) : 0.f;
+  return ((uint32_t)__half_as_ushort(sh) << 16) | __half_as_ushort(mh);
+}
+
+// Codes of eight values, value i in nibble i.  The float's bits are 0x4b400000 + c; they are
+// added up shifted and the constants' sum taken off once.
+SPEC_DEVICE_INLINE uint32_t kv4_codes(const float (&x)[8], float m, float inv) {
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = __fmaf_rn(__fsub_rn(x[i], m), inv, 12582912.f);
-    w |= (__float_as_uint(t) & 15u) << (4 * i);
+  for (int i = 7; i >= 0; --i)
+    w = (w << 4) + __float_as_uint(__fmaf_rn(__fsub_rn(x[i], m), inv, 12582912.f));
+  return w - 0x4b400000u * 0x11111111u;
+}
+
+// Eight of the caller's values: saturated in their own type (fp16 at once; bf16 to +-65536,
+// its next numbers beyond, so NaN and infinities are gone) ...
+template <bool BF16>
+SPEC_DEVICE_INLINE void kv4_clamp(uint32_t (&w)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (BF16) {
+      __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162*>(&w[i]);
+      v = __hmin2(__hmax2(v, __float2bfloat162_rn(-65536.f)), __float2bfloat162_rn(65536.f));
+      w[i] = *reinterpret_cast<uint32_t*>(&v);
+    } else {
+      __half2 v = *reinterpret_cast<__half2*>(&w[i]);
+      v = __hmin2(__hmax2(v, __float2half2_rn(-65504.f)), __float2half2_rn(65504.f));
+      w[i] = *reinterpret_cast<uint32_t*>(&v);
+    }
   }
-  par = ((uint32_t)__half_as_ushort(sh) << 16) | __half_as_ushort(mh);
-  return w;
+}
+// ... their minimum (low half) and negated maximum (high half) over LANES neighbouring
+// lanes ...
+template <bool BF16>
+SPEC_DEVICE_INLINE uint32_t kv4_min2(uint32_t a, uint32_t b) {
+  if (BF16) {
+    __nv_bfloat162 v = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  __half2 v = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+template <bool BF16, int LANES>
+SPEC_DEVICE_INLINE uint32_t kv4_extremes(const uint32_t (&w)[4]) {
+  uint32_t lo = kv4_min2<BF16>(kv4_min2<BF16>(w[0], w[1]), kv4_min2<BF16>(w[2], w[3]));
+  uint32_t hi = kv4_min2<BF16>(kv4_min2<BF16>(w[0] ^ 0x80008000u, w[1] ^ 0x80008000u),
+                               kv4_min2<BF16>(w[2] ^ 0x80008000u, w[3] ^ 0x80008000u));
+  uint32_t r = kv4_min2<BF16>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) r = kv4_min2<BF16>(r, __shfl_xor_sync(0xffffffffu, r, o));
+  return r;
+}
+// ... and as fp32.
+template <bool BF16>
+SPEC_DEVICE_INLINE void kv4_floats(const uint32_t (&w)[4], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = kv4_unpack2<BF16>(w[i]);
+    x[2 * i] = BF16 ? kv4_sat(f.x) : f.x;
+    x[2 * i + 1] = BF16 ? kv4_sat(f.y) : f.y;
+  }
 }
 
-// Store a thread's codes and its token's parameters in the token's cell.
-template <int HD>
-SPEC_DEVICE_INLINE void kv4_store(uint8_t* block, int t, int j8, const uint32_t (&code)[2], const uint32_t (&par)[2]) {
-  reinterpret_cast<uint32_t*>(block + t * (HD / 2))[j8] = code[0];
-  uint8_t* v = block + kPage * HD / 2;
-  *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) = (uint16_t)code[1];
-  *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) = (uint16_t)(code[1] >> 16);
-  if (j8 < 2) reinterpret_cast<uint32_t*>(block + kPage * HD)[j8 * kPage + t] = j8 ? par[1] : par[0];
-}
-
-// One token and kv head per hd / 8 threads, eight dims of K and of V each.  The
-// warp's tokens are neighbouring rows of one head, so a token pair's V pieces meet
-// in one 128-byte row of the block.
-template <int HD, bool BF16>
+// Both kernels: grid (chunks of 8 RPW rows, kv heads); a warp takes RPW <= 16 consecutive
+// rows of one head, 32 / (hd / 8) of them at a time with eight dims per lane.  Lane (kv,
+// row) -- the upper half of the warp for V -- looks after one row's slot and parameters,
+// so a row's address chain and its division are paid once and in parallel for all 16.  A V
+// piece is two bytes, next to the same dims of the neighbouring token: where a pair of rows
+// fills a pair of cells, the lanes of the two rows exchange halves and move whole words.
+//
+// What bounds them: HBM for many rows.  262144 rows of 8 heads (head_dim 128) are read in
+// 207 us, 0.97 of the measured copy rate over 1.36 GB; a write of 65536 rows and their
+// reading back take 120 us, 0.84 of it.  (One row per half-warp, with every address and
+// division computed by all of its lanes and int-to-float conversions, took 282 and 188: the
+// special-function and integer pipes were the limit.)  For few rows it is the latency of
+// one warp's chain, so a warp then takes one step of rows only.
+template <int HD, bool BF16, int RPW>
 __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
-  constexpr int kLanes = HD / 8;
-  constexpr int kTok = 32 / kLanes;  // tokens of a warp
+  constexpr int L = HD / 8;                 // lanes of a row
+  constexpr int T = 32 / L;                 // rows at a time
+  constexpr int IT = RPW / T;
   pdl_wait();
   pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long wid = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const int h = (int)(wid % p.Hkv);
-  const long long r = wid / p.Hkv * kTok + lane / kLanes;
-  const int j8 = lane % kLanes;
-  const bool in = r < p.rows.total_rows;
-  const long long slot = in ? kv4_slot(p.rows, (int)r) : -1;
-  uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-  if (slot >= 0) {
-    const long long blk = r / p.row_blk, rr = r % p.row_blk;
-    const long long at = blk * p.blk_stride + h * p.head_stride + j8 * 8;
-    kw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k) + at + rr * p.k_row_stride);
-    vw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + at + rr * p.v_row_stride);
+  const int lane = threadIdx.x & 31, h = blockIdx.y, j8 = lane % L;
+  const int r0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * RPW;
+  const int n = p.rows.total_rows - r0;     // rows from r0 on
+  if (n <= 0) return;
+  uint32_t w[2][IT][4];
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int tok = it * T + lane / L;
+    const int r = r0 + min(tok, n - 1);
+    const long long at = (long long)(r / p.row_blk) * p.blk_stride + (long long)h * p.head_stride + j8 * 8;
+    const int rr = r % p.row_blk;
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.k) + at + rr * p.k_row_stride));
+    const uint4 b = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.v) + at + rr * p.v_row_stride));
+    w[0][it][0] = a.x, w[0][it][1] = a.y, w[0][it][2] = a.z, w[0][it][3] = a.w;
+    w[1][it][0] = b.x, w[1][it][1] = b.y, w[1][it][2] = b.z, w[1][it][3] = b.w;
   }
-  uint32_t code[2], par[2];
+  const int my_row = lane & 15, my_kv = lane >> 4;
+  const int my_slot = my_row < min(n, RPW) ? kv4_slot(p.rows, r0 + my_row) : -1;
+  uint32_t mine = 0;                        // extremes of this lane's row
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 w = i ? vw : kw;
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    float x[8];
+  for (int it = 0; it < IT; ++it) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 f = kv4_unpack2<BF16>(ws[e]);
-      x[2 * e] = kv4_sat(f.x);
-      x[2 * e + 1] = kv4_sat(f.y);
+    for (int kv = 0; kv < 2; ++kv) {
+      kv4_clamp<BF16>(w[kv][it]);
+      const uint32_t e = __shfl_sync(0xffffffffu, kv4_extremes<BF16, L>(w[kv][it]), my_row % T * L);
+      if (my_row / T == it && my_kv == kv) mine = e;
     }
-    code[i] = kv4_quantise<kLanes>(x, par[i]);
   }
-  if (slot < 0) return;
-  uint8_t* block = p.pool + ((slot / kPage) * p.Hkv + h) * (long long)kv4_block_bytes(HD);
-  const int t = (int)(slot % kPage);
-  kv4_store<HD>(block, t, j8, code, par);
+  const float2 ext = kv4_unpack2<BF16>(mine);
+  float m, inv;
+  const uint32_t par = kv4_params(BF16 ? kv4_sat(ext.x) : ext.x, BF16 ? kv4_sat(-ext.y) : -ext.y, m, inv);
+  constexpr int kBlock = kv4_block_bytes(HD);
+  if (my_slot >= 0)
+    reinterpret_cast<uint32_t*>(p.pool + ((long long)(my_slot / kPage) * p.Hkv + h) * kBlock + kPage * HD)[
+        my_kv * kPage + my_slot % kPage] = par;
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int tok = it * T + lane / L;
+    const int slot = __shfl_sync(0xffffffffu, my_slot, tok), other_slot = __shfl_sync(0xffffffffu, my_slot, tok ^ 1);
+    uint32_t code[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const float tm = __shfl_sync(0xffffffffu, m, kv * 16 + tok), ti = __shfl_sync(0xffffffffu, inv, kv * 16 + tok);
+      float x[8];
+      kv4_floats<BF16>(w[kv][it], x);
+      code[kv] = kv4_codes(x, tm, ti);
+    }
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, code[1], L);
+    if (slot < 0) continue;
+    uint8_t* block = p.pool + ((long long)(slot / kPage) * p.Hkv + h) * kBlock;
+    const int t = slot % kPage;
+    reinterpret_cast<uint32_t*>(block + t * (HD / 2))[j8] = code[0];
+    uint8_t* v = block + kPage * HD / 2;
+    if (other_slot == (slot ^ 1) && (tok & 1) == (slot & 1)) {
+      // the even row stores dims 0..3 of both, the odd one dims 4..7
+      const int odd = tok & 1;
+      *reinterpret_cast<uint32_t*>(v + kv4_v_piece<HD>(t & ~1, j8 * 8 + 4 * odd)) =
+          odd ? __byte_perm(other, code[1], 0x7632) : __byte_perm(code[1], other, 0x5410);
+    } else {
+      *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) = (uint16_t)code[1];
+      *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) = (uint16_t)(code[1] >> 16);
+    }
+  }
+}
+
+// s * c + m of eight codes, rounded once to the caller's type.  fp16: a nibble OR-ed under
+// 0x6400 (or 0x5400, one nibble up) is the number 1024 + c (64 + c), so a subtraction gives
+// c exactly and one fused multiply-add the result.  `sat`: 15 s + m may pass 65504 (by at most
+// 16: s is rounded up); the result is then held to it.
+template <bool BF16>
+SPEC_DEVICE_INLINE uint4 kv4_expand8(uint32_t code, uint32_t par, bool sat) {
+  uint32_t o[4];
+  if (BF16) {
+    const float2 ms = __half22float2(*reinterpret_cast<const __half2*>(&par));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = kv4_pack2<true>(__fmaf_rn((float)((code >> (8 * i)) & 15u), ms.y, ms.x),
+                             __fmaf_rn((float)((code >> (8 * i + 4)) & 15u), ms.y, ms.x));
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  const uint32_t m2 = __byte_perm(par, par, 0x1010), s2 = __byte_perm(par, par, 0x3232);
+  const uint32_t hi = code >> 8;
+  const uint32_t raw[4] = {(code & 0x000f000fu) | 0x64006400u, (code & 0x00f000f0u) | 0x54005400u,
+                           (hi & 0x000f000fu) | 0x64006400u, (hi & 0x00f000f0u) | 0x54005400u};
+  uint32_t v[4];                            // (0, 4) (1, 5) (2, 6) (3, 7)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&raw[i]), __float2half2_rn(i & 1 ? 64.f : 1024.f));
+    __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&s2), *reinterpret_cast<const __half2*>(&m2));
+    if (sat) r = __hmin2(r, __float2half2_rn(65504.f));
+    v[i] = *reinterpret_cast<uint32_t*>(&r);
+  }
+  return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                    __byte_perm(v[2], v[3], 0x7632));
+}
+
+template <int HD, bool BF16, int RPW>
+__global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
+  constexpr int L = HD / 8;
+  constexpr int T = 32 / L;
+  constexpr int IT = RPW / T;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, h = blockIdx.y, j8 = lane % L;
+  const int r0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * RPW;
+  const int n = p.rows.total_rows - r0;
+  if (n <= 0) return;
+  const int my_row = lane & 15, my_kv = lane >> 4;
+  const int my_slot = my_row < min(n, RPW) ? kv4_slot(p.rows, r0 + my_row) : -2;
+  constexpr int kBlock = kv4_block_bytes(HD);
+  uint32_t par = 0;                         // a position without a page reads as zeros
+  if (my_slot >= 0)
+    par = reinterpret_cast<const uint32_t*>(p.pool + ((long long)(my_slot / kPage) * p.Hkv + h) * kBlock + kPage * HD)[
+        my_kv * kPage + my_slot % kPage];
+  uint32_t kc[IT], vc[IT];
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int tok = it * T + lane / L, odd = tok & 1;
+    const int slot = __shfl_sync(0xffffffffu, my_slot, tok), other_slot = __shfl_sync(0xffffffffu, my_slot, tok ^ 1);
+    kc[it] = vc[it] = 0;
+    if (slot < 0) continue;
+    const uint8_t* block = p.pool + ((long long)(slot / kPage) * p.Hkv + h) * kBlock;
+    const int t = slot % kPage;
+    kc[it] = reinterpret_cast<const uint32_t*>(block + t * (HD / 2))[j8];
+    const uint8_t* v = block + kPage * HD / 2;
+    if (other_slot == (slot ^ 1) && odd == (slot & 1))
+      vc[it] = *reinterpret_cast<const uint32_t*>(v + kv4_v_piece<HD>(t & ~1, j8 * 8 + 4 * odd));  // both rows' dims
+    else
+      vc[it] = *reinterpret_cast<const uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) |
+               ((uint32_t)*reinterpret_cast<const uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) << 16);
+  }
+  const float2 ms = __half22float2(*reinterpret_cast<const __half2*>(&par));
+  const bool sat = __any_sync(0xffffffffu, fmaf(15.f, ms.y, ms.x) > 65504.f);
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int tok = it * T + lane / L, odd = tok & 1;
+    const int slot = __shfl_sync(0xffffffffu, my_slot, tok), other_slot = __shfl_sync(0xffffffffu, my_slot, tok ^ 1);
+    const uint32_t kp = __shfl_sync(0xffffffffu, par, tok), vp = __shfl_sync(0xffffffffu, par, 16 + tok);
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, vc[it], L);
+    uint32_t v = vc[it];
+    if (slot >= 0 && other_slot == (slot ^ 1) && odd == (slot & 1))
+      v = odd ? __byte_perm(other, v, 0x7632) : __byte_perm(v, other, 0x5410);
+    if (slot == -2) continue;               // past the last row, or a row of no sequence
+    const long long at = ((long long)(r0 + tok) * p.Hkv + h) * L + j8;
+    __stcs(reinterpret_cast<uint4*>(p.k) + at, kv4_expand8<BF16>(kc[it], kp, sat));
+    __stcs(reinterpret_cast<uint4*>(p.v) + at, kv4_expand8<BF16>(v, vp, sat));
+  }
 }
 
 // Pseudo-random cells.  grid (pages, n_layers, n); each block fills one page of one layer.
@@ -149,84 +303,59 @@ __global__ void kv4_fill_kernel(uint8_t* pool, long long layer_bytes, const int3
   for (int e = threadIdx.x / kLanes; e < Hkv * kPage; e += blockDim.x / kLanes) {
     const int h = e / kPage, t = e % kPage;
     const long long base = ((((long long)layer * num_pages + pg) * Hkv + h) * kPage + t) * HD + j8 * 8;
-    float x[2][8];
+    uint8_t* block = pool + layer * layer_bytes + ((long long)pg * Hkv + h) * kv4_block_bytes(HD);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint64_t w = splitmix64(seed ^ (uint64_t)(base + i) * 0x2545F4914F6CDD1Dull);
-      x[0][i] = ((float)(uint32_t)(w & 0xffffffu) * (1.0f / 16777216.0f) * 2.f - 1.f) * scale;
-      x[1][i] = ((float)(uint32_t)((w >> 32) & 0xffffffu) * (1.0f / 16777216.0f) * 2.f - 1.f) * scale;
+    for (int kv = 0; kv < 2; ++kv) {
+      float x[8];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) x[kv][i] = __half2float(to_act(x[kv][i]));
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t w = splitmix64(seed ^ (uint64_t)(base + i) * 0x2545F4914F6CDD1Dull) >> (32 * kv);
+        x[i] = ((float)(uint32_t)(w & 0xffffffu) * (1.0f / 16777216.0f) * 2.f - 1.f) * scale;
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __half2 v = __halves2half2(to_act(x[2 * i]), to_act(x[2 * i + 1]));
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      const float2 ext = kv4_unpack2<false>(kv4_extremes<false, kLanes>(w));
+      kv4_floats<false>(w, x);
+      float m, inv;
+      const uint32_t par = kv4_params(ext.x, -ext.y, m, inv);
+      const uint32_t code = kv4_codes(x, m, inv);
+      if (j8 == 0) reinterpret_cast<uint32_t*>(block + kPage * HD)[kv * kPage + t] = par;
+      if (kv == 0) {
+        reinterpret_cast<uint32_t*>(block + t * (HD / 2))[j8] = code;
+      } else {
+        uint8_t* v = block + kPage * HD / 2;
+        *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) = (uint16_t)code;
+        *reinterpret_cast<uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) = (uint16_t)(code >> 16);
+      }
     }
-    uint32_t code[2], par[2];
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) code[kv] = kv4_quantise<kLanes>(x[kv], par[kv]);
-    kv4_store<HD>(pool + layer * layer_bytes + ((long long)pg * Hkv + h) * kv4_block_bytes(HD), t, j8, code, par);
   }
 }
 
-// Two fp32 to fp16, finite: s is rounded up, so 15 s + m can pass 65504 by 16.
-SPEC_DEVICE_INLINE uint32_t pack_f16x2_sat(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
+template <typename P, typename K>
+cudaError_t launch_rows(K kernel, int rows_per_warp, const P& p, cudaStream_t st) {
+  const unsigned chunks = (unsigned)(((long long)p.rows.total_rows + 8 * rows_per_warp - 1) / (8 * rows_per_warp));
+  return launch_k(kernel, dim3(chunks, p.Hkv), dim3(256), 0, st, p);
 }
 
-// s * c + m of eight codes, rounded once to the caller's type.
-template <bool BF16>
-SPEC_DEVICE_INLINE uint4 kv4_expand8(uint32_t code, uint32_t par) {
-  const float m = __half2float(__ushort_as_half((unsigned short)(par & 0xffffu)));
-  const float s = __half2float(__ushort_as_half((unsigned short)(par >> 16)));
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = __fmaf_rn((float)((code >> (8 * i)) & 15u), s, m);
-    const float hi = __fmaf_rn((float)((code >> (8 * i + 4)) & 15u), s, m);
-    w[i] = BF16 ? kv4_pack2<true>(lo, hi) : pack_f16x2_sat(lo, hi);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+// One step of rows per warp while all warps are resident at once (64 on each of 152 SMs): measured
+// (8 heads of 128, a write and its reading back) 80 rows 4.5 against 9.0 us.
+bool few_rows(const Kv4Rows& r, int Hkv, int hd) { return (long long)r.total_rows * Hkv <= 152ll * 64 * (256 / hd); }
 
 template <int HD, bool BF16>
-__global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ Kv4ReadParams p) {
-  constexpr int kLanes = HD / 8;
-  constexpr int kTok = 32 / kLanes;
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long wid = (long long)blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5);
-  const int h = (int)(wid % p.Hkv);
-  const long long r = wid / p.Hkv * kTok + lane / kLanes;
-  const int j8 = lane % kLanes;
-  if (r >= p.rows.total_rows) return;
-  const long long slot = kv4_slot(p.rows, (int)r);
-  if (slot == -2) return;
-  uint32_t kc = 0, vc = 0, kp = 0, vp = 0;  // a position without a page reads as zeros
-  if (slot >= 0) {
-    const uint8_t* block = p.pool + ((slot / kPage) * p.Hkv + h) * (long long)kv4_block_bytes(HD);
-    const int t = (int)(slot % kPage);
-    kc = reinterpret_cast<const uint32_t*>(block + t * (HD / 2))[j8];
-    const uint8_t* v = block + kPage * HD / 2;
-    vc = *reinterpret_cast<const uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) |
-         ((uint32_t)*reinterpret_cast<const uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) << 16);
-    const uint32_t* par = reinterpret_cast<const uint32_t*>(block + kPage * HD);
-    kp = par[t];
-    vp = par[kPage + t];
-  }
-  const long long at = (r * p.Hkv + h) * kLanes + j8;
-  reinterpret_cast<uint4*>(p.k)[at] = kv4_expand8<BF16>(kc, kp);
-  reinterpret_cast<uint4*>(p.v)[at] = kv4_expand8<BF16>(vc, vp);
+cudaError_t launch_write(const Kv4WriteParams& p, cudaStream_t st) {
+  constexpr int kStep = 256 / HD;
+  return few_rows(p.rows, p.Hkv, HD) ? launch_rows(kv4_write_kernel<HD, BF16, kStep>, kStep, p, st)
+                                     : launch_rows(kv4_write_kernel<HD, BF16, 16>, 16, p, st);
 }
-
-// Blocks of 8 warps; a warp takes 256 / hd rows of one head.
-template <typename P, typename K>
-cudaError_t launch_rows(K kernel, const P& p, cudaStream_t st) {
-  const long long per = 256 / p.hd;
-  const long long warps = (p.rows.total_rows + per - 1) / per * p.Hkv;
-  if (warps == 0) return cudaSuccess;
-  const long long blocks = (warps + 7) / 8;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_k(kernel, dim3((unsigned)blocks), dim3(256), 0, st, p);
+template <int HD, bool BF16>
+cudaError_t launch_read(const Kv4ReadParams& p, cudaStream_t st) {
+  constexpr int kStep = 256 / HD;
+  return few_rows(p.rows, p.Hkv, HD) ? launch_rows(kv4_read_kernel<HD, BF16, kStep>, kStep, p, st)
+                                     : launch_rows(kv4_read_kernel<HD, BF16, 16>, 16, p, st);
 }
 
 }  // namespace
@@ -239,15 +368,15 @@ cudaError_t launch_kv4_fill_pages(uint8_t* pool, long long layer_bytes, const in
 }
 
 cudaError_t launch_kv4_write(const Kv4WriteParams& p, cudaStream_t st) {
-  if (p.hd == 128)
-    return p.bf16 ? launch_rows(kv4_write_kernel<128, true>, p, st) : launch_rows(kv4_write_kernel<128, false>, p, st);
-  return p.bf16 ? launch_rows(kv4_write_kernel<64, true>, p, st) : launch_rows(kv4_write_kernel<64, false>, p, st);
+  if (p.rows.total_rows == 0) return cudaSuccess;
+  if (p.hd == 128) return p.bf16 ? launch_write<128, true>(p, st) : launch_write<128, false>(p, st);
+  return p.bf16 ? launch_write<64, true>(p, st) : launch_write<64, false>(p, st);
 }
 
 cudaError_t launch_kv4_read(const Kv4ReadParams& p, cudaStream_t st) {
-  if (p.hd == 128)
-    return p.bf16 ? launch_rows(kv4_read_kernel<128, true>, p, st) : launch_rows(kv4_read_kernel<128, false>, p, st);
-  return p.bf16 ? launch_rows(kv4_read_kernel<64, true>, p, st) : launch_rows(kv4_read_kernel<64, false>, p, st);
+  if (p.rows.total_rows == 0) return cudaSuccess;
+  if (p.hd == 128) return p.bf16 ? launch_read<128, true>(p, st) : launch_read<128, false>(p, st);
+  return p.bf16 ? launch_read<64, true>(p, st) : launch_read<64, false>(p, st);
 }
 
 }  // namespace spec

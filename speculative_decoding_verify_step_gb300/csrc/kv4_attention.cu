@@ -266,7 +266,7 @@ struct Cfg {
   static constexpr int kTeams = kWarps / TW;
   static constexpr int kBlock = kPage * HD + 2 * kPage * 4;    // bytes of a page of one kv head: a stage
   // CTAs per SM by the registers of a warp
-  static constexpr int kRegs = NT * (HD / 4 / TW + 8 + 16 / TW) + (TW == 1 ? 90 : 70);
+  static constexpr int kRegs = NT * (HD / 4 / TW + 8 + 16 / TW) + (TW == 1 ? 90 : 68);
   static constexpr int kCtas = kRegs <= 128 ? 4 : kRegs <= 168 ? 3 : 2;
   static constexpr int kQ = NT * (HD / 32) * 512;              // query fragments
   static constexpr int kP = TW == 1 ? 0 : 2 * NT * 1024;       // weights of two pages
