@@ -384,12 +384,13 @@ spec_status spec_kv4_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
  * kv_len[b] + 1, ...; row j sees positions < kv_len[b] and the window rows that are
  * its ancestors (parent_host: HOST [W] as in spec_verify_tree_step, or NULL: the
  * chain 0..j).  W = 1 is the decode step.  Query head h reads kv head
- * h / (n_heads / n_kv_heads); scores are scale * (q . k), softmax in fp32, one
- * rounding of the result (weights are fp16 with fp32 accumulation).  A row that sees
- * nothing is zeros.  Rows of a sequence beyond W are left as they are.
+ * h / (n_heads / n_kv_heads); q's values are saturated like x above, scores are
+ * scale * (q . k) with |scale| <= 2^40, softmax in fp32, one rounding of the result
+ * (weights are fp16 with fp32 accumulation).  out may be q.  A row that sees nothing is
+ * zeros.  Rows of a sequence beyond W are left as they are.
  * W * (n_heads / n_kv_heads) <= 64.  max_kv_len: an upper bound of kv_len for the
  * launch shape, 0: unknown (results do not depend on it beyond the order of the
- * sums).  workspace: device memory of spec_kv4_attention_workspace() bytes for the same
+ * sums, not even where it is too small).  workspace: device memory of spec_kv4_attention_workspace() bytes for the same
  * arguments (0: none needed, may be NULL; -1: a shape the call refuses), 16-byte aligned,
  * for the partial results of sequences that several SMs share; it holds nothing between
  * calls, and calls that may overlap need one each.  A device-side wait that runs out (about

@@ -1568,7 +1568,7 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
     return fail(SPEC_ERR_UNSUPPORTED, "width * group size must be <= 64 (%d * %d)", W, n_heads / n_kv_heads);
   if ((long long)B * n_kv_heads * max_pages > (1 << 30))
     return fail(SPEC_ERR_UNSUPPORTED, "B * n_kv_heads * max_pages must be at most 2^30");
-  if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID_ARG, "scale is not finite");
+  if (!(std::fabs(scale) <= 1099511627776.f)) return fail(SPEC_ERR_INVALID_ARG, "|scale| must be at most 2^40");
   if (max_kv_len < 0) return fail(SPEC_ERR_INVALID_ARG, "max_kv_len is negative");
   int depth[16];
   uint32_t anc[16];

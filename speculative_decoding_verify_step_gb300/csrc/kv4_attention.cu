@@ -43,9 +43,9 @@
 // team of four keeps a warp's accumulators small (8 registers per 8 rows, against 32),
 // so wide windows fit, and has a page's result sooner; one warp needs no barriers.
 // Measured (head_dim 128, 8 kv heads): one row tile, 2 x 65520 tokens 35 against 43 us;
-// two, 8 x 32768 tokens 78 against 88; three, 64 x 512-2048 tokens 69 against 66.  In a
-// team the scores of the next page are computed before the barrier that releases this
-// page's weights: one barrier per page.
+// two, 8 x 32768 tokens 78 against 88; three, 64 x 512-2048 tokens 67 against 64 (8 x 32768
+// tokens 112 against 116).  In a team the scores of the next page are computed before the
+// barrier that releases this page's weights: one barrier per page.
 //
 // What bounds it.  mma.sync runs at 8 cycles per m16n8k16 and SM quarter here and shares
 // its pipe with the fp32 instructions; AND and shift take 2 cycles, exp2 and movmatrix 4
@@ -54,7 +54,10 @@
 // 390.  The pipes overlap little at two warps per SM quarter, so 16 rows run at about
 // 600 cycles a page and 8 rows at about 400, next to the memory's rate.  (More CTAs per
 // SM with spilled registers, half pages, and packed fp32 pairs -- 3 cycles each -- were
-// all slower.)
+// all slower.)  The wide windows were also built on tcgen05, codes unpacked into shared
+// memory, S and O in tensor memory: with a token per thread a score costs twice the
+// instructions, and the phases between its two barriers per tile do not overlap; 24 rows
+// of 8 x 32768 tokens took 246 against 116 us, 60 rows 364 against 306.
 //
 // The running maximum moves only when a score passes it by more than 2^8: the
 // barrier (or vote) carries that question, and the exchange of maxima and the
@@ -404,11 +407,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
 
   // Queries: each row is scaled by a power of two (largest element in [2^14, 2^15)),
   // so the factor 1/16 of the odd columns costs no precision; the sum of the scaled
-  // row and the factor back to exp2 units are kept per row.  One warp per row, four
-  // rows at a time.
+  // row and the factor back to exp2 units are kept per row.  One warp per row, up to
+  // eight rows at a time: their loads and reductions overlap.
   {
     constexpr int PER = HD / 32;  // elements of a lane
-    constexpr int RB = NT == 1 ? 2 : 4;
+    constexpr int RB = NT <= 4 ? NT * 2 : 8;
     for (int r0 = warp; r0 < ROWS; r0 += RB * kWarps) {
       uint32_t raw[RB][PER / 2];
 #pragma unroll
@@ -446,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
       int sh[RB];
 #pragma unroll
       for (int k = 0; k < RB; ++k) {
-        // 2^sh with 2^14 <= mx 2^sh < 2^15; rows below 2^-40 count as zeros
-        sh[k] = mx[k] > 9.1e-13f ? 14 - (int)((__float_as_uint(mx[k]) >> 23) - 127u) : 0;
+        // 2^sh with 2^14 <= mx 2^sh < 2^15; rows below 2^-112 count as zeros (|scale| <= 2^40)
+        sh[k] = mx[k] > 1.9259299e-34f ? 14 - (int)((__float_as_uint(mx[k]) >> 23) - 127u) : 0;
         const float up = __uint_as_float((uint32_t)(127 + sh[k]) << 23);
         sum[k] = 0.f;
 #pragma unroll
@@ -1032,7 +1035,7 @@ int hint_pages(const Kv4AttnParams& p) { return (p.kv_len_hint + kPage - 1) / kP
 
 // Short caches: the CTAs of a group as one cluster, where all clusters fit the GPU at once (14 of
 // 16 CTAs, 36 of 8, 74 of 4 and 152 of 2 do with two CTAs per SM) and a CTA gets four pages at
-// most.  No workspace and no second launch: 7.0 against 8.2 us at 1024 tokens, one sequence of 8
+// most.  No workspace and no second launch: 6.5 against 8.2 us at 1024 tokens, one sequence of 8
 // kv heads.  0: not short.
 int cluster_size(int B, int Hkv, int pages) {
   const long long groups = (long long)B * Hkv;
@@ -1073,7 +1076,8 @@ cudaError_t launch_pieces(Kv4AttnParams p, cudaStream_t st) {
   const int occ = (int)std::min<long long>(C::kCtas, (std::max(most, groups) + p.sm_count - 1) / p.sm_count);
   p.slots = occ * p.sm_count;
   p.stages = C::stages(occ);
-  const long long ctas = groups < p.slots ? std::min<long long>(p.slots, groups * pages) : groups + p.slots;
+  // as many CTAs as the plan can make of any lengths: the hint sets the speed, not the result
+  const long long ctas = groups < p.slots ? p.slots : groups + p.slots;
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
   e = launch_k(kv4_attention_kernel<HD, NT, TW, false>, dim3((unsigned)ctas), dim3(kThreads),
                C::kFixed + p.stages * C::kBlock, st, p);

@@ -586,6 +586,8 @@ def spec_kv4_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
     Hq = q.shape[-2]
     if ragged:
         W = max_width if max_width is not None else max(1, min(16, 64 // max(1, Hq // H)))
+        if not 1 <= W <= 16:
+            raise ValueError(f"max_width {W} outside 1..16")
     elif max_width is not None and max_width < W:
         raise ValueError(f"q has {W} rows per sequence, more than max_width {max_width}")
     par = None

@@ -323,6 +323,86 @@ def test_scale(scale):
     check(got[0], *rows_ref(np64(q[0]), held[0], 146, scale=scale))
 
 
+def test_tiny_queries_under_a_large_scale():
+    """Scores of order one from queries of order 1e-13: such rows are not zeros."""
+    spec = spec_()
+    c = Cache([150], 2, 128)
+    held = c.fill(18)
+    q = (1e-13 * torch.randn(1, 2, 4, 128, generator=torch.Generator().manual_seed(1))).bfloat16()
+    got = spec.spec_kv4_attention(q.cuda(), c.pool, torch.tensor([148], dtype=torch.int32, device="cuda"), c.table, scale=2.0 ** 40)
+    check(got[0], *rows_ref(np64(q[0]), held[0], 148, scale=2.0 ** 40, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_queries_that_are_not_numbers_are_saturated(dtype):
+    """Each such element outweighs the rest of its row, so the row's weight sits on one token."""
+    spec = spec_()
+    c = Cache([90], 1, 64)
+    held = c.fill(19)
+    q = torch.randn(1, 4, 1, 64, generator=torch.Generator().manual_seed(2)).to(dtype)
+    for j, x in enumerate(("inf", "-inf", "nan")):
+        q[0, j, 0, 3 * j] = float(x)
+    got = spec.spec_kv4_attention(q.cuda(), c.pool, torch.tensor([86], dtype=torch.int32, device="cuda"), c.table)
+    check(got[0], *rows_ref(O.saturate(np64(q[0])), held[0], 86, dtype=dtype))
+
+
+@pytest.mark.parametrize("lens,W,grp", [([20000], 1, 4), ([9000, 20000, 5], 4, 4), ([12000], 12, 4)])
+def test_a_length_bound_that_is_too_small(lens, W, grp):
+    """max_kv_len sets the launch shape only: all pages are attended to whatever it says."""
+    spec = spec_()
+    Hkv, hd = 2, 128
+    c = Cache([n + W for n in lens], Hkv, hd, seed=W)
+    held = c.fill(20)
+    q = torch.randn(len(lens), W, Hkv * grp, hd, generator=torch.Generator().manual_seed(W)).half()
+    kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for hint in (1, 64, 300, 700, 2000, 6000):
+        got = spec.spec_kv4_attention(q.cuda(), c.pool, kv_len, c.table, max_kv_len=hint)
+        for b, n in enumerate(lens):
+            check(got[b], *rows_ref(np64(q[b]), held[b], n))
+
+
+def test_out_may_be_q():
+    spec = spec_()
+    for lens in ([200, 3], [30000, 64]):
+        c = Cache([n + 4 for n in lens], 2, 128)
+        c.fill(21)
+        kv_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        q = torch.randn(2, 4, 8, 128).half().cuda()
+        want = spec.spec_kv4_attention(q, c.pool, kv_len, c.table)
+        assert spec.spec_kv4_attention(q, c.pool, kv_len, c.table, out=q) is q
+        assert torch.equal(q, want)
+
+
+def test_calls_at_once_on_streams_and_in_graphs():
+    """Eager calls on two streams and replays of two graphs, in flight together, over caches whose
+    sequences are shared by many CTAs: each gives the bits it gives alone."""
+    spec = spec_()
+    cases = []
+    for lens, W in (([9000, 30000], 2), ([20000], 5)):
+        c = Cache([n + W for n in lens], 2, 128, seed=W)
+        c.fill(22 + W)
+        q = torch.randn(len(lens), W, 8, 128, generator=torch.Generator().manual_seed(W)).half().cuda()
+        cases.append((q, c.pool, torch.tensor(lens, dtype=torch.int32, device="cuda"), c.table))
+    want = [spec.spec_kv4_attention(*a) for a in cases]
+    torch.cuda.synchronize()
+    graphs, outs = [], [torch.empty_like(a[0]) for a in cases]
+    for a, o in zip(cases, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            spec.spec_kv4_attention(*a, out=o)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = []
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got.append((i, spec.spec_kv4_attention(*cases[i])))
+            with torch.cuda.stream(streams[2 + i]):
+                graphs[i].replay()
+                got.append((i, outs[i].clone()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in got)
+
+
 def test_one_sequence_per_page_order_and_shared_pages():
     """Two sequences over the same pages (a shared prefix) see the same tokens."""
     spec = spec_()

@@ -110,7 +110,7 @@ def test_read_refusals(spec, kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(n=0, total=0), 1), (dict(n=17, total=34), 1), (dict(Hq=5), 1), (dict(Hq=0), 1), (dict(q=None), 1),
     (dict(out=None), 1), (dict(q=4104), 1), (dict(out=4104), 1), (dict(qs=248), 1), (dict(qs=260), 1),
-    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(hint=-1), 1), (dict(ws=None, max_pages=4096), 1), (dict(ws=4100, max_pages=4096), 1),
+    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(scale=1.2e12), 1), (dict(scale=-1.2e12), 1), (dict(hint=-1), 1), (dict(ws=None, max_pages=4096), 1), (dict(ws=4100, max_pages=4096), 1),
     (dict(n=9, total=18, Hq=16), 7),                                  # 9 rows x 8 heads of a group
     (dict(parent=(ctypes.c_int32 * 3)(0, 0, 1)), 1), (dict(parent=(ctypes.c_int32 * 3)(-1, 1, 0)), 1)])
 def test_attention_refusals(spec, kw, status):
