@@ -1605,10 +1605,13 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
   for (int j = 0; j < 16; ++j) p.anc[j] = j < W ? anc[j] : 0u;
   p.kv_len_hint = kv4_len_hint(max_pages, max_kv_len, W);
   const int group_rows = W * (n_heads / n_kv_heads);
-  if (kv4_attention_workspace(B, n_kv_heads, group_rows, head_dim, p.kv_len_hint, 1) > 0)
+  long long need = kv4_attention_workspace(B, n_kv_heads, group_rows, head_dim, p.kv_len_hint, 1);  // needed on any GPU
+  if (need > 0)
     if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
   CUDA_TRY(current_sm_count(&p.sm_count));
-  const long long need = kv4_attention_workspace(B, n_kv_heads, group_rows, head_dim, p.kv_len_hint, p.sm_count);
+  need = kv4_attention_workspace(B, n_kv_heads, group_rows, head_dim, p.kv_len_hint, p.sm_count);
+  if (need > 0)
+    if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
   if (workspace_bytes < need)
     return fail(SPEC_ERR_INVALID_ARG, "workspace_bytes=%lld, %lld needed", (long long)workspace_bytes, need);
   p.workspace = static_cast<float*>(workspace);

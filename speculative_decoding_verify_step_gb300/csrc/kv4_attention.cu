@@ -131,6 +131,13 @@ SPEC_DEVICE_INLINE void bulk_load(void* dst, const void* src, uint32_t bytes, ui
                : "memory");
 }
 
+// Bytes of this CTA's shared memory to another CTA of the cluster (shared::cluster addresses).
+SPEC_DEVICE_INLINE void bulk_push(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // Window geometry of sequence b, from the call's tables.
 struct Kv4Seq {
   int sid, row0, Wb, L, n_keys, pages;
@@ -181,14 +188,14 @@ SPEC_DEVICE_INLINE Kv4Plan kv4_plan(const Kv4AttnParams& p, const Kv4Seq& mine) 
   const int lane = threadIdx.x & 31;
   int n = mine.pages;
   for (int b = lane + 32; b < p.B; b += 32) n += kv4_seq(p, b).pages;
-  n = warp_sum(n) * p.Hkv;
+  n = (int)__reduce_add_sync(0xffffffffu, (unsigned)n) * p.Hkv;
   const int groups = p.B * p.Hkv;
   const int share = groups < p.slots ? p.slots - groups : p.slots;
   Kv4Plan r;
   r.target = max(1, (n + share - 1) / share);
   int k = kv4_pieces(mine.pages, r.target);
   for (int b = lane + 32; b < p.B; b += 32) k += kv4_pieces(kv4_seq(p, b).pages, r.target);
-  r.total = warp_sum(k) * p.Hkv;
+  r.total = (int)__reduce_add_sync(0xffffffffu, (unsigned)k) * p.Hkv;
   return r;
 }
 // The sequence that holds piece x (below the total; per sequence all pieces of head 0, then
@@ -275,12 +282,15 @@ struct Cfg {
   static constexpr int kP = TW == 1 ? 0 : 2 * NT * 1024;       // weights of two pages
   static constexpr int kFixed = kQ + kP;
   static constexpr int kStatic = NT * 8 * 4 * (5 + 2 * kWarps + kTeams) + 512;  // static shared memory, at most
+  static constexpr int kRec = HD + 4;                          // floats of a row's partial: O, maximum, sum
+  // A cluster's partials of this CTA's rows: cs ceil(rows / cs) records at most, cs up to 16.
+  static constexpr int kRecv = (NT + 1) / 2 * 16 * kRec * 4;
   // Ring depth with `ctas` CTAs on an SM: 228 KB, 1 KB of system use per CTA.  A multiple
   // of the teams, so that the pages of one stage are one team's, in order: a team that
   // waited for a stage's next page while another team's was still in flight would take
   // the phase before for its own.
-  static constexpr int stages(int ctas) {
-    const int n = (233472 / ctas - 1024 - kStatic - kFixed) / kBlock;
+  static constexpr int stages(int ctas, int other = 0) {
+    const int n = (233472 / ctas - 1024 - kStatic - kFixed - other) / kBlock;
     return (n < kMaxStages ? n : kMaxStages) / kTeams * kTeams;
   }
   static_assert(kCtas <= (NT <= 3 ? 4 : 3), "workspace");
@@ -288,6 +298,7 @@ struct Cfg {
   static_assert(TW == 1 || TW == kWarps, "a team is one warp or the CTA");
   static_assert(stages(kCtas) >= (TW == 1 ? 2 : 4) * kTeams, "ring");
   static_assert(kTeams * NT * 8 * HD * 4 <= stages(kCtas) * kBlock, "the teams' partials reuse the ring");
+  static_assert(TW == 1 || (stages(2, kRecv) >= 4 && NT * 8 * kRec * 4 <= stages(2, kRecv) * kBlock), "clusters");
 };
 
 // Query row r of the CTA is window row r / grp, head r % grp of the group.
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   __shared__ float4 s_row[ROWS / 2];          // rows 2i, 2i + 1: sums of q, factors to exp2 units
   __shared__ float2 s_max[TEAMS][ROWS / 2];   // running maxima
   __shared__ float s_red[kWarps][ROWS], s_red2[kWarps][ROWS];
-  __shared__ float s_m[CL ? ROWS : 1], s_l[CL ? ROWS : 1];
+  __shared__ uint64_t received;               // partials of the cluster's CTAs
   __shared__ uint32_t s_smax[kWarps];
   __shared__ uint32_t s_anc[16];
   __shared__ int s_fail;
@@ -324,9 +335,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   // the merge kernel reads the call's tables before its own wait, so it may only start
   // once they are complete
   if (!p.early) pdl_wait();
-  pdl_launch_dependents();
+  // Clusters let the next kernel in only as they end: its first CTAs would take places that
+  // its other clusters, if it has any, then lack (back to back, 32 clusters of 8 CTAs took 24
+  // against 17 us; let in after the loop, 22).
+  if (!CL) pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+    if (CL) mbar_init(&received, 1);
     s_fail = 0;
     fence_barrier_init();
   }
@@ -364,7 +379,15 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   const int L = seq.L, n_keys = seq.n_keys, Wb = seq.Wb, row0 = seq.row0, rows = seq.Wb * grp;
   const int key_base = pg0 * kPage;
   bool failed = false;
+  // a cluster's CTA finishes rows [own0, own0 + own)
+  const int share = CL ? (rows + pieces - 1) / pieces : 0;
+  const int own0 = share * piece, own = max(0, min(rows - own0, share));
   __syncthreads();
+  if (CL && pieces > 1) {
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&received, pieces * own * C::kRec * 4);
+    __syncwarp();
+    cluster_arrive();  // its barrier is ready to receive
+  }
 
   // Page numbers of the piece's pages [base, base + 32) and the 32 after them, one per
   // lane, and which of the first 32 are there.
@@ -390,100 +413,73 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     }
   };
   int issued = 0;
-  if (warp == 0) {
+  if (p.early) {
     // before pdl_wait only pages without window slots may be read
-    for (; issued < min(S, npg); ++issued) {
-      if (p.early && key_base + (issued + 1) * kPage > L) break;
-      issue(issued, issued);
-    }
+    if (warp == 0)
+      for (; issued < min(S, npg) && key_base + (issued + 1) * kPage <= L; ++issued) issue(issued, issued);
+    pdl_wait();
   }
-  if (p.early) pdl_wait();
+  // Queries: a lane takes eight dims of a row, two rows (head_dim 64: four) at a time per
+  // warp, all loads before the pages' (which they would queue behind).  Each row is scaled
+  // by a power of two (largest element in [2^14, 2^15)), so the factor 1/16 of the odd
+  // columns costs no precision; the sum of the scaled row and the factor back to exp2 units
+  // are kept per row.
+  constexpr int RPP = HD == 128 ? 2 : 4;                       // rows of a warp at a time
+  constexpr int QP = (ROWS + kWarps * RPP - 1) / (kWarps * RPP);
+  const int q_cc = lane & 3, q_w = lane / (4 * RPP);           // dims (q_cc WORDS + q_w) 8 ..
+  const int q_r = warp * RPP + ((lane >> 2) & (RPP - 1));      // rows q_r, q_r + kWarps RPP, ..
+  uint4 raw[QP];
+#pragma unroll
+  for (int k = 0; k < QP; ++k) {
+    const int r = q_r + k * kWarps * RPP;
+    raw[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows)
+      raw[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (row0 + r / grp) * p.q_row_stride +
+                                               (long long)(kvh * grp + r % grp) * HD + (q_cc * WORDS + q_w) * 8);
+  }
   if (warp == 0)
     for (; issued < min(S, npg); ++issued) issue(issued, issued);
   if (threadIdx.x == kThreads - 1) {
     l2_prefetch_share(p.l2_next[0], p.l2_next_bytes[0]);
     l2_prefetch_share(p.l2_next[1], p.l2_next_bytes[1]);
   }
-
-  // Queries: each row is scaled by a power of two (largest element in [2^14, 2^15)),
-  // so the factor 1/16 of the odd columns costs no precision; the sum of the scaled
-  // row and the factor back to exp2 units are kept per row.  One warp per row, up to
-  // eight rows at a time: their loads and reductions overlap.
-  {
-    constexpr int PER = HD / 32;  // elements of a lane
-    constexpr int RB = NT <= 4 ? NT * 2 : 8;
-    for (int r0 = warp; r0 < ROWS; r0 += RB * kWarps) {
-      uint32_t raw[RB][PER / 2];
 #pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        const int r = r0 + k * kWarps;
+  for (int k = 0; k < QP; ++k) {
+    const uint32_t in[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+    float x[8], mx = 0.f, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < PER / 2; ++i) raw[k][i] = 0;
-        if (r < rows) {
-          const uint16_t* qr = static_cast<const uint16_t*>(p.q) + (row0 + r / grp) * p.q_row_stride +
-                               (long long)(kvh * grp + r % grp) * HD + lane * PER;
-          if constexpr (PER == 4) {
-            const uint2 w = *reinterpret_cast<const uint2*>(qr);
-            raw[k][0] = w.x, raw[k][1] = w.y;
-          } else {
-            raw[k][0] = *reinterpret_cast<const uint32_t*>(qr);
-          }
-        }
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = p.bf16 ? kv4_unpack2<true>(in[i]) : kv4_unpack2<false>(in[i]);
+      x[2 * i] = kv4_sat(f.x);
+      x[2 * i + 1] = kv4_sat(f.y);
+      mx = fmaxf(mx, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      if (o < 4 || o >= 4 * RPP) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    // 2^sh with 2^14 <= mx 2^sh < 2^15; rows below 2^-112 count as zeros (|scale| <= 2^40)
+    const int sh = mx > 1.9259299e-34f ? 14 - (int)((__float_as_uint(mx) >> 23) - 127u) : 0;
+    const float up = __uint_as_float(((uint32_t)(127 + sh) << 23) | (p.scale < 0.f ? 0x80000000u : 0u));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[i] *= up;
+      sum += x[i];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+      if (o < 4 || o >= 4 * RPP) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int r = q_r + k * kWarps * RPP;
+    if (r < ROWS) {
+      if (q_cc == 0 && q_w == 0) {
+        float* row = reinterpret_cast<float*>(&s_row[r >> 1]) + (r & 1);
+        row[0] = sum * 5.9604644775390625e-8f;  // in the units of the code products (2^-24)
+        row[2] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * 16777216.f * __uint_as_float((uint32_t)(127 - sh) << 23),
+                       1e-30f);
       }
-      float x[RB][PER], mx[RB], sum[RB];
-#pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        mx[k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER / 2; ++i) {
-          const float2 f = p.bf16 ? kv4_unpack2<true>(raw[k][i]) : kv4_unpack2<false>(raw[k][i]);
-          x[k][2 * i] = kv4_sat(f.x);
-          x[k][2 * i + 1] = kv4_sat(f.y);
-          mx[k] = fmaxf(mx[k], fmaxf(fabsf(x[k][2 * i]), fabsf(x[k][2 * i + 1])));
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < RB; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
-      int sh[RB];
-#pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        // 2^sh with 2^14 <= mx 2^sh < 2^15; rows below 2^-112 count as zeros (|scale| <= 2^40)
-        sh[k] = mx[k] > 1.9259299e-34f ? 14 - (int)((__float_as_uint(mx[k]) >> 23) - 127u) : 0;
-        const float up = __uint_as_float((uint32_t)(127 + sh[k]) << 23);
-        sum[k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          x[k][i] *= p.scale < 0.f ? -up : up;
-          sum[k] += x[k][i];
-        }
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < RB; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
-#pragma unroll
-      for (int k = 0; k < RB; ++k) {
-        const int r = r0 + k * kWarps;
-        if (r >= ROWS) break;
-        if (lane == 0) {
-          float* row = reinterpret_cast<float*>(&s_row[r >> 1]) + (r & 1);
-          row[0] = sum[k] * 5.9604644775390625e-8f;  // in the units of the code products (2^-24)
-          row[2] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * 16777216.f *
-                             __uint_as_float((uint32_t)(127 - sh[k]) << 23),
-                         1e-30f);
-        }
-        // fragment of lane (r % 8, cc), word w: halves (d0, d4) (d1, d5)/16 (d2, d6) (d3, d7)/16
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int d = lane * PER + i;
-          const int cc = d / (HD / 4), w = (d % (HD / 4)) / 8, n = d % 8;
-          __half* dst =
-              reinterpret_cast<__half*>(qfrag + (((r >> 3) * WORDS + w) * 32 + (r & 7) * 4 + cc) * 16);
-          dst[(n & 3) * 2 + (n >> 2)] = __float2half_rn((n & 1) ? x[k][i] * 0.0625f : x[k][i]);
-        }
-      }
+      // fragment of lane (r % 8, q_cc), word q_w: halves (d0, d4) (d1, d5)/16 (d2, d6) (d3, d7)/16
+      *reinterpret_cast<uint4*>(qfrag + (((r >> 3) * WORDS + q_w) * 32 + (r & 7) * 4 + q_cc) * 16) =
+          make_uint4(pack_f16x2(x[0], x[4]), pack_f16x2(x[1] * 0.0625f, x[5] * 0.0625f), pack_f16x2(x[2], x[6]),
+                     pack_f16x2(x[3] * 0.0625f, x[7] * 0.0625f));
     }
   }
   __syncthreads();
@@ -854,7 +850,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     }
   }
   team_sync<TW>();
-  float* const part = reinterpret_cast<float*>(ring);  // [TEAMS][ROWS][HD]
+  constexpr int REC = CL ? C::kRec : HD;  // floats of a row
+  float* const part = reinterpret_cast<float*>(ring);  // [TEAMS][ROWS][REC]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -864,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
 #pragma unroll
       for (int w = 0; w < TW; ++w) bias += s_red2[team * TW + w][r];
       const float u0 = e_up * 16777216.f, u1 = e_up * 1048576.f;
-      float* o = part + (team * ROWS + r) * HD + g * (HD / 8) + piece0 * 4;
+      float* o = part + (team * ROWS + r) * REC + g * (HD / 8) + piece0 * 4;
       if constexpr (PW == 1)
         *reinterpret_cast<float2*>(o + (tw & 1) * 2) =
             make_float2(fmaf(acc[nt][0][e], u0, bias), fmaf(acc[nt][0][2 + e], u1, bias));
@@ -875,11 +872,66 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
               make_float4(fmaf(acc[nt][2 * w][e], u0, bias), fmaf(acc[nt][2 * w][2 + e], u1, bias),
                           fmaf(acc[nt][(2 * w + 1) % PW][e], u0, bias), fmaf(acc[nt][(2 * w + 1) % PW][2 + e], u1, bias));
     }
+  constexpr int V4 = HD / 4;
+  if constexpr (CL) {
+    if (pieces > 1) {
+      // Every CTA sends each row's partial to the CTA that finishes the row, one bulk copy per
+      // CTA, and merges what it receives: sum_i 2^(m_i - M) o_i over the cluster.
+      if (threadIdx.x < ROWS) {
+        float l = 0.f;
+#pragma unroll
+        for (int k = 0; k < TW; ++k) l += s_red[k][threadIdx.x];
+        const float m = reinterpret_cast<const float*>(s_max[0])[threadIdx.x];
+        // a wait that ran out: a maximum that is NaN makes the row NaN
+        *reinterpret_cast<float2*>(part + threadIdx.x * REC + HD) = make_float2(s_fail ? NAN : m, l);
+      }
+      fence_proxy_async();
+      __syncthreads();
+      cluster_wait();  // every CTA's barrier is ready
+      float* const recv = reinterpret_cast<float*>(qfrag + C::kFixed);  // [pieces][own][REC]
+      if (threadIdx.x < pieces) {
+        const int n = max(0, min(rows - share * (int)threadIdx.x, share));
+        if (n > 0)
+          bulk_push(mapa_u32(smem_u32(recv + piece * n * REC), threadIdx.x), part + threadIdx.x * share * REC, n * REC * 4,
+                    mapa_u32(smem_u32(&received), threadIdx.x));
+      }
+      const bool ok = mbar_wait(&received, 0, p.status);
+      __syncwarp();
+      cluster_arrive();  // all copies to this CTA have landed: when all have, no source is needed
+      for (int it = threadIdx.x; it < own * V4; it += kThreads) {
+        const int r = it / V4, d4 = it % V4;
+        float M = kNoMax, l = 0.f, m[16];
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < pieces) {
+            m[i] = recv[(i * own + r) * REC + HD];
+            M = fmaxf(M, m[i]);
+          }
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < pieces) {
+            const float4 x = *reinterpret_cast<const float4*>(recv + (i * own + r) * REC + d4 * 4);
+            const float w = ex2(m[i] - M);
+            l = fmaf(w, recv[(i * own + r) * REC + HD + 1], l);
+            o.x = fmaf(w, x.x, o.x);
+            o.y = fmaf(w, x.y, o.y);
+            o.z = fmaf(w, x.z, o.z);
+            o.w = fmaf(w, x.w, o.w);
+          }
+        if (!ok) o = make_float4(NAN, NAN, NAN, NAN), l = 1.f;
+        const int row = own0 + r;
+        store_row4(p, row0 + row / grp, kvh * grp + row % grp, HD, d4, o, l);
+      }
+      __syncwarp();
+      cluster_wait();
+      return;
+    }
+  }
   __syncthreads();
   // the CTA's: sum_i 2^(m_i - M) o_i over the teams; normalised and rounded where the
   // group is whole, else left in the workspace
   {
-    constexpr int V4 = HD / 4;
     const bool whole = pieces == 1;
     float* const ws = CL ? nullptr : kv4_partial(p.workspace, slot, ROWS, HD);
     for (int it = threadIdx.x; it < rows * V4; it += kThreads) {
@@ -894,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
 #pragma unroll
       for (int i = 0; i < TEAMS; ++i) {
         const float w = TEAMS == 1 ? 1.f : ex2(m[i] - M);
-        const float4 x = *reinterpret_cast<const float4*>(part + (i * ROWS + r) * HD + d4 * 4);
+        const float4 x = *reinterpret_cast<const float4*>(part + (i * ROWS + r) * REC + d4 * 4);
         o.x = fmaf(w, x.x, o.x);
         o.y = fmaf(w, x.y, o.y);
         o.z = fmaf(w, x.z, o.z);
@@ -903,14 +955,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
         for (int k = 0; k < TW; ++k) l = fmaf(w, s_red[i * TW + k][r], l);
       }
       if (s_fail) o = make_float4(NAN, NAN, NAN, NAN), l = 1.f;  // a wait ran out
-      if (whole) {
+      if (CL || whole) {
         store_row4(p, row0 + r / grp, kvh * grp + r % grp, HD, d4, o, l);
-      } else if (CL) {  // the first team's place; each item reads and writes its own four values
-        *reinterpret_cast<float4*>(part + r * HD + d4 * 4) = o;
-        if (d4 == 0) {
-          s_m[r] = M;
-          s_l[r] = l;
-        }
       } else {
         *reinterpret_cast<float4*>(ws + r * HD + d4 * 4) = o;
         if (d4 == 0) {
@@ -919,102 +965,106 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
         }
       }
     }
-    if constexpr (CL) {
-      if (pieces > 1) {
-        cluster_arrive();
-        cluster_wait();
-        // the cluster's CTAs share the rows; all remote loads of a row are in flight together
-        const uint32_t o_base = smem_u32(part), m_base = smem_u32(s_m), l_base = smem_u32(s_l);
-        const int n_my = rows > piece ? (rows - piece + pieces - 1) / pieces : 0;
-        for (int it = threadIdx.x; it < n_my * V4; it += kThreads) {
-          const int r = piece + it / V4 * pieces, d4 = it % V4;
-          float M = kNoMax, ms[16], ls[16];
-          float4 os[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (i < pieces) {
-              ms[i] = ld_dsmem_f32(mapa_u32(m_base + r * 4, i));
-              ls[i] = ld_dsmem_f32(mapa_u32(l_base + r * 4, i));
-              os[i] = ld_dsmem_f4(mapa_u32(o_base + (r * HD + d4 * 4) * 4, i));
-              M = fmaxf(M, ms[i]);
-            }
-          }
-          float l = 0.f;
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            if (i < pieces) {
-              const float w = ex2(ms[i] - M);
-              l = fmaf(w, ls[i], l);
-              o.x = fmaf(w, os[i].x, o.x);
-              o.y = fmaf(w, os[i].y, o.y);
-              o.z = fmaf(w, os[i].z, o.z);
-              o.w = fmaf(w, os[i].w, o.w);
-            }
-          }
-          store_row4(p, row0 + r / grp, kvh * grp + r % grp, HD, d4, o, l);
-        }
-        __syncwarp();
-        cluster_arrive();  // keep this CTA's shared memory until every CTA has read it
-        cluster_wait();
-      }
-    }
   }
 }
 
 // Merge the partials of one cut group: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
-// grid (chunks of 128 float4 of a group's rows, Hkv, B).
-template <int HD>
-__global__ void __launch_bounds__(128) kv4_merge_kernel(const __grid_constant__ Kv4AttnParams p, int ws_rows) {
+// grid (shares of a group's rows, Hkv, B).  A group of few has many partials, and reading them
+// one after the other is what a merge costs: hd / 4 lanes take a row, and up to all warps
+// share its partials, eight loads in flight each.
+__host__ __device__ constexpr int merge_split(int n, int warps) {  // warps of a row, a power of two
+  int split = 1;
+  while (split < warps && split * (warps == 16 ? 4 : 8) < n) split *= 2;
+  return split;
+}
+template <int HD, int kMergeWarps>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    kv4_merge_kernel(const __grid_constant__ Kv4AttnParams p, int ws_rows) {
   constexpr int V4 = HD / 4;
+  constexpr int RPW = 32 / V4;  // rows of a warp
+  __shared__ float4 s_o[kMergeWarps][32];
+  __shared__ float2 s_ml[kMergeWarps][32];
   const int b = blockIdx.z, kvh = blockIdx.y, grp = p.Hq / p.Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Kv4Seq mine = kv4_first_seqs(p);
   const Kv4Seq seq = kv4_seq_at(p, mine, b);
   const Kv4Plan plan = kv4_plan(p, mine);
   const int n = kv4_pieces(seq.pages, plan.target);
+  if (n < 2) {  // one CTA finished the group
+    pdl_wait();
+    return;
+  }
   int before_cut = 0;  // partials of the sequences before this one
-  for (int i = threadIdx.x & 31; i < b; i += 32) {
+  for (int i = lane; i < b; i += 32) {
     const int k = kv4_pieces(i < 32 ? mine.pages : kv4_seq(p, i).pages, plan.target);
     if (k > 1) before_cut += k;
   }
-  const int i0 = warp_sum(before_cut) * p.Hkv + kvh * n;
+  const int i0 = (int)__reduce_add_sync(0xffffffffu, (unsigned)before_cut) * p.Hkv + kvh * n;
   pdl_wait();
   pdl_launch_dependents();
-  if (n < 2) return;  // one CTA finished the group
-  const int it = blockIdx.x * 128 + threadIdx.x;
-  const int r = it / V4, d4 = it % V4;
-  if (r >= seq.Wb * grp) return;
-  float M = kNoMax, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int NB = 8;  // partials whose loads are in flight together
-  for (int k0 = 0; k0 < n; k0 += NB) {
-    float ms[NB], ls[NB];
-    float4 os[NB];
-    float mb = M;
+  const int split = merge_split(n, kMergeWarps);
+  const int part = warp & (split - 1), at_once = kMergeWarps / split * RPW;
+  const int d4 = lane % V4, rows = seq.Wb * grp;
+  for (int r0 = blockIdx.x * at_once; r0 < rows; r0 += gridDim.x * at_once) {
+    const int r = r0 + warp / split * RPW + lane / V4;
+    const int rr = min(r, rows - 1);
+    float M = kNoMax, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int NB = 8;  // partials whose loads are in flight together
+    for (int k0 = part; k0 < n; k0 += NB * split) {
+      float ms[NB], ls[NB];
+      float4 os[NB];
+      float mb = M;
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const float* ws = kv4_partial(p.workspace, i0 + min(k0 + k, n - 1), ws_rows, HD);
-      os[k] = *reinterpret_cast<const float4*>(ws + r * HD + d4 * 4);
-      ms[k] = ws[ws_rows * HD + r];
-      ls[k] = ws[ws_rows * HD + ws_rows + r];
-      mb = fmaxf(mb, ms[k]);
-    }
-    const float a = ex2(M - mb);
-    M = mb;
-    l *= a;
-    o.x *= a, o.y *= a, o.z *= a, o.w *= a;
-#pragma unroll
-    for (int k = 0; k < NB; ++k)
-      if (k0 + k < n) {
-        const float w = ex2(ms[k] - M);
-        l = fmaf(w, ls[k], l);
-        o.x = fmaf(w, os[k].x, o.x);
-        o.y = fmaf(w, os[k].y, o.y);
-        o.z = fmaf(w, os[k].z, o.z);
-        o.w = fmaf(w, os[k].w, o.w);
+      for (int k = 0; k < NB; ++k) {
+        const float* ws = kv4_partial(p.workspace, i0 + min(k0 + k * split, n - 1), ws_rows, HD);
+        os[k] = *reinterpret_cast<const float4*>(ws + rr * HD + d4 * 4);
+        ms[k] = ws[ws_rows * HD + rr];
+        ls[k] = ws[ws_rows * HD + ws_rows + rr];
       }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) mb = fmaxf(mb, ms[k]);
+      const float a = ex2(M - mb);
+      M = mb;
+      l *= a;
+      o.x *= a, o.y *= a, o.z *= a, o.w *= a;
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+        if (k0 + k * split < n) {
+          const float w = ex2(ms[k] - M);
+          l = fmaf(w, ls[k], l);
+          o.x = fmaf(w, os[k].x, o.x);
+          o.y = fmaf(w, os[k].y, o.y);
+          o.z = fmaf(w, os[k].z, o.z);
+          o.w = fmaf(w, os[k].w, o.w);
+        }
+    }
+    if (split > 1) {
+      s_o[warp][lane] = o;
+      s_ml[warp][lane] = make_float2(M, l);
+      __syncthreads();
+      if (part == 0) {
+        float top = M;
+        for (int k = 1; k < split; ++k) top = fmaxf(top, s_ml[warp + k][lane].x);
+        const float a = ex2(M - top);
+        l *= a;
+        o.x *= a, o.y *= a, o.z *= a, o.w *= a;
+#pragma unroll 4
+        for (int k = 1; k < split; ++k) {
+          const float2 ml = s_ml[warp + k][lane];
+          const float4 x = s_o[warp + k][lane];
+          const float w = ex2(ml.x - top);
+          l = fmaf(w, ml.y, l);
+          o.x = fmaf(w, x.x, o.x);
+          o.y = fmaf(w, x.y, o.y);
+          o.z = fmaf(w, x.z, o.z);
+          o.w = fmaf(w, x.w, o.w);
+        }
+      }
+      __syncthreads();
+    }
+    if (part == 0 && r < rows) store_row4(p, seq.row0 + r / grp, kvh * grp + r % grp, HD, d4, o, l);
   }
-  store_row4(p, seq.row0 + r / grp, kvh * grp + r % grp, HD, d4, o, l);
 }
 
 // Function attributes are per device: one bit per device once they are set there.
@@ -1034,29 +1084,32 @@ cudaError_t configure(K kernel, int smem, bool cluster, std::atomic<uint64_t>& d
 int hint_pages(const Kv4AttnParams& p) { return (p.kv_len_hint + kPage - 1) / kPage; }
 
 // Short caches: the CTAs of a group as one cluster, where all clusters fit the GPU at once (14 of
-// 16 CTAs, 36 of 8, 74 of 4 and 152 of 2 do with two CTAs per SM) and a CTA gets four pages at
-// most.  No workspace and no second launch: 6.5 against 8.2 us at 1024 tokens, one sequence of 8
-// kv heads.  0: not short.
-int cluster_size(int B, int Hkv, int pages) {
+// 16 CTAs, 36 of 8, 74 of 4 and 152 of 2 do with two CTAs per SM) and a CTA gets few pages: nine
+// at most where the clusters fill the SMs, six where they leave some idle.  No workspace and no
+// second launch.  0: not short.  Clusters against pieces, in us (8 kv heads of 128; 1, 5 and 15
+// rows of 4 query heads each):
+//   sequences x tokens   1 x 4096    1 x 8192   4 x 4096    8 x 2048    16 x 1024
+//   pages of a CTA       4           8          8           8           8
+//   1 row                 8.4,  9.7  11.0,  9.9 11.3, 11.2  11.5, 11.4  11.5, 11.3
+//   5 rows               12.4, 13.5  16.7, 15.3 17.3, 20.9  17.7, 18.6  18.1, 20.0
+//   15 rows              20.9, 25.7  28.2, 30.9 32.3, 36.2  33.4, 38.5
+// and at 16 pages for each CTA (8 x 4096 tokens, 1 and 5 rows) 16.9, 14.5 and 26.1, 25.2.
+int cluster_size(int B, int Hkv, int pages, int sm_count) {
   const long long groups = (long long)B * Hkv;
   if (pages <= 4 && groups <= (1 << 30)) return 1;
   const struct { int cs, fit; } sizes[] = {{2, 152}, {4, 74}, {8, 36}, {16, 14}};
+  int cs = 0;  // the widest that fits: fewer pages for each CTA
   for (const auto& s : sizes)
-    if (groups <= s.fit && pages <= 4 * s.cs) {
-      int cs = s.cs;  // the widest that fits: fewer pages for each CTA
-      for (const auto& w : sizes)
-        if (w.cs > cs && groups <= w.fit && pages >= w.cs) cs = w.cs;
-      return cs;
-    }
-  return 0;
+    if (groups <= s.fit && pages >= s.cs) cs = s.cs;
+  return pages <= (groups * cs > sm_count ? 9 : 6) * cs ? cs : 0;
 }
 
 template <int HD, int NT>
 cudaError_t launch_cluster(Kv4AttnParams p, int cs, cudaStream_t st) {
   using C = Cfg<HD, NT, kWarps>;
   static std::atomic<uint64_t> done{0};
-  p.stages = C::stages(2);
-  const int smem = C::kFixed + p.stages * C::kBlock;
+  p.stages = C::stages(2, C::kRecv);
+  const int smem = C::kFixed + C::kRecv + p.stages * C::kBlock;
   cudaError_t e = configure(kv4_attention_kernel<HD, NT, kWarps, true>, smem, true, done);
   if (e != cudaSuccess) return e;
   p.cluster = cs;
@@ -1082,13 +1135,18 @@ cudaError_t launch_pieces(Kv4AttnParams p, cudaStream_t st) {
   e = launch_k(kv4_attention_kernel<HD, NT, TW, false>, dim3((unsigned)ctas), dim3(kThreads),
                C::kFixed + p.stages * C::kBlock, st, p);
   if (e != cudaSuccess) return e;
-  const int chunks = (p.W * (p.Hq / p.Hkv) * (HD / 4) + 127) / 128;
-  return launch_k(kv4_merge_kernel<HD>, dim3(chunks, p.Hkv, p.B), dim3(128), 0, st, p, NT * 8);
+  // four warps, or sixteen for groups that may have sixteen partials or more
+  const int n = (int)std::max<long long>(1, p.slots / groups), rows = p.W * (p.Hq / p.Hkv);
+  const auto merge = [&](auto kernel, int warps) {
+    const int at_once = warps / merge_split(n, warps) * (128 / HD);
+    return launch_k(kernel, dim3((rows + at_once - 1) / at_once, p.Hkv, p.B), dim3(warps * 32), 0, st, p, NT * 8);
+  };
+  return n >= 16 ? merge(kv4_merge_kernel<HD, 16>, 16) : merge(kv4_merge_kernel<HD, 4>, 4);
 }
 
 template <int HD, int NT>
 cudaError_t launch_nt(const Kv4AttnParams& p, cudaStream_t st) {
-  if (const int cs = cluster_size(p.B, p.Hkv, hint_pages(p))) return launch_cluster<HD, NT>(p, cs, st);
+  if (const int cs = cluster_size(p.B, p.Hkv, hint_pages(p), p.sm_count)) return launch_cluster<HD, NT>(p, cs, st);
   return launch_pieces<HD, NT, (NT <= 2 ? 1 : kWarps)>(p, st);
 }
 
@@ -1112,7 +1170,7 @@ cudaError_t launch_hd(const Kv4AttnParams& p, cudaStream_t st) {
 // The partials of cut groups: at most two for each slot of the largest grid (4 CTAs per SM, 3
 // from four row tiles on).
 long long kv4_attention_workspace(int B, int Hkv, int rows, int hd, int kv_len_hint, int sm_count) {
-  if (cluster_size(B, Hkv, (kv_len_hint + kPage - 1) / kPage)) return 0;
+  if (cluster_size(B, Hkv, (kv_len_hint + kPage - 1) / kPage, sm_count)) return 0;
   const int nt = (rows + 7) / 8;
   return 2ll * (nt <= 3 ? 4 : 3) * sm_count * nt * 8 * (hd + 2) * 4;
 }
