@@ -33,7 +33,9 @@
 // caches need neither: the CTAs of a group are one thread-block cluster and merge
 // through distributed shared memory.  (One list of all pages cut into exactly equal
 // shares was slower: a share that crosses from one group into the next pays the
-// prologue and the epilogue twice.)
+// prologue and the epilogue twice.)  In a cluster every CTA sends each row's partial to the
+// CTA that finishes the row, in one bulk copy per CTA, into memory kept for it: reading the
+// others' partials instead took 3 to 8 thousand cycles more, a remote load at a time.
 //
 // A page of one kv head is one block (8704 bytes at head_dim 128) and one bulk copy
 // into the CTA's ring.  A team of TW warps works on a page: with TW = 1 each of the
@@ -42,10 +44,10 @@
 // passing through shared memory.  Either way every code is unpacked once per CTA.  A
 // team of four keeps a warp's accumulators small (8 registers per 8 rows, against 32),
 // so wide windows fit, and has a page's result sooner; one warp needs no barriers.
-// Measured (head_dim 128, 8 kv heads): one row tile, 2 x 65520 tokens 35 against 43 us;
-// two, 8 x 32768 tokens 78 against 88; three, 64 x 512-2048 tokens 67 against 64 (8 x 32768
-// tokens 112 against 116).  In a team the scores of the next page are computed before the
-// barrier that releases this page's weights: one barrier per page.
+// Measured (head_dim 128, 8 kv heads; one warp, four): one row tile, 2 x 65520 tokens 32, 37
+// us; two, 8 x 32768 tokens 76, 83; three, 64 x 512-2048 tokens 63, 58 (8 x 32768 tokens 109,
+// 111).  In a team the scores of the next page are computed before the barrier that
+// releases this page's weights: one barrier per page.
 //
 // What bounds it.  mma.sync runs at 8 cycles per m16n8k16 and SM quarter here and shares
 // its pipe with the fp32 instructions; AND and shift take 2 cycles, exp2 and movmatrix 4
