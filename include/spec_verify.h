@@ -342,10 +342,10 @@ spec_status spec_kv_write(spec_model* m, int32_t seq_id, int32_t n_tokens, const
  *     x' = clamp(x, -65504, 65504), NaN -> -65504 (the library's fp16 saturation)
  *     m  = fp16 rounded down of min x',   s = fp16 rounded up of (max x' - m) / 15
  *     c  = floor((x' - m) / s + 1/2) in 0..15, 0 where s = 0
- * and the cache holds c (4 bits), s and m (fp16) and stands for s * c + m.  (A
- * quotient less than 2^-20 of its value below a half counts as the half.)  The
- * order of the bytes inside a block is the library's own: write with spec_kv4_write,
- * take values out with spec_kv4_read.
+ * and the cache holds c (4 bits), s and m (fp16) and stands for s * c + m.  (The
+ * differences x' - m and max x' - m are rounded to fp32, nothing else is.)  The order
+ * of the bytes inside a block is the library's own: write with spec_kv4_write, take
+ * values out with spec_kv4_read.
  *
  * Rows of a call: sequence b owns flat rows row_off[b] .. row_off[b + 1] - 1 (device
  * [B + 1], non-decreasing, row_off[0] >= 0), or rows_per_seq rows each where row_off

@@ -3,7 +3,8 @@ verify window's attention over held values.
 
 Per vector x (one token's K or V of one kv head): x' = clamp(x, -65504, 65504) with NaN
 -> -65504, m = fp16 rounded down of min x', s = fp16 rounded up of (max x' - m) / 15,
-c = floor((x' - m) / s + 1/2) (0 where s = 0); it stands for s * c + m.
+c = floor((x' - m) / s + 1/2) (0 where s = 0); it stands for s * c + m.  The differences
+with m are fp32 numbers.
 """
 import numpy as np
 
@@ -28,23 +29,15 @@ def quantise(x):
     """x [..., hd] -> (codes, s, m); s and m [..., 1]."""
     x = saturate(x)
     m = half_down(x.min(-1, keepdims=True))
-    s = half_up((x.max(-1, keepdims=True) - m) / 15.0)
-    q = np.divide(x - m, s, out=np.zeros_like(x), where=s > 0)
+    d = (x - m).astype(np.float32).astype(np.float64)
+    s = half_up(d.max(-1, keepdims=True) / 15.0)
+    q = np.divide(d, s, out=np.zeros_like(x), where=s > 0)
     return np.clip(np.floor(q + 0.5), 0, 15), s, m
 
 
 def held(x):
     c, s, m = quantise(x)
     return c * s + m
-
-
-def near_half(x, width=2.0 ** -18):
-    """Values whose quotient lies within `width` of itself of a half: their code may go either way."""
-    x = saturate(x)
-    _, s, m = quantise(x)
-    q = np.divide(x - m, s, out=np.zeros_like(x), where=s > 0)
-    f = q - np.floor(q)
-    return (np.abs(f - 0.5) <= width * np.maximum(q, 1)) & (f != 0.5)
 
 
 def window_mask(n_rows, parent=None):

@@ -45,10 +45,9 @@ SPEC_DEVICE_INLINE int kv4_slot(const Kv4Rows& a, int r) {
 }
 
 // Offset m, scale s and the factor of the quotients of a vector with the given extremes.
-// The code of x is floor((x - m) / s + 1/2): the sum (x - m) * inv + 1.5 * 2^23 rounds to
-// the nearest whole number in the float's last bits.  inv is 1/s raised by 2^-20 of
-// itself, so an exact half (about one value in a thousand: x, m and s have 11 bits)
-// always goes up, whichever way 1/s was rounded.
+// inv is 1/s raised by 2^-20 of itself, more than all roundings of a quotient (3 x 2^-24), so
+// a code taken with it is never too small, and too large only where the quotient lies within
+// 2^-20 of itself below a half.
 SPEC_DEVICE_INLINE uint32_t kv4_params(float lo, float hi, float& m, float& inv) {
   const __half mh = kv4_half_down(lo);
   m = __half2float(mh);
@@ -58,14 +57,41 @@ SPEC_DEVICE_INLINE uint32_t kv4_params(float lo, float hi, float& m, float& inv)
   return ((uint32_t)__half_as_ushort(sh) << 16) | __half_as_ushort(mh);
 }
 
-// Codes of eight values, value i in nibble i.  The float's bits are 0x4b400000 + c; they are
-// added up shifted and the constants' sum taken off once.
-SPEC_DEVICE_INLINE uint32_t kv4_codes(const float (&x)[8], float m, float inv) {
+// Codes of eight values, value i in nibble i.  With d = x - m, the sum d inv + 1.5 * 2^23
+// rounds to the nearest whole number in the float's last bits: 0x4b400000 + c, added up
+// shifted and the constants' sum taken off once.  An exact half (about one value in a
+// thousand: x, m and s have 11 bits) goes up.  The rest d - s c, whose bits fit a float,
+// shows a code that is too large by being below -s/2; that is rare (about one value in a
+// million) and mended apart.  Two values to an instruction, each rounded as by itself.
+SPEC_DEVICE_INLINE uint32_t kv4_codes(const float (&x)[8], float m, float s, float inv) {
   uint32_t w = 0;
+  float least = 0.f;
 #pragma unroll
-  for (int i = 7; i >= 0; --i)
-    w = (w << 4) + __float_as_uint(__fmaf_rn(__fsub_rn(x[i], m), inv, 12582912.f));
-  return w - 0x4b400000u * 0x11111111u;
+  for (int i = 6; i >= 0; i -= 2) {
+    float lo, hi, rlo, rhi;
+    asm("{\n\t.reg .b64 d, f, c, t;\n\t"
+        "mov.b64 d, {%4, %5};\n\tmov.b64 t, {%6, %6};\n\tadd.rn.f32x2 d, d, t;\n\t"
+        "mov.b64 t, {%7, %7};\n\tmov.b64 c, {%8, %8};\n\tfma.rn.f32x2 f, d, t, c;\n\tmov.b64 {%0, %1}, f;\n\t"
+        "mov.b64 c, {%9, %9};\n\tadd.rn.f32x2 f, f, c;\n\t"
+        "mov.b64 t, {%10, %10};\n\tfma.rn.f32x2 f, f, t, d;\n\tmov.b64 {%2, %3}, f;\n\t}"
+        : "=f"(lo), "=f"(hi), "=f"(rlo), "=f"(rhi)
+        : "f"(x[i]), "f"(x[i + 1]), "f"(-m), "f"(inv), "f"(12582912.f), "f"(-12582912.f), "f"(-s));
+    w = (w << 4) + __float_as_uint(hi);
+    w = (w << 4) + __float_as_uint(lo);
+    least = fminf(fminf(rlo, rhi), least);
+  }
+  w -= 0x4b400000u * 0x11111111u;
+  if (least < -0.5f * s) {
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+      float xi = x[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) xi = i == k ? x[k] : xi;
+      const float c = (float)((w >> (4 * i)) & 15u);
+      if (__fmaf_rn(c, -s, __fsub_rn(xi, m)) < -0.5f * s) w -= 1u << (4 * i);
+    }
+  }
+  return w;
 }
 
 // Eight of the caller's values: saturated in their own type (fp16 at once; bf16 to +-65536,
@@ -86,15 +112,21 @@ SPEC_DEVICE_INLINE void kv4_clamp(uint32_t (&w)[4]) {
   }
 }
 // ... their minimum (low half) and negated maximum (high half) over LANES neighbouring
-// lanes ...
+// lanes, NaN if there is one ...
 template <bool BF16>
 SPEC_DEVICE_INLINE uint32_t kv4_min2(uint32_t a, uint32_t b) {
   if (BF16) {
-    __nv_bfloat162 v = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    __nv_bfloat162 v = __hmin2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
     return *reinterpret_cast<uint32_t*>(&v);
   }
-  __half2 v = __hmin2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+  __half2 v = __hmin2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<uint32_t*>(&v);
+}
+// Whether such a pair is within +-65504 (then so is every value, and saturating changes none).
+template <bool BF16>
+SPEC_DEVICE_INLINE bool kv4_in_range(uint32_t e) {
+  const float2 f = kv4_unpack2<BF16>(e);
+  return f.x >= -65504.f && f.y >= -65504.f;
 }
 template <bool BF16, int LANES>
 SPEC_DEVICE_INLINE uint32_t kv4_extremes(const uint32_t (&w)[4]) {
@@ -108,13 +140,16 @@ SPEC_DEVICE_INLINE uint32_t kv4_extremes(const uint32_t (&w)[4]) {
 }
 // ... and as fp32.
 template <bool BF16>
-SPEC_DEVICE_INLINE void kv4_floats(const uint32_t (&w)[4], float (&x)[8]) {
+SPEC_DEVICE_INLINE void kv4_floats(const uint32_t (&w)[4], bool in_range, float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = kv4_unpack2<BF16>(w[i]);
-    x[2 * i] = BF16 ? kv4_sat(f.x) : f.x;
-    x[2 * i + 1] = BF16 ? kv4_sat(f.y) : f.y;
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
   }
+  if (BF16 && !in_range)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = kv4_sat(x[i]);
 }
 
 // Both kernels: grid (chunks of 8 RPW rows, kv heads); a warp takes RPW <= 16 consecutive
@@ -156,18 +191,29 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
   const int my_row = lane & 15, my_kv = lane >> 4;
   const int my_slot = my_row < min(n, RPW) ? kv4_slot(p.rows, r0 + my_row) : -1;
   uint32_t mine = 0;                        // extremes of this lane's row
+  bool in_range = true;                     // all of the warp's values
+  // Saturating costs eight instructions of eight values: it is done only where the extremes
+  // show a value that needs it, for all of the warp's rows, and they are taken again.
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    bool fits = true;
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
+    for (int it = 0; it < IT; ++it) {
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      kv4_clamp<BF16>(w[kv][it]);
-      const uint32_t e = __shfl_sync(0xffffffffu, kv4_extremes<BF16, L>(w[kv][it]), my_row % T * L);
-      if (my_row / T == it && my_kv == kv) mine = e;
+      for (int kv = 0; kv < 2; ++kv) {
+        if (pass == 1) kv4_clamp<BF16>(w[kv][it]);
+        const uint32_t all = kv4_extremes<BF16, L>(w[kv][it]);
+        fits = fits && kv4_in_range<BF16>(all);
+        const uint32_t e = __shfl_sync(0xffffffffu, all, my_row % T * L);
+        if (my_row / T == it && my_kv == kv) mine = e;
+      }
     }
+    if (__all_sync(0xffffffffu, fits) || pass == 1) break;
+    in_range = false;
   }
   const float2 ext = kv4_unpack2<BF16>(mine);
   float m, inv;
-  const uint32_t par = kv4_params(BF16 ? kv4_sat(ext.x) : ext.x, BF16 ? kv4_sat(-ext.y) : -ext.y, m, inv);
+  const uint32_t par = kv4_params(kv4_sat(ext.x), kv4_sat(-ext.y), m, inv);
   constexpr int kBlock = kv4_block_bytes(HD);
   if (my_slot >= 0)
     reinterpret_cast<uint32_t*>(p.pool + ((long long)(my_slot / kPage) * p.Hkv + h) * kBlock + kPage * HD)[
@@ -179,10 +225,12 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
     uint32_t code[2];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const float tm = __shfl_sync(0xffffffffu, m, kv * 16 + tok), ti = __shfl_sync(0xffffffffu, inv, kv * 16 + tok);
+      const uint32_t tp = __shfl_sync(0xffffffffu, par, kv * 16 + tok);
+      const float ti = __shfl_sync(0xffffffffu, inv, kv * 16 + tok);
+      const float2 ms = __half22float2(*reinterpret_cast<const __half2*>(&tp));
       float x[8];
-      kv4_floats<BF16>(w[kv][it], x);
-      code[kv] = kv4_codes(x, tm, ti);
+      kv4_floats<BF16>(w[kv][it], in_range, x);
+      code[kv] = kv4_codes(x, ms.x, ms.y, ti);
     }
     const uint32_t other = __shfl_xor_sync(0xffffffffu, code[1], L);
     if (slot < 0) continue;
@@ -319,10 +367,10 @@ __global__ void kv4_fill_kernel(uint8_t* pool, long long layer_bytes, const int3
         w[i] = *reinterpret_cast<const uint32_t*>(&v);
       }
       const float2 ext = kv4_unpack2<false>(kv4_extremes<false, kLanes>(w));
-      kv4_floats<false>(w, x);
+      kv4_floats<false>(w, true, x);
       float m, inv;
       const uint32_t par = kv4_params(ext.x, -ext.y, m, inv);
-      const uint32_t code = kv4_codes(x, m, inv);
+      const uint32_t code = kv4_codes(x, m, __half2float(__ushort_as_half((unsigned short)(par >> 16))), inv);
       if (j8 == 0) reinterpret_cast<uint32_t*>(block + kPage * HD)[kv * kPage + t] = par;
       if (kv == 0) {
         reinterpret_cast<uint32_t*>(block + t * (HD / 2))[j8] = code;
