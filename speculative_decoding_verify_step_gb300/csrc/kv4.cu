@@ -45,53 +45,54 @@ SPEC_DEVICE_INLINE int kv4_slot(const Kv4Rows& a, int r) {
 }
 
 // Offset m, scale s and the factor of the quotients of a vector with the given extremes.
-// inv is 1/s raised by 2^-20 of itself, more than all roundings of a quotient (3 x 2^-24), so
-// a code taken with it is never too small, and too large only where the quotient lies within
-// 2^-20 of itself below a half.
-SPEC_DEVICE_INLINE uint32_t kv4_params(float lo, float hi, float& m, float& inv) {
+// With d = x - m, the sum d inv + 1.5 * 2^23 rounds to the nearest whole number in the
+// float's last bits.  inv is 1/s raised by 2^-22 of itself, more than the roundings of inv and
+// of the product (2^-23), so an exact half (about one value in a thousand: x, m and s have
+// 11 bits) goes up and no code is too small; one is too large only if 2 d lies less than
+// 2^-16.5 s below an odd multiple of s (q < 14.5, at most 1.5 * 2^-22 of it).  That difference
+// is a multiple of s's last bit (2^-11 s at least) or of twice x's or m's, so x or m is below
+// 2^-6.5 s then.  The quotient of such an x lies that near to zero's, -m/s: `near` tells of
+// rows whose -m/s is within 0.0115 of a half, or whose m is below 0.0115 s (two or three rows
+// of a hundred).  All others need no second look.
+SPEC_DEVICE_INLINE uint32_t kv4_params(float lo, float hi, float& m, float& inv, bool& near) {
   const __half mh = kv4_half_down(lo);
   m = __half2float(mh);
   const __half sh = kv4_half_up(__fdiv_rn(__fsub_rn(hi, m), 15.f));
   const float s = __half2float(sh);
-  inv = s > 0.f ? __fmul_rn(__frcp_rn(s), 1.f + 9.5367431640625e-7f) : 0.f;
+  inv = s > 0.f ? __fmul_rn(__frcp_rn(s), 1.f + 2.384185791015625e-7f) : 0.f;
+  const float zero = -m * inv;
+  near = fabsf(zero - floorf(zero) - 0.5f) < 0.0115f || fabsf(m) < 0.0115f * s;
   return ((uint32_t)__half_as_ushort(sh) << 16) | __half_as_ushort(mh);
 }
 
-// Codes of eight values, value i in nibble i.  With d = x - m, the sum d inv + 1.5 * 2^23
-// rounds to the nearest whole number in the float's last bits: 0x4b400000 + c, added up
-// shifted and the constants' sum taken off once.  An exact half (about one value in a
-// thousand: x, m and s have 11 bits) goes up.  The rest d - s c, whose bits fit a float,
-// shows a code that is too large by being below -s/2; that is rare (about one value in a
-// million) and mended apart.  Two values to an instruction, each rounded as by itself.
-SPEC_DEVICE_INLINE uint32_t kv4_codes(const float (&x)[8], float m, float s, float inv) {
+// Codes of eight values, value i in nibble i.  The sums' bits are 0x4b400000 + c; they are
+// added up shifted and the constants' sum taken off once.  Two values to an instruction, each
+// rounded as by itself.
+SPEC_DEVICE_INLINE uint32_t kv4_codes(const float (&x)[8], float m, float inv) {
   uint32_t w = 0;
-  float least = 0.f;
 #pragma unroll
   for (int i = 6; i >= 0; i -= 2) {
-    float lo, hi, rlo, rhi;
-    asm("{\n\t.reg .b64 d, f, c, t;\n\t"
-        "mov.b64 d, {%4, %5};\n\tmov.b64 t, {%6, %6};\n\tadd.rn.f32x2 d, d, t;\n\t"
-        "mov.b64 t, {%7, %7};\n\tmov.b64 c, {%8, %8};\n\tfma.rn.f32x2 f, d, t, c;\n\tmov.b64 {%0, %1}, f;\n\t"
-        "mov.b64 c, {%9, %9};\n\tadd.rn.f32x2 f, f, c;\n\t"
-        "mov.b64 t, {%10, %10};\n\tfma.rn.f32x2 f, f, t, d;\n\tmov.b64 {%2, %3}, f;\n\t}"
-        : "=f"(lo), "=f"(hi), "=f"(rlo), "=f"(rhi)
-        : "f"(x[i]), "f"(x[i + 1]), "f"(-m), "f"(inv), "f"(12582912.f), "f"(-12582912.f), "f"(-s));
+    float lo, hi;
+    asm("{\n\t.reg .b64 d, f, t;\n\t"
+        "mov.b64 d, {%2, %3};\n\tmov.b64 t, {%4, %4};\n\tadd.rn.f32x2 d, d, t;\n\t"
+        "mov.b64 t, {%5, %5};\n\tmov.b64 f, {%6, %6};\n\tfma.rn.f32x2 f, d, t, f;\n\tmov.b64 {%0, %1}, f;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "f"(x[i]), "f"(x[i + 1]), "f"(-m), "f"(inv), "f"(12582912.f));
     w = (w << 4) + __float_as_uint(hi);
     w = (w << 4) + __float_as_uint(lo);
-    least = fminf(fminf(rlo, rhi), least);
   }
-  w -= 0x4b400000u * 0x11111111u;
-  if (least < -0.5f * s) {
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      float xi = x[0];
+  return w - 0x4b400000u * 0x11111111u;
+}
+// The same for rows that are near: a code that is too large leaves d - s c, whose bits fit
+// a float, below -s/2.
+SPEC_DEVICE_INLINE uint32_t kv4_codes_near(const float (&x)[8], float m, float s, float inv) {
+  uint32_t w = 0;
 #pragma unroll
-      for (int k = 1; k < 8; ++k) xi = i == k ? x[k] : xi;
-      const float c = (float)((w >> (4 * i)) & 15u);
-      if (__fmaf_rn(c, -s, __fsub_rn(xi, m)) < -0.5f * s) w -= 1u << (4 * i);
-    }
+  for (int i = 7; i >= 0; --i) {
+    const float d = __fsub_rn(x[i], m), f = __fmaf_rn(d, inv, 12582912.f);
+    w = (w << 4) + __float_as_uint(f) - (__fmaf_rn(__fsub_rn(f, 12582912.f), -s, d) < -0.5f * s ? 1u : 0u);
   }
-  return w;
+  return w - 0x4b400000u * 0x11111111u;
 }
 
 // Eight of the caller's values: saturated in their own type (fp16 at once; bf16 to +-65536,
@@ -161,12 +162,14 @@ SPEC_DEVICE_INLINE void kv4_floats(const uint32_t (&w)[4], bool in_range, float 
 //
 // What bounds them: HBM for many rows.  262144 rows of 8 heads (head_dim 128) are read in
 // 207 us, 0.97 of the measured copy rate over 1.36 GB; a write of 65536 rows and their
-// reading back take 120 us, 0.84 of it.  (One row per half-warp, with every address and
-// division computed by all of its lanes and int-to-float conversions, took 282 and 188: the
-// special-function and integer pipes were the limit.)  For few rows it is the latency of
+// reading back take 125 us, 0.80 of it, of which the write is 75: its instructions.  (One
+// row per half-warp, with every address and division computed by all of its lanes and
+// int-to-float conversions, took 282 and 188: the special-function and integer pipes were
+// the limit.  The second look at every row took 138 in place of 125, at near rows after the
+// others 132; scalar differences and quotients 128; saturating every value 132.)  For few rows it is the latency of
 // one warp's chain, so a warp then takes one step of rows only.
 template <int HD, bool BF16, int RPW>
-__global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
+__global__ void __launch_bounds__(256, RPW == 16 ? 3 : 1) kv4_write_kernel(const __grid_constant__ Kv4WriteParams p) {
   constexpr int L = HD / 8;                 // lanes of a row
   constexpr int T = 32 / L;                 // rows at a time
   constexpr int IT = RPW / T;
@@ -196,24 +199,23 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
   // show a value that needs it, for all of the warp's rows, and they are taken again.
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
-    bool fits = true;
 #pragma unroll
     for (int it = 0; it < IT; ++it) {
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         if (pass == 1) kv4_clamp<BF16>(w[kv][it]);
-        const uint32_t all = kv4_extremes<BF16, L>(w[kv][it]);
-        fits = fits && kv4_in_range<BF16>(all);
-        const uint32_t e = __shfl_sync(0xffffffffu, all, my_row % T * L);
+        const uint32_t e = __shfl_sync(0xffffffffu, kv4_extremes<BF16, L>(w[kv][it]), my_row % T * L);
         if (my_row / T == it && my_kv == kv) mine = e;
       }
     }
-    if (__all_sync(0xffffffffu, fits) || pass == 1) break;
+    if (pass == 1 || __all_sync(0xffffffffu, kv4_in_range<BF16>(mine))) break;
     in_range = false;
   }
   const float2 ext = kv4_unpack2<BF16>(mine);
   float m, inv;
-  const uint32_t par = kv4_params(kv4_sat(ext.x), kv4_sat(-ext.y), m, inv);
+  bool my_near;
+  const uint32_t par = kv4_params(kv4_sat(ext.x), kv4_sat(-ext.y), m, inv, my_near);
+  const uint32_t near = __ballot_sync(0xffffffffu, my_near);
   constexpr int kBlock = kv4_block_bytes(HD);
   if (my_slot >= 0)
     reinterpret_cast<uint32_t*>(p.pool + ((long long)(my_slot / kPage) * p.Hkv + h) * kBlock + kPage * HD)[
@@ -225,12 +227,15 @@ __global__ void __launch_bounds__(256) kv4_write_kernel(const __grid_constant__ 
     uint32_t code[2];
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
-      const uint32_t tp = __shfl_sync(0xffffffffu, par, kv * 16 + tok);
-      const float ti = __shfl_sync(0xffffffffu, inv, kv * 16 + tok);
-      const float2 ms = __half22float2(*reinterpret_cast<const __half2*>(&tp));
+      const float tm = __shfl_sync(0xffffffffu, m, kv * 16 + tok), ti = __shfl_sync(0xffffffffu, inv, kv * 16 + tok);
       float x[8];
       kv4_floats<BF16>(w[kv][it], in_range, x);
-      code[kv] = kv4_codes(x, ms.x, ms.y, ti);
+      if (near >> (kv * 16 + it * T) & ((1u << T) - 1u)) {
+        const uint32_t s = __shfl_sync(0xffffffffu, par, kv * 16 + tok) >> 16;
+        code[kv] = kv4_codes_near(x, tm, __half2float(__ushort_as_half((unsigned short)s)), ti);
+      } else {
+        code[kv] = kv4_codes(x, tm, ti);
+      }
     }
     const uint32_t other = __shfl_xor_sync(0xffffffffu, code[1], L);
     if (slot < 0) continue;
@@ -369,8 +374,9 @@ __global__ void kv4_fill_kernel(uint8_t* pool, long long layer_bytes, const int3
       const float2 ext = kv4_unpack2<false>(kv4_extremes<false, kLanes>(w));
       kv4_floats<false>(w, true, x);
       float m, inv;
-      const uint32_t par = kv4_params(ext.x, -ext.y, m, inv);
-      const uint32_t code = kv4_codes(x, m, __half2float(__ushort_as_half((unsigned short)(par >> 16))), inv);
+      bool near;
+      const uint32_t par = kv4_params(ext.x, -ext.y, m, inv, near);
+      const uint32_t code = kv4_codes_near(x, m, __half2float(__ushort_as_half((unsigned short)(par >> 16))), inv);
       if (j8 == 0) reinterpret_cast<uint32_t*>(block + kPage * HD)[kv * kPage + t] = par;
       if (kv == 0) {
         reinterpret_cast<uint32_t*>(block + t * (HD / 2))[j8] = code;
