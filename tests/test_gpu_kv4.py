@@ -172,6 +172,29 @@ def test_quotients_next_to_a_half(hd):
         assert torch.equal(got.cpu(), ref)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_many_rows_with_a_few_that_need_saturating(dtype, hd):
+    """More rows than warps hold at once, at odd positions, in two sequences: every value as the oracle
+    holds it, also beside rows with infinities, NaN, values past fp16 (bf16) and no spread."""
+    spec = spec_()
+    Hkv, lens, first = 8, [2603, 3000], [3, 62]
+    assert sum(lens) * Hkv > 152 * 64 * 256 // hd
+    c = Cache([n + f for n, f in zip(lens, first)], Hkv, hd, seed=hd)
+    g = torch.Generator().manual_seed(hd)
+    k, v = (torch.randn(sum(lens), Hkv, hd, generator=g) * torch.exp(torch.randn(sum(lens), Hkv, 1, generator=g)) for _ in range(2))
+    k[17, 3, 5], k[18, 3], v[700, 0, 0], v[701, 7, 63], k[2602, 1, 9] = float("nan"), 2.5, float("inf"), float("-inf"), 1e30
+    k, v = k.to(dtype), v.to(dtype)
+    start = torch.tensor(first, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, lens[0], sum(lens)], dtype=torch.int32, device="cuda")
+    spec.spec_kv4_write(k.cuda(), v.cuda(), start, c.table, c.pool, row_off=off)
+    for x, y in zip((k, v), spec.spec_kv4_read(c.pool, start, c.table, sum(lens), row_off=off, dtype=dtype)):
+        ref = O.held(np64(x))
+        if dtype == torch.float16:
+            ref = np.minimum(ref, O.HALF_MAX)              # what a read gives at most
+        assert (np.abs(np64(y) - ref) <= STEP[dtype] * np.abs(ref) + 2.0 ** -25 + 2.0 ** -23 * np.abs(ref)).all()
+
+
 @pytest.mark.parametrize("hd", [64, 128])
 def test_write_touches_its_cells_only(hd):
     """Neighbours in the page, other pages and other heads keep their bytes; a token at a time gives
