@@ -83,14 +83,15 @@ SPEC_DEVICE_INLINE uint32_t kv4_codes(const float (&x)[8], float m, float inv) {
   }
   return w - 0x4b400000u * 0x11111111u;
 }
-// The same for rows that are near: a code that is too large leaves d - s c, whose bits fit
-// a float, below -s/2.
+// The same for rows that are near: a code c is too large where d < (c - 1/2) s.  c - 1/2 is
+// exact, and an fma's sign is that of the exact d - (c - 1/2) s.  (d - s c itself need not fit
+// a float: for c = 1 and d the last number below s/2 it rounds to -s/2.)
 SPEC_DEVICE_INLINE uint32_t kv4_codes_near(const float (&x)[8], float m, float s, float inv) {
   uint32_t w = 0;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
     const float d = __fsub_rn(x[i], m), f = __fmaf_rn(d, inv, 12582912.f);
-    w = (w << 4) + __float_as_uint(f) - (__fmaf_rn(__fsub_rn(f, 12582912.f), -s, d) < -0.5f * s ? 1u : 0u);
+    w = (w << 4) + __float_as_uint(f) - (__fmaf_rn(__fsub_rn(f, 12582912.f) - 0.5f, -s, d) < 0.f ? 1u : 0u);
   }
   return w - 0x4b400000u * 0x11111111u;
 }
