@@ -7,6 +7,8 @@
 //   c  = floor((x' - m) / s + 1/2), 0 where s = 0        (a half goes up)
 // and stands for s * c + m, which a read rounds once to the caller's type.  Rounding
 // s up and m down keeps every quotient inside [0, 15], so no code needs a clamp.
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "kv4.h"
 #include "kvstate.cuh"
@@ -162,7 +164,7 @@ SPEC_DEVICE_INLINE void kv4_floats(const uint32_t (&w)[4], bool in_range, float 
 // fills a pair of cells, the lanes of the two rows exchange halves and move whole words.
 //
 // What bounds them: HBM for many rows.  262144 rows of 8 heads (head_dim 128) are read in
-// 207 us, 0.97 of the measured copy rate over 1.36 GB; a write of 65536 rows and their
+// 207 us (either type), 0.97 of the measured copy rate over 1.36 GB; a write of 65536 rows and their
 // reading back take 125 us, 0.80 of it, of which the write is 75: its instructions.  (One
 // row per half-warp, with every address and division computed by all of its lanes and
 // int-to-float conversions, took 282 and 188: the special-function and integer pipes were
@@ -256,19 +258,38 @@ __global__ void __launch_bounds__(256, RPW == 16 ? 3 : 1) kv4_write_kernel(const
   }
 }
 
+// s * c + m, or the odd one of the two floats around it: an inexact sum is then never a tie of
+// bf16's, so rounding it to bf16 next is one rounding in all.
+SPEC_DEVICE_INLINE float kv4_value_odd(uint32_t c, float s, float m) {
+  const float lo = __fmaf_rd((float)c, s, m), hi = __fmaf_ru((float)c, s, m);
+  return __float_as_uint(lo) & 1u ? lo : hi;
+}
+
 // s * c + m of eight codes, rounded once to the caller's type.  fp16: a nibble OR-ed under
 // 0x6400 (or 0x5400, one nibble up) is the number 1024 + c (64 + c), so a subtraction gives
-// c exactly and one fused multiply-add the result.  `sat`: 15 s + m may pass 65504 (by at most
-// 16: s is rounded up); the result is then held to it.
+// c exactly and one fused multiply-add the result.  bf16: the sum is rounded to fp32 on the way,
+// which most parameters leave exact: s c + m is a multiple of the smaller one's last bit (2^-11
+// of it at least) and below 2 max(15 s, |m|).  CARE, where kv4_care says so of a row of
+// the warp: the results are held to 65504 (fp16), the sums are kept odd (bf16; for all rows it
+// cost a fifth of a large read: 262144 rows of 8 heads 250 against 207 us).
 template <bool BF16>
-SPEC_DEVICE_INLINE uint4 kv4_expand8(uint32_t code, uint32_t par, bool sat) {
+SPEC_DEVICE_INLINE bool kv4_care(uint32_t par) {
+  const float2 ms = __half22float2(*reinterpret_cast<const __half2*>(&par));
+  const float m = fabsf(ms.x), s = ms.y;
+  if (BF16) return m > 0.f && s > 0.f && fmaxf(m, 15.f * s) > 4096.f * fminf(m, s);
+  return fmaf(15.f, s, ms.x) > 65504.f;  // by at most 16: s is rounded up
+}
+template <bool BF16, bool CARE>
+SPEC_DEVICE_INLINE uint4 kv4_expand8(uint32_t code, uint32_t par) {
   uint32_t o[4];
   if (BF16) {
     const float2 ms = __half22float2(*reinterpret_cast<const __half2*>(&par));
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = kv4_pack2<true>(__fmaf_rn((float)((code >> (8 * i)) & 15u), ms.y, ms.x),
-                             __fmaf_rn((float)((code >> (8 * i + 4)) & 15u), ms.y, ms.x));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c0 = (code >> (8 * i)) & 15u, c1 = (code >> (8 * i + 4)) & 15u;
+      o[i] = CARE ? kv4_pack2<true>(kv4_value_odd(c0, ms.y, ms.x), kv4_value_odd(c1, ms.y, ms.x))
+                  : kv4_pack2<true>(__fmaf_rn((float)c0, ms.y, ms.x), __fmaf_rn((float)c1, ms.y, ms.x));
+    }
     return make_uint4(o[0], o[1], o[2], o[3]);
   }
   const uint32_t m2 = __byte_perm(par, par, 0x1010), s2 = __byte_perm(par, par, 0x3232);
@@ -280,7 +301,7 @@ SPEC_DEVICE_INLINE uint4 kv4_expand8(uint32_t code, uint32_t par, bool sat) {
   for (int i = 0; i < 4; ++i) {
     const __half2 c = __hsub2(*reinterpret_cast<const __half2*>(&raw[i]), __float2half2_rn(i & 1 ? 64.f : 1024.f));
     __half2 r = __hfma2(c, *reinterpret_cast<const __half2*>(&s2), *reinterpret_cast<const __half2*>(&m2));
-    if (sat) r = __hmin2(r, __float2half2_rn(65504.f));
+    if (CARE) r = __hmin2(r, __float2half2_rn(65504.f));
     v[i] = *reinterpret_cast<uint32_t*>(&r);
   }
   return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
@@ -322,22 +343,25 @@ __global__ void __launch_bounds__(256) kv4_read_kernel(const __grid_constant__ K
       vc[it] = *reinterpret_cast<const uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8)) |
                ((uint32_t)*reinterpret_cast<const uint16_t*>(v + kv4_v_piece<HD>(t, j8 * 8 + 4)) << 16);
   }
-  const float2 ms = __half22float2(*reinterpret_cast<const __half2*>(&par));
-  const bool sat = __any_sync(0xffffffffu, fmaf(15.f, ms.y, ms.x) > 65504.f);
+  const auto expand = [&](auto care) {
+    constexpr bool kCare = decltype(care)::value;
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int tok = it * T + lane / L, odd = tok & 1;
-    const int slot = __shfl_sync(0xffffffffu, my_slot, tok), other_slot = __shfl_sync(0xffffffffu, my_slot, tok ^ 1);
-    const uint32_t kp = __shfl_sync(0xffffffffu, par, tok), vp = __shfl_sync(0xffffffffu, par, 16 + tok);
-    const uint32_t other = __shfl_xor_sync(0xffffffffu, vc[it], L);
-    uint32_t v = vc[it];
-    if (slot >= 0 && other_slot == (slot ^ 1) && odd == (slot & 1))
-      v = odd ? __byte_perm(other, v, 0x7632) : __byte_perm(v, other, 0x5410);
-    if (slot == -2) continue;               // past the last row, or a row of no sequence
-    const long long at = ((long long)(r0 + tok) * p.Hkv + h) * L + j8;
-    __stcs(reinterpret_cast<uint4*>(p.k) + at, kv4_expand8<BF16>(kc[it], kp, sat));
-    __stcs(reinterpret_cast<uint4*>(p.v) + at, kv4_expand8<BF16>(v, vp, sat));
-  }
+    for (int it = 0; it < IT; ++it) {
+      const int tok = it * T + lane / L, odd = tok & 1;
+      const int slot = __shfl_sync(0xffffffffu, my_slot, tok), other_slot = __shfl_sync(0xffffffffu, my_slot, tok ^ 1);
+      const uint32_t kp = __shfl_sync(0xffffffffu, par, tok), vp = __shfl_sync(0xffffffffu, par, 16 + tok);
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, vc[it], L);
+      uint32_t v = vc[it];
+      if (slot >= 0 && other_slot == (slot ^ 1) && odd == (slot & 1))
+        v = odd ? __byte_perm(other, v, 0x7632) : __byte_perm(v, other, 0x5410);
+      if (slot == -2) continue;             // past the last row, or a row of no sequence
+      const long long at = ((long long)(r0 + tok) * p.Hkv + h) * L + j8;
+      __stcs(reinterpret_cast<uint4*>(p.k) + at, kv4_expand8<BF16, kCare>(kc[it], kp));
+      __stcs(reinterpret_cast<uint4*>(p.v) + at, kv4_expand8<BF16, kCare>(v, vp));
+    }
+  };
+  if (__any_sync(0xffffffffu, kv4_care<BF16>(par))) expand(std::true_type{});
+  else expand(std::false_type{});
 }
 
 // Pseudo-random cells.  grid (pages, n_layers, n); each block fills one page of one layer.
