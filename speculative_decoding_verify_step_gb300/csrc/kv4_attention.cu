@@ -6,7 +6,7 @@
 //   O[r]    = sum_k P (s_k c_k + m_k) = sum_k (P s_k) c_k + sum_k P m_k
 // so the tensor cores multiply the bare codes, and the two parameters of a token are
 // applied to its score and its weight, in fp32.  Softmax is taken in one pass over
-// the pages with a running maximum and sum per row.
+// the pages with a running maximum (of P s, below) and sum per row.
 //
 // Codes as fp16.  A nibble left in place, x & 0x000f000f, is a pair of fp16
 // subnormals c * 2^-24 (x & 0x00f000f0: c * 2^-20), which the tensor cores multiply
@@ -19,8 +19,8 @@
 // narrow window costs half.  S comes out as [token, row]; one movmatrix per 8 x 8
 // tile turns the weights into the B operand of the PV product.
 //
-// Rounding.  P s_k is rounded to fp16 (scaled by a power of two that follows the
-// largest s seen, so small scales stay normal numbers).  c lies in 0..15, so that
+// Rounding.  P s_k is rounded to fp16: by 2^-11 of itself, or 2^-25 of the row's largest P s_k
+// where it is subnormal (see the running maximum below).  c lies in 0..15, so that
 // rounding would weigh on c's mean of 7.5 as well; the kernel sums the rounded
 // weights R with one more MMA per step (A = ones) and forms
 //   O = sum (P s)_fp16 c - 7.5 R + sum P (m + 7.5 s),
@@ -61,10 +61,15 @@
 // instructions, and the phases between its two barriers per tile do not overlap; 24 rows
 // of 8 x 32768 tokens took 246 against 116 us, 60 rows 364 against 306.
 //
-// The running maximum moves only when a score passes it by more than 2^8: the
-// barrier (or vote) carries that question, and the exchange of maxima and the
-// rescaling of the accumulators are a rare branch.  Weights are then at most 2^8
-// times 2^4 (the same slack for the scale of V), far below fp16's largest.
+// The running maximum of a row is that of t = score + floor(log2 s), s being V's scale, over the
+// tokens the row sees: a token that it does not see, or hardly weighs, may have any scale.
+// (One exponent for all rows, of the largest s alone, left the other weights few bits beside
+// one such token.)  The weights are 2^(score - maximum), so their products with s lie
+// below 2^9 and the largest is at least 1; the weights themselves and their sums, in fp32, may
+// pass 2^32 where s is tiny.  The maximum of a row moves only when a t passes it by more than 8:
+// the barrier (or vote) carries that question, asked of the largest score and the largest s of a
+// thread's tokens, and the exact maxima, their exchange and the rescaling of the accumulators
+// are a rare branch.  What a row does not see leaves no trace in its result.
 #include <math.h>
 
 #include <algorithm>
@@ -82,7 +87,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kMaxStages = 24;        // pages of a CTA's ring
 constexpr float kNoMax = -1e30f;      // running maximum of a row that has seen no token
-constexpr float kSlack = 8.f;         // how far (log2) a score may pass the running maximum
+constexpr float kSlack = 8.f;         // how far t may pass the running maximum
 
 SPEC_DEVICE_INLINE float ex2(float x) {
   float y;
@@ -106,6 +111,12 @@ SPEC_DEVICE_INLINE void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// floor(log2 s) of a parameter word; -24, the least scale's, where s is 0.
+SPEC_DEVICE_INLINE float log2_scale(uint32_t w) {
+  const uint32_t e = __float_as_uint(__half2float(__ushort_as_half((unsigned short)(w >> 16)))) >> 23;
+  return fmaxf(__uint_as_float(0x4b000000u | e) - 8388735.f, -24.f);
 }
 
 // 8 x 8 transpose of 16-bit elements across the warp.
@@ -321,10 +332,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   uint8_t* const qfrag = smem + S * C::kBlock;
   __shared__ uint64_t full[kMaxStages];
   __shared__ float4 s_row[ROWS / 2];          // rows 2i, 2i + 1: sums of q, factors to exp2 units
-  __shared__ float2 s_max[TEAMS][ROWS / 2];   // running maxima
+  __shared__ float2 s_max[TEAMS][ROWS / 2];   // running maxima of t
   __shared__ float s_red[kWarps][ROWS], s_red2[kWarps][ROWS];
   __shared__ uint64_t received;               // partials of the cluster's CTAs
-  __shared__ uint32_t s_smax[kWarps];
   __shared__ uint32_t s_anc[16];
   __shared__ int s_fail;
 
@@ -497,12 +507,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     lrow[nt][0] = lrow[nt][1] = zrow[nt][0] = zrow[nt][1] = 0.f;
   }
   uint32_t vw[2 * MT];                      // V parameter words of the lane's tokens
-  uint32_t s_lim = 1;                       // V scales (fp16 bits) below this keep 2^-e
-  float inv_e = 1.f;                        // 2^-e: the weights are P s 2^-e
 
   const int kk = tw * MT * 16 + g;          // this lane's first token in a page
-  // Scores of page j (in stage s, phase parity par) into sc; returns whether a score or a
-  // scale passes its limit.
+  // Scores of page j (in stage s, phase parity par) into sc; returns whether a t may pass its
+  // row's maximum by more than the slack.
   auto scores = [&](int j, int s, uint32_t par) -> bool {
     if (j - base >= 32) {
       base += 32;
@@ -587,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
       ks[t] = f.y;
       smax = max(smax, vw[t]);
     }
-    bool over = (smax >> 16) >= s_lim;
+    const float lim = kSlack - log2_scale(smax);
+    bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float4 row = s_row[nt * 4 + c];
@@ -618,22 +627,25 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
         m0 = fmaxf(m0, sc[nt][t >> 1][(t & 1) * 2]);
         m1 = fmaxf(m1, sc[nt][t >> 1][(t & 1) * 2 + 1]);
       }
-      over |= fmaf(m0, row.z, -top.x) > kSlack || fmaf(m1, row.w, -top.y) > kSlack;
+      over |= fmaf(m0, row.z, -top.x) > lim || fmaf(m1, row.w, -top.y) > lim;
     }
     return over;
   };
 
-  // Move the running maxima (and 2^-e) to what this page's scores and scales ask for and
-  // rescale the accumulators.
+  // Move the running maxima that a t of this page passes by more than the slack, and rescale the
+  // accumulators.
   auto raise_max = [&] {
+    float lg[2 * MT];
+#pragma unroll
+    for (int t = 0; t < 2 * MT; ++t) lg[t] = log2_scale(vw[t]);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float4 row = s_row[nt * 4 + c];
-      float m0 = sc[nt][0][0], m1 = sc[nt][0][1];
+      float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-      for (int t = 1; t < 2 * MT; ++t) {
-        m0 = fmaxf(m0, sc[nt][t >> 1][(t & 1) * 2]);
-        m1 = fmaxf(m1, sc[nt][t >> 1][(t & 1) * 2 + 1]);
+      for (int t = 0; t < 2 * MT; ++t) {
+        m0 = fmaxf(m0, fmaf(sc[nt][t >> 1][(t & 1) * 2], row.z, lg[t]));
+        m1 = fmaxf(m1, fmaf(sc[nt][t >> 1][(t & 1) * 2 + 1], row.w, lg[t]));
       }
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
@@ -641,47 +653,31 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
         m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
       }
       if (g == 0) {
-        s_red[warp][nt * 8 + 2 * c] = m0 * row.z;
-        s_red[warp][nt * 8 + 2 * c + 1] = m1 * row.w;
+        s_red[warp][nt * 8 + 2 * c] = m0;
+        s_red[warp][nt * 8 + 2 * c + 1] = m1;
       }
     }
-    uint32_t smax = 0;
-#pragma unroll
-    for (int t = 0; t < 2 * MT; ++t) smax = max(smax, vw[t]);
-    smax = __reduce_max_sync(0xffffffffu, smax) >> 16;
-    if (lane == 0) s_smax[warp] = smax;
     team_sync<TW>();
+    // the maximum of row r, `old` until now
+    const auto raised = [&](float old, int r) {
+      float m = s_red[team * TW][r];
 #pragma unroll
-    for (int w = 0; w < TW; ++w) smax = max(smax, s_smax[team * TW + w]);
-    float re = 1.f;
-    if (smax >= s_lim) {
-      const uint32_t e = __float_as_uint(__half2float(__ushort_as_half((unsigned short)smax))) >> 23;
-      const float now = __uint_as_float((254u - e) << 23);
-      re = now / inv_e;
-      inv_e = now;
-      // the limit is 2^4 times the power of two at or below smax
-      s_lim = __half_as_ushort(__float2half_rn(fminf(__uint_as_float((e + 4u) << 23), 65504.f)));
-      if (s_lim == 0x7bffu) s_lim = 0x7c00u;
-    }
+      for (int w = 1; w < TW; ++w) m = fmaxf(m, s_red[team * TW + w][r]);
+      return m - old > kSlack ? m : old;
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const float2 old = s_max[team][nt * 4 + c];
-      float2 now = old;
-#pragma unroll
-      for (int w = 0; w < TW; ++w) {
-        now.x = fmaxf(now.x, s_red[team * TW + w][nt * 8 + 2 * c]);
-        now.y = fmaxf(now.y, s_red[team * TW + w][nt * 8 + 2 * c + 1]);
-      }
-      const float a0 = ex2(old.x - now.x), a1 = ex2(old.y - now.y);
+      const float a0 = ex2(old.x - raised(old.x, nt * 8 + 2 * c)), a1 = ex2(old.y - raised(old.y, nt * 8 + 2 * c + 1));
 #pragma unroll
       for (int t = 0; t < PW; ++t) {
-        acc[nt][t][0] *= a0 * re;
-        acc[nt][t][1] *= a1 * re;
-        acc[nt][t][2] *= a0 * re;
-        acc[nt][t][3] *= a1 * re;
+        acc[nt][t][0] *= a0;
+        acc[nt][t][1] *= a1;
+        acc[nt][t][2] *= a0;
+        acc[nt][t][3] *= a1;
       }
-      accr[nt][0] *= a0 * re;
-      accr[nt][1] *= a1 * re;
+      accr[nt][0] *= a0;
+      accr[nt][1] *= a1;
       lrow[nt][0] *= a0;
       lrow[nt][1] *= a1;
       zrow[nt][0] *= a0;
@@ -690,10 +686,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     team_sync<TW>();
     for (int r = tw * 32 + lane; r < ROWS; r += TW * 32) {
       float* top = reinterpret_cast<float*>(s_max[team]) + r;
-      float m = *top;
-#pragma unroll
-      for (int w = 0; w < TW; ++w) m = fmaxf(m, s_red[team * TW + w][r]);
-      *top = m;
+      *top = raised(*top, r);
     }
     team_sync<TW>();
   };
@@ -705,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&vw[2 * t + u]));
-      vs[u] = f.y * inv_e;
+      vs[u] = f.y;
       vz[u] = fmaf(7.5f, f.y, f.x);
     }
 #pragma unroll
@@ -833,7 +826,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   }
   __syncthreads();
   // The teams' partials: sums over the team's tokens, then O, in the ring's place.
-  const float e_up = 1.f / inv_e;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float2 l = make_float2(lrow[nt][0], lrow[nt][1]), z = make_float2(zrow[nt][0], zrow[nt][1]);
@@ -847,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     if (g == 0) {
       s_red[warp][nt * 8 + 2 * c] = l.x;
       s_red[warp][nt * 8 + 2 * c + 1] = l.y;
-      s_red2[warp][nt * 8 + 2 * c] = z.x - 7.5f * e_up * accr[nt][0];
-      s_red2[warp][nt * 8 + 2 * c + 1] = z.y - 7.5f * e_up * accr[nt][1];
+      s_red2[warp][nt * 8 + 2 * c] = z.x - 7.5f * accr[nt][0];
+      s_red2[warp][nt * 8 + 2 * c + 1] = z.y - 7.5f * accr[nt][1];
     }
   }
   team_sync<TW>();
@@ -862,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
       float bias = 0.f;
 #pragma unroll
       for (int w = 0; w < TW; ++w) bias += s_red2[team * TW + w][r];
-      const float u0 = e_up * 16777216.f, u1 = e_up * 1048576.f;
+      constexpr float u0 = 16777216.f, u1 = 1048576.f;  // a nibble left in place is c 2^-24 or 2^-20
       float* o = part + (team * ROWS + r) * REC + g * (HD / 8) + piece0 * 4;
       if constexpr (PW == 1)
         *reinterpret_cast<float2*>(o + (tw & 1) * 2) =
