@@ -889,7 +889,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
           bulk_push(mapa_u32(smem_u32(recv + piece * n * REC), threadIdx.x), part + threadIdx.x * share * REC, n * REC * 4,
                     mapa_u32(smem_u32(&received), threadIdx.x));
       }
+      __syncwarp();
+      cluster_arrive();  // this CTA's copies are issued
       const bool ok = mbar_wait(&received, 0, p.status);
+      __syncwarp();
+      cluster_wait();
+      // all copies are issued, also those of a CTA that this one did not wait out: they land now
+      if (!ok) (void)mbar_wait(&received, 0, nullptr);
       __syncwarp();
       cluster_arrive();  // all copies to this CTA have landed: when all have, no source is needed
       for (int it = threadIdx.x; it < own * V4; it += kThreads) {
