@@ -363,6 +363,14 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
 #pragma unroll
     for (int i = 0; i < TEAMS; ++i) s_max[i][threadIdx.x] = make_float2(kNoMax, kNoMax);
 
+  // this CTA's share of the next projections' weights
+  auto prefetch_next = [&] {
+    if (threadIdx.x == kThreads - 1) {
+      l2_prefetch_share(p.l2_next[0], p.l2_next_bytes[0]);
+      l2_prefetch_share(p.l2_next[1], p.l2_next_bytes[1]);
+    }
+  };
+
   int kvh, piece, pieces, slot = 0;
   Kv4Seq seq;
   if constexpr (CL) {
@@ -376,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     const Kv4Plan plan = kv4_plan(p, mine);
     if ((int)blockIdx.x >= plan.total) {
       if (p.early) pdl_wait();  // the grid's end stands for the predecessor's, too
+      prefetch_next();
       return;
     }
     int before, before_cut;
@@ -451,10 +460,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   }
   if (warp == 0)
     for (; issued < min(S, npg); ++issued) issue(issued, issued);
-  if (threadIdx.x == kThreads - 1) {
-    l2_prefetch_share(p.l2_next[0], p.l2_next_bytes[0]);
-    l2_prefetch_share(p.l2_next[1], p.l2_next_bytes[1]);
-  }
+  prefetch_next();
 #pragma unroll
   for (int k = 0; k < QP; ++k) {
     const uint32_t in[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
