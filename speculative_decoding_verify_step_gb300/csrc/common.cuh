@@ -177,6 +177,8 @@ SPEC_DEVICE_INLINE uint64_t l2_policy_evict_first() {
 // memory writes become visible to the cluster) and wait (acquire).  Every thread
 // of every CTA in the cluster takes part, a whole warp at a time.
 SPEC_DEVICE_INLINE void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// The first half without the release, for a phase that only counts arrivals.
+SPEC_DEVICE_INLINE void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 SPEC_DEVICE_INLINE void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // Shared-memory address `a` of this CTA mapped into the shared memory of cluster

@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
                     mapa_u32(smem_u32(&received), threadIdx.x));
       }
       __syncwarp();
-      cluster_arrive();  // this CTA's copies are issued
+      cluster_arrive_relaxed();  // this CTA's copies are issued (with the release a round of 32 layers took 10 us more)
       const bool ok = mbar_wait(&received, 0, p.status);
       __syncwarp();
       cluster_wait();

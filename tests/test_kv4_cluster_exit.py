@@ -10,7 +10,7 @@ import re
 
 SRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "speculative_decoding_verify_step_gb300", "csrc",
                    "kv4_attention.cu")
-OPS = {"bulk_push": "PUSH", "mbar_wait": "RECEIVE", "cluster_arrive": "ARRIVE", "cluster_wait": "AWAIT"}
+OPS = {"bulk_push": "PUSH", "mbar_wait": "RECEIVE", "cluster_arrive": "ARRIVE", "cluster_arrive_relaxed": "ARRIVE", "cluster_wait": "AWAIT"}
 
 
 def protocol():
@@ -21,7 +21,7 @@ def protocol():
     merge = kernel[kernel.index("if constexpr (CL)", first):]
     merge = merge[:merge.index("return;")]
     ops = [("ARRIVE", False)]
-    for hit in re.finditer(r"(if \(!ok\)[^;{]*?)?\b(bulk_push|mbar_wait|cluster_arrive|cluster_wait)\(", merge):
+    for hit in re.finditer(r"(if \(!ok\)[^;{]*?)?\b(bulk_push|mbar_wait|cluster_arrive_relaxed|cluster_arrive|cluster_wait)\(", merge):
         ops.append((OPS[hit.group(2)], bool(hit.group(1))))
     return ops
 
