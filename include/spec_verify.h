@@ -351,7 +351,7 @@ spec_status spec_kv_write(spec_model* m, int32_t seq_id, int32_t n_tokens, const
  * [B + 1], non-decreasing, row_off[0] >= 0), or rows_per_seq rows each where row_off
  * is NULL (total_rows = B * rows_per_seq).  Its rows sit at token positions start[b],
  * start[b] + 1, ... (device [B]) of page_table[b] (device [B, max_pages], entries in
- * 0..num_pages-1).  Rows of no sequence are left as they are.  A position past the
+ * 0..num_pages-1).  Rows of no sequence are left as they are.  A position below 0 or past the
  * page table, or whose page entry is outside the pool (-1: none), has no cell: it is
  * not written, reads as zeros and is never attended to.
  * dtype (SPEC_F16 or SPEC_BF16) is the type of the caller's k, v, q and out.  Strides

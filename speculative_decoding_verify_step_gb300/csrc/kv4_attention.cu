@@ -163,8 +163,8 @@ SPEC_DEVICE_INLINE Kv4Seq kv4_seq(const Kv4AttnParams& p, int b) {
   s.row0 = max(0, min(s.row0, p.total_rows));
   s.Wb = max(0, min(min(s.Wb, p.W), p.total_rows - s.row0));
   const int cap = p.max_pages * kPage;
-  s.L = max(0, min(p.kv_len[b], cap));
-  s.n_keys = s.sid >= 0 && s.sid < p.table_rows && s.Wb > 0 ? min(s.L + s.Wb, cap) : 0;
+  s.L = max(-kMaxWidth, min(p.kv_len[b], cap));  // below 0: the window's first rows have no cell
+  s.n_keys = s.sid >= 0 && s.sid < p.table_rows && s.Wb > 0 ? max(0, min(s.L + s.Wb, cap)) : 0;
   s.pages = (s.n_keys + kPage - 1) / kPage;
   return s;
 }
