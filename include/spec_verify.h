@@ -411,14 +411,16 @@ spec_status spec_kv_fill_random(spec_model* m, int32_t n, const int32_t* seq_ids
                                 uint64_t seed, float scale, void* stream);
 
 /* Per-kernel timing for reports.  While enabled, every weight-streaming
- * projection launch and every attention launch of a forward is bracketed by CUDA
- * events on the call's stream (this serialises those launches; use it in a
- * separate measuring pass), and no kernel prefetches the next kernel's weights
- * into L2, so every launch is timed on the bytes it moves itself.  Classes: 0 QKV, 1 O, 2 gate/up, 3 down, 4 LM head,
- * 5 attention (+ merge).  spec_read_profile synchronises the device, adds the
- * recorded durations to ms[6] and launch counts to launches[6], and its
- * algorithmic HBM bytes (weights; K/V pages read) to bytes[6], then clears the
- * record.  At most 1024 launches are recorded between two reads. */
+ * projection launch and every attention launch of a forward (with a 4-bit cache
+ * also every write of a window's cells) is bracketed by CUDA events on the call's
+ * stream (this serialises those launches; use it in a separate measuring pass),
+ * and no kernel prefetches the next kernel's weights into L2, so every launch is
+ * timed on the bytes it moves itself.  Classes: 0 QKV, 1 O, 2 gate/up, 3 down,
+ * 4 LM head, 5 attention (+ merge; the write of the cells counts as a launch of its
+ * own).  spec_read_profile synchronises the device, adds the recorded durations to
+ * ms[6] and launch counts to launches[6], and its algorithmic HBM bytes (weights;
+ * K/V pages read; rows read and cells written) to bytes[6], then clears the record.
+ * At most 1024 launches are recorded between two reads. */
 spec_status spec_set_profiling(spec_model* m, int32_t enable);
 spec_status spec_read_profile(spec_model* m, double* ms, int64_t* launches, double* bytes);
 

@@ -304,6 +304,8 @@ spec_status forward(spec_model* m, int B, int W, const int32_t* seq_ids, const i
   const long long bound = std::min<long long>(max_len_bound(m) + W, c.max_seq_len);
   const double tok_bytes = m->kv4 ? (double)kv4_block_bytes(hd) / kPage : 2.0 * 2.0 * hd;  // K and V of one kv head
   const double kv_bytes = tok_bytes * Hkv * (double)B * (double)bound;
+  // fp16 rows read, cells written by a launch of their own
+  const double kv4_write_bytes = (4.0 * hd + tok_bytes) * Hkv * (double)M;
   // While a short-context attention runs, HBM has room for about kAttnL2Budget
   // bytes beyond the attention's own K/V: that much of the O projection's and
   // then the gate/up projection's weights is prefetched into L2 (none once the
@@ -389,7 +391,7 @@ spec_status forward(spec_model* m, int B, int W, const int32_t* seq_ids, const i
     if (m->kv4) {
       kw.pool = m->kv4_pool + l * m->kv4_layer;
       ka.pool = kw.pool;
-      CUDA_TRY(launch_kv4_write(kw, st));
+      CUDA_TRY(profiled(m, 5, kv4_write_bytes, st, [&] { return launch_kv4_write(kw, st); }));
       for (int i = 0; i < 2; ++i) {
         ka.l2_next[i] = ap.l2_next[i];
         ka.l2_next_bytes[i] = ap.l2_next_bytes[i];
