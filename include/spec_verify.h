@@ -388,7 +388,8 @@ spec_status spec_kv4_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
  * scale * (q . k) with |scale| <= 2^40, softmax in fp32, one rounding of the result
  * (weights are fp16 with fp32 accumulation).  out may be q.  A row that sees nothing is
  * zeros.  Rows of a sequence beyond W are left as they are.
- * W * (n_heads / n_kv_heads) <= 64.  max_kv_len: an upper bound of kv_len for the
+ * W * (n_heads / n_kv_heads) <= 64, B and n_kv_heads <= 65535, max_pages and num_pages
+ * <= 2^24, B * n_kv_heads * max_pages <= 2^30.  max_kv_len: an upper bound of kv_len for the
  * launch shape, 0: unknown (results do not depend on it beyond the order of the
  * sums, not even where it is too small).  workspace: device memory of spec_kv4_attention_workspace() bytes for the same
  * arguments (0: none needed, may be NULL; -1: a shape the call refuses), 16-byte aligned,

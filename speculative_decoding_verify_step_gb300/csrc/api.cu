@@ -1463,6 +1463,17 @@ spec_status kv4_check_stride(long long stride, long long least, const char* name
   return SPEC_OK;
 }
 
+// The shapes of an attention call.
+spec_status kv4_check_window(int B, int W, int Hq, int Hkv, int max_pages, int max_kv_len) {
+  if (Hq < 1 || Hq % Hkv) return fail(SPEC_ERR_INVALID_ARG, "n_heads=%d must be a multiple of n_kv_heads=%d", Hq, Hkv);
+  if ((long long)W * (Hq / Hkv) > 64)
+    return fail(SPEC_ERR_UNSUPPORTED, "width * group size must be <= 64 (%d * %d)", W, Hq / Hkv);
+  if ((long long)B * Hkv * max_pages > (1 << 30))
+    return fail(SPEC_ERR_UNSUPPORTED, "B * n_kv_heads * max_pages must be at most 2^30");
+  if (max_kv_len < 0) return fail(SPEC_ERR_INVALID_ARG, "max_kv_len is negative");
+  return SPEC_OK;
+}
+
 // Upper bound of a sequence's cached and window tokens, for the launch shape.
 int kv4_len_hint(int max_pages, int max_kv_len, int W) {
   const long long cap = std::min<long long>((long long)max_pages * kPage, 0x40000000ll);
@@ -1548,8 +1559,9 @@ spec_status spec_kv4_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
 
 int64_t spec_kv4_attention_workspace(int32_t B, int32_t W, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                      int32_t max_pages, int32_t max_kv_len) {
-  if (B < 1 || W < 1 || W > kMaxWidth || n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads || max_pages < 1 ||
-      max_kv_len < 0 || (long long)W * (n_heads / n_kv_heads) > 64 || (head_dim != 64 && head_dim != 128))
+  // ragged rows, none of them: the rest of the shape is what is asked
+  if (W < 1 || W > kMaxWidth || kv4_check(B, 0, W, &max_pages, max_pages, 1, n_kv_heads, head_dim, SPEC_F16) ||
+      kv4_check_window(B, W, n_heads, n_kv_heads, max_pages, max_kv_len))
     return -1;
   int sms = 0;
   if (current_sm_count(&sms) != cudaSuccess) return -1;
@@ -1564,14 +1576,8 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
                                void* out, void* workspace, int64_t workspace_bytes, void* stream) {
   if (W < 1 || W > kMaxWidth) return fail(SPEC_ERR_INVALID_ARG, "width %d outside 1..%d", W, kMaxWidth);
   if (spec_status s = kv4_check(B, total_rows, W, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype)) return s;
-  if (n_heads < 1 || n_heads % n_kv_heads)
-    return fail(SPEC_ERR_INVALID_ARG, "n_heads=%d must be a multiple of n_kv_heads=%d", n_heads, n_kv_heads);
-  if ((long long)W * (n_heads / n_kv_heads) > 64)
-    return fail(SPEC_ERR_UNSUPPORTED, "width * group size must be <= 64 (%d * %d)", W, n_heads / n_kv_heads);
-  if ((long long)B * n_kv_heads * max_pages > (1 << 30))
-    return fail(SPEC_ERR_UNSUPPORTED, "B * n_kv_heads * max_pages must be at most 2^30");
+  if (spec_status s = kv4_check_window(B, W, n_heads, n_kv_heads, max_pages, max_kv_len)) return s;
   if (!(std::fabs(scale) <= 1099511627776.f)) return fail(SPEC_ERR_INVALID_ARG, "|scale| must be at most 2^40");
-  if (max_kv_len < 0) return fail(SPEC_ERR_INVALID_ARG, "max_kv_len is negative");
   int depth[16];
   uint32_t anc[16];
   if (parent_host) {
