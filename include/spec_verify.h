@@ -112,7 +112,7 @@ spec_status spec_model_create(const spec_config* cfg, spec_model** out);
  * 128, 3.56x at 64.  Every call of this header works on either; a window's K and V are
  * quantised as they are written, so its rows attend to the held values and a verify
  * round sees what decode steps would have left.  Against an fp16 cache the logits move by
- * the 4-bit rounding. */
+ * the 4-bit rounding.  num_pages is at most 2^24 then. */
 typedef enum spec_kv_format { SPEC_KV_F16 = 0, SPEC_KV_INT4 = 1 } spec_kv_format;
 spec_status spec_model_create_kv(const spec_config* cfg, int32_t kv_format, spec_model** out);
 

@@ -627,6 +627,8 @@ spec_status spec_model_create_kv(const spec_config* cfg, int32_t kv_format, spec
   if (kv_format != SPEC_KV_F16 && kv_format != SPEC_KV_INT4) return fail(SPEC_ERR_INVALID_ARG, "unknown kv_format %d", kv_format);
   spec_status s = validate_cfg(*cfg);
   if (s != SPEC_OK) return s;
+  if (kv_format == SPEC_KV_INT4 && cfg->num_pages > (1 << 24))  // an fp16 cache of as many has no room on the GPU
+    return fail(SPEC_ERR_INVALID_ARG, "num_pages=%d above 2^24", cfg->num_pages);
   int dev = 0;
   CUDA_TRY(cudaGetDevice(&dev));
   cudaDeviceProp prop;
