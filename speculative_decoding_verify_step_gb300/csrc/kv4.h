@@ -60,6 +60,7 @@ struct Kv4AttnParams {
   int max_pages, num_pages, table_rows;
   int sm_count, kv_len_hint;   // launch shape only
   float scale;                 // of q . k
+  float scale_m, scale_2;      // |scale| log2(e) as a mantissa in [1, 2) (or 0) times a power of two: set by the launcher
   uint32_t anc[16];            // window rows that row j sees (bit i)
   // Inside a model's forward: the cached pages and the sequence state were complete
   // before the predecessor let this kernel launch, so only q and the window's K/V

@@ -70,10 +70,19 @@
 // the barrier (or vote) carries that question, asked of the largest score and the largest s of a
 // thread's tokens, and the exact maxima, their exchange and the rescaling of the accumulators
 // are a rare branch.  What a row does not see leaves no trace in its result.
+//
+// Large scores.  Queries and keys of +-65504, or a large `scale`, take scores past 2^24, where a
+// float's last bit is a whole power of two of weight or more: score and maximum have to be numbers
+// of one grid, or the largest weight is off by any power.  So the mantissa of scale * log2(e) goes
+// into the products with s and m, and what is left of it for a row, with the row's own power of
+// two, only shifts the score: a product and a difference without rounding.  floor(log2 s) is added
+// to the score with a rounding towards the score, so the largest P s stays between
+// min(1, s) and max(2, s).
 #include <math.h>
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "kv4.cuh"
 #include "kv4.h"
@@ -117,6 +126,11 @@ SPEC_DEVICE_INLINE void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a
 SPEC_DEVICE_INLINE float log2_scale(uint32_t w) {
   const uint32_t e = __float_as_uint(__half2float(__ushort_as_half((unsigned short)(w >> 16)))) >> 23;
   return fmaxf(__uint_as_float(0x4b000000u | e) - 8388735.f, -24.f);
+}
+
+// score + lg, rounded towards the score.
+SPEC_DEVICE_INLINE float plus_log2(float score, float lg) {
+  return lg < 0.f ? __fadd_ru(score, lg) : __fadd_rd(score, lg);
 }
 
 // 8 x 8 transpose of 16-bit elements across the warp.
@@ -443,8 +457,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
   // Queries: a lane takes eight dims of a row, two rows (head_dim 64: four) at a time per
   // warp, all loads before the pages' (which they would queue behind).  Each row is scaled
   // by a power of two (largest element in [2^14, 2^15)), so the factor 1/16 of the odd
-  // columns costs no precision; the sum of the scaled row and the factor back to exp2 units
-  // are kept per row.
+  // columns costs no precision; the sum of the scaled row and the factor (a power of two) back to
+  // exp2 units are kept per row.
   constexpr int RPP = HD == 128 ? 2 : 4;                       // rows of a warp at a time
   constexpr int QP = (ROWS + kWarps * RPP - 1) / (kWarps * RPP);
   const int q_cc = lane & 3, q_w = lane / (4 * RPP);           // dims (q_cc WORDS + q_w) 8 ..
@@ -490,9 +504,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     if (r < ROWS) {
       if (q_cc == 0 && q_w == 0) {
         float* row = reinterpret_cast<float*>(&s_row[r >> 1]) + (r & 1);
-        row[0] = sum * 5.9604644775390625e-8f;  // in the units of the code products (2^-24)
-        row[2] = fmaxf(fabsf(p.scale) * 1.4426950408889634f * 16777216.f * __uint_as_float((uint32_t)(127 - sh) << 23),
-                       1e-30f);
+        row[0] = sum * (p.scale_m * 5.9604644775390625e-8f);  // in the units of the code products (2^-24)
+        row[2] = fmaxf(p.scale_2 * 16777216.f * __uint_as_float((uint32_t)(127 - sh) << 23), 0x1p-100f);
       }
       // fragment of lane (r % 8, q_cc), word q_w: halves (d0, d4) (d1, d5)/16 (d2, d6) (d3, d7)/16
       *reinterpret_cast<uint4*>(qfrag + (((r >> 3) * WORDS + q_w) * 32 + (r & 7) * 4 + q_cc) * 16) =
@@ -598,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
     for (int t = 0; t < 2 * MT; ++t) {
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&kw[t]));
       km[t] = f.x;
-      ks[t] = f.y;
+      ks[t] = f.y * p.scale_m;
       smax = max(smax, vw[t]);
     }
     const float lim = kSlack - log2_scale(smax);
@@ -650,8 +663,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
       float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 2 * MT; ++t) {
-        m0 = fmaxf(m0, fmaf(sc[nt][t >> 1][(t & 1) * 2], row.z, lg[t]));
-        m1 = fmaxf(m1, fmaf(sc[nt][t >> 1][(t & 1) * 2 + 1], row.w, lg[t]));
+        m0 = fmaxf(m0, plus_log2(sc[nt][t >> 1][(t & 1) * 2] * row.z, lg[t]));
+        m1 = fmaxf(m1, plus_log2(sc[nt][t >> 1][(t & 1) * 2 + 1] * row.w, lg[t]));
       }
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
@@ -669,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT, TW>::kCtas))
       float m = s_red[team * TW][r];
 #pragma unroll
       for (int w = 1; w < TW; ++w) m = fmaxf(m, s_red[team * TW + w][r]);
-      return m - old > kSlack ? m : old;
+      return m - old >= kSlack ? m : old;
     };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -1181,7 +1194,11 @@ long long kv4_attention_workspace(int B, int Hkv, int rows, int hd, int kv_len_h
   return 2ll * (nt <= 3 ? 4 : 3) * sm_count * nt * 8 * (hd + 2) * 4;
 }
 
-cudaError_t launch_kv4_attention(const Kv4AttnParams& p, cudaStream_t st) {
+cudaError_t launch_kv4_attention(const Kv4AttnParams& params, cudaStream_t st) {
+  Kv4AttnParams p = params;
+  int e = 0;
+  p.scale_m = 2.f * std::frexp(std::fabs(p.scale) * 1.4426950408889634f, &e);
+  p.scale_2 = std::ldexp(1.f, std::max(e - 1, -126));
   return p.hd == 128 ? launch_hd<128>(p, st) : launch_hd<64>(p, st);
 }
 
