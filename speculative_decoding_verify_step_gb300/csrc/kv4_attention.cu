@@ -26,9 +26,13 @@
 //   O = sum (P s)_fp16 c - 7.5 R + sum P (m + 7.5 s),
 // which leaves only the rounding of the weights of c - 7.5.  Everything else is fp32.
 //
-// Work split.  A group is a sequence and a kv head.  Long groups are cut into pieces of
-// about equal length, as many as the GPU holds CTAs; a CTA takes one piece.  A group of
-// one piece is finished there; the others leave partials (unnormalised O, running
+// Work split.  A group is a sequence and a kv head.  Groups longer than a common target are
+// cut into pieces of at most that many pages; a CTA takes one piece.  With few groups the target
+// gives about as many pieces as the GPU holds CTAs.  The more groups there are, up to that number,
+// the fewer cuts are left for the long ones (kv4_plan), and a batch of one long sequence
+// among short ones is unbalanced there: width 4, 36 x 1024 + 1 x 32768 tokens 184 us, with 37 x 1024,
+// where the rule for more groups than CTAs begins, 50; decode, 55 x 1024 + 1 x 65520 279, with 56 47.
+// A group of one piece is finished by its CTA; the others leave partials (unnormalised O, running
 // maximum and sum per row) in the workspace, and a second kernel merges them.  Short
 // caches need neither: the CTAs of a group are one thread-block cluster and merge
 // through distributed shared memory.  (One list of all pages cut into exactly equal
@@ -44,19 +48,23 @@
 // passing through shared memory.  Either way every code is unpacked once per CTA.  A
 // team of four keeps a warp's accumulators small (8 registers per 8 rows, against 32),
 // so wide windows fit, and has a page's result sooner; one warp needs no barriers.
-// Measured (head_dim 128, 8 kv heads; one warp, four): one row tile, 2 x 65520 tokens 32, 37
-// us; two, 8 x 32768 tokens 76, 83; three, 64 x 512-2048 tokens 63, 58 (8 x 32768 tokens 109,
-// 111).  In a team the scores of the next page are computed before the barrier that
+// Measured when the rule was made (head_dim 128, 8 kv heads; one warp, four): one row tile, 2 x
+// 65520 tokens 32, 37 us; two, 8 x 32768 tokens 76, 83; three, 64 x 512-2048 tokens 63, 58 (8 x
+// 32768 tokens 109, 111).  Teams of two warps have no figure: with the ring they had, a wait ran
+// out.  In a team the scores of the next page are computed before the barrier that
 // releases this page's weights: one barrier per page.
 //
 // What bounds it.  mma.sync runs at 8 cycles per m16n8k16 and SM quarter here and shares
 // its pipe with the fp32 instructions; AND and shift take 2 cycles, exp2 and movmatrix 4
 // (measured).  Per page and 16 query rows that is 272 + 75 cycles of the first pipe, 209
 // of the integer pipe and 48 of the special functions; HBM delivers a page per SM in
-// 390.  The pipes overlap little at two warps per SM quarter, so 16 rows run at about
-// 600 cycles a page and 8 rows at about 400, next to the memory's rate.  (More CTAs per
-// SM with spilled registers, half pages, and packed fp32 pairs -- 3 cycles each -- were
-// all slower.)  The wide windows were also built on tcgen05, codes unpacked into shared
+// 365 at the 1.87 GHz of these runs.  Registers allow two CTAs per SM at two row tiles (222 a
+// thread) and three at one (150), so two and three warps per SM quarter, and the pipes overlap
+// little: 8 x 32768 tokens at 16 rows take at most 566 cycles a page where an SM has two CTAs,
+// with 42% of the issue slots used, and 2 x 65520 tokens at 8 rows 460, prologue
+// included, with 46%.  (At one and two tiles more CTAs per SM, for which the loop spilled, half pages,
+// and packed fp32 pairs -- 3 cycles each -- were all slower.  Three and five tiles of 128 dims
+// spill a few words at their bound of four and three CTAs.)  The wide windows were also built on tcgen05, codes unpacked into shared
 // memory, S and O in tensor memory: with a token per thread a score costs twice the
 // instructions, and the phases between its two barriers per tile do not overlap; 24 rows
 // of 8 x 32768 tokens took 246 against 116 us, 60 rows 364 against 306.
