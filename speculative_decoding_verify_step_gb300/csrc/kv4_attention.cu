@@ -268,6 +268,13 @@ SPEC_DEVICE_INLINE float* kv4_partial(float* ws, int i, int rows, int hd) {
   return ws + (long long)i * rows * (hd + 2);
 }
 
+// Two output values as fp16, saturated; what is no number stays none.
+SPEC_DEVICE_INLINE uint32_t out_f16x2(float a, float b) {
+  const __half2 most = __float2half2_rn(65504.f);
+  const __half2 v = __hmin2_nan(__hmax2_nan(__floats2half2_rn(a, b), __hneg2(most)), most);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // Four output values of a row: o / l in the caller's type; a row that sees no token is zeros.
 SPEC_DEVICE_INLINE void store_row4(const Kv4AttnParams& p, int row, int head, int hd, int d4, float4 o, float l) {
   const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -276,7 +283,8 @@ SPEC_DEVICE_INLINE void store_row4(const Kv4AttnParams& p, int row, int head, in
     w.x = kv4_pack2<true>(o.x * inv, o.y * inv);
     w.y = kv4_pack2<true>(o.z * inv, o.w * inv);
   } else {
-    w = pack_act4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    w.x = out_f16x2(o.x * inv, o.y * inv);
+    w.y = out_f16x2(o.z * inv, o.w * inv);
   }
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + ((long long)row * p.Hq + head) * hd + d4 * 4) = w;
 }
