@@ -19,7 +19,7 @@
 
 namespace spec {
 bool g_use_pdl = true;
-int g_launch_count = 0;
+thread_local int g_launch_count = 0;
 void record_error(const char* msg);
 }  // namespace spec
 

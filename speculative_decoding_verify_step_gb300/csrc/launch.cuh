@@ -8,7 +8,7 @@
 
 namespace spec {
 
-extern int g_launch_count;
+extern thread_local int g_launch_count;  // of this host thread: calls may come from several
 
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
