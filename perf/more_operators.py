@@ -3,7 +3,7 @@ paged KV cache (written, attended over, cut down by accumulated attention weight
 sampler that turns draft logits into a token and the distribution q it was drawn from.
 
 The cache.  A page holds 64 tokens; per kv head it is four sub-blocks of 16 tokens.  A
-sub-block has one power-of-two scale 2^e for K and one for V (-16 <= e <= 8) and holds each
+sub-block has one power-of-two scale 2^e for K and one for V (-15 <= e <= 8) and holds each
 value x as the e4m3 number nearest to clamp(x, -65504, 65504) / 2^e (ties to even).  Writing the first
 token of a sub-block sets e to the least exponent whose 448 * 2^e reaches the largest of the
 call's values there; a later write into it only raises e, and what the sub-block held is then
@@ -171,10 +171,10 @@ def _clamped(x):
 
 
 def _exponent(a):
-    """Least e in -16..8 with a <= 448 * 2^e, for a >= 0."""
+    """Least e in -15..8 with a <= 448 * 2^e, for a >= 0."""
     m, x = torch.frexp(a)
     e = x - 9 + (m > 0.875).to(x.dtype)
-    return torch.where(a > 0, e, torch.full_like(e, -16)).clamp(-16, 8)
+    return torch.where(a > 0, e, torch.full_like(e, -15)).clamp(-15, 8)
 
 
 def _codes(x, e):
@@ -386,7 +386,7 @@ def _plain_write(s):
         most = torch.zeros(nblk, hkv, device=pos.device)
         most = most.scatter_reduce(0, blk.unsqueeze(1).expand(-1, hkv), new.abs().amax(-1), "amax")
         exp = _exponent(most)
-        was = torch.where(old.unsqueeze(1), e.view(-1, hkv)[seq], torch.full((), -16, dtype=e.dtype, device=pos.device))
+        was = torch.where(old.unsqueeze(1), e.view(-1, hkv)[seq], torch.full((), -15, dtype=e.dtype, device=pos.device))
         exp = exp.scatter_reduce(0, blk.unsqueeze(1).expand(-1, hkv), was, "amax")[blk].unsqueeze(-1)
         y = torch.where(old.view(-1, 1, 1), mine, new)
         out.append(_rounded(torch.ldexp(_codes(y, exp).float(), exp), s["dtype"]))
@@ -497,10 +497,10 @@ def _exact_held(y, first=None):
     n = len(y)
     y = torch.cat([y, y.new_zeros((-n % SUB,) + y.shape[1:])]).unflatten(0, (-1, SUB))
     a = y.abs().amax((1, 3))
-    e = torch.full_like(a, -16)
+    e = torch.full_like(a, -15)
     if first is not None and n:
         e[0] = first.double()
-    for k in range(-15, 9):
+    for k in range(-14, 9):
         e = torch.where((e <= k - 1) & (a > 448 * 2.0 ** (k - 1)), torch.full_like(e, k), e)
     unit = torch.exp2(e).view(-1, 1, y.shape[2], 1)
     scaled = y / unit
