@@ -404,6 +404,40 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
                                const int32_t* parent_host, float scale, int32_t max_kv_len, const void* pool,
                                void* out, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------ 8-bit paged KV cache (no model)
+ *
+ * The 4-bit cache's calls over a cache held in 8 bits: pages of 64 tokens, one block of
+ * spec_kv8_block_bytes(head_dim) = 128 * head_dim + 64 bytes per (page, kv head),
+ * [num_pages, n_kv_heads, block], 16-byte aligned; 1.99x smaller than fp16.  Each 16
+ * tokens of a page (a sub-block) have one power-of-two scale per kv head for K and one
+ * for V.  A value x is held as
+ *     x' = clamp(x, -65504, 65504), NaN -> -65504
+ *     c  = the e4m3 number nearest to x' / 2^e, ties to even; it stands for c * 2^e
+ * with -15 <= e <= 8.  A write of a sub-block's first token sets e to the least exponent
+ * with |x'| <= 448 * 2^e for all rows of the call in the sub-block; what the sub-block
+ * held behind them is lost.  A write of later tokens only raises e to hold its rows,
+ * and then the other tokens' values are rounded to the coarser grid (which changes none
+ * of 2^-6 * 2^e and above).  So what a cache holds may depend, by that much, on how
+ * its writes were split, and a write touches whole sub-blocks: within a call, and in
+ * calls that may overlap, a sub-block's rows belong to one sequence and one call.
+ * Rows, positions, row_off, start, page_table, dtype, strides, streams and positions
+ * without a cell are as in spec_kv4_write.  Bytes that were never written may hold
+ * anything: they have no effect on tokens that were. */
+int64_t spec_kv8_block_bytes(int32_t head_dim);
+
+/* Quantise rows k, v [total_rows, n_kv_heads, head_dim] into their cells. */
+spec_status spec_kv8_write(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                           const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* k, const void* v,
+                           int64_t k_stride, int64_t v_stride, void* pool, void* stream);
+
+/* Expand cells to k, v (contiguous [total_rows, n_kv_heads, head_dim]): c * 2^e, rounded
+ * once (fp16: at most 65504).  Positions without a cell read as zeros. */
+spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                          const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* pool, void* k, void* v,
+                          void* stream);
+
 /* Timing aid for long contexts: give each sequence (host ids) lens_host[b]
  * cached tokens with pseudo-random bf16 K/V (a hash of seed and position, scaled
  * by `scale`; quantised, if the cache is held in 4 bits), without running the model.  Attention time does not depend on

@@ -15,6 +15,8 @@
 #include "kernels.h"
 #include "kv4.cuh"
 #include "kv4.h"
+#include "kv8.cuh"
+#include "kv8.h"
 #include "sampling.cuh"
 
 namespace spec {
@@ -1626,6 +1628,65 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
     return fail(SPEC_ERR_INVALID_ARG, "workspace_bytes=%lld, %lld needed", (long long)workspace_bytes, need);
   p.workspace = static_cast<float*>(workspace);
   CUDA_TRY(launch_kv4_attention(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ 8-bit paged KV cache
+extern "C" {
+
+int64_t spec_kv8_block_bytes(int32_t head_dim) {
+  return head_dim == 64 || head_dim == 128 ? kv8_block_bytes(head_dim) : 0;
+}
+
+spec_status spec_kv8_write(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                           const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                           int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* k, const void* v,
+                           int64_t k_stride, int64_t v_stride, void* pool, void* stream) {
+  if (spec_status s = kv4_check(B, total_rows, rows_per_seq, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype))
+    return s;
+  if (total_rows == 0) return SPEC_OK;
+  if (!start || !page_table) return fail(SPEC_ERR_INVALID_ARG, "start or page_table is NULL");
+  if (spec_status s = kv4_check_ptr(k, "k")) return s;
+  if (spec_status s = kv4_check_ptr(v, "v")) return s;
+  if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
+  if (spec_status s = kv4_check_stride(k_stride, (long long)n_kv_heads * head_dim, "k_stride")) return s;
+  if (spec_status s = kv4_check_stride(v_stride, (long long)n_kv_heads * head_dim, "v_stride")) return s;
+  Kv8WriteParams p{};
+  p.rows = kv4_rows(B, rows_per_seq, total_rows, row_off, start, page_table, max_pages, num_pages);
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.bf16 = dtype == SPEC_BF16;
+  p.k = k;
+  p.v = v;
+  p.k_row_stride = k_stride;
+  p.v_row_stride = v_stride;
+  p.pool = static_cast<uint8_t*>(pool);
+  CUDA_TRY(launch_kv8_write(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, const int32_t* row_off,
+                          const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
+                          int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* pool, void* k, void* v,
+                          void* stream) {
+  if (spec_status s = kv4_check(B, total_rows, rows_per_seq, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype))
+    return s;
+  if (total_rows == 0) return SPEC_OK;
+  if (!start || !page_table) return fail(SPEC_ERR_INVALID_ARG, "start or page_table is NULL");
+  if (spec_status s = kv4_check_ptr(k, "k")) return s;
+  if (spec_status s = kv4_check_ptr(v, "v")) return s;
+  if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
+  Kv8ReadParams p{};
+  p.rows = kv4_rows(B, rows_per_seq, total_rows, row_off, start, page_table, max_pages, num_pages);
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.bf16 = dtype == SPEC_BF16;
+  p.k = k;
+  p.v = v;
+  p.pool = static_cast<const uint8_t*>(pool);
+  CUDA_TRY(launch_kv8_read(p, static_cast<cudaStream_t>(stream)));
   return SPEC_OK;
 }
 

@@ -45,7 +45,7 @@ EXPORTS = ["spec_model_create", "spec_model_destroy", "spec_model_set_weight", "
            "spec_set_profiling", "spec_read_profile", "spec_accept_greedy_noalloc", "spec_verify_ragged",
            "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write",
            "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention", "spec_kv4_attention_workspace",
-           "spec_model_create_kv"]
+           "spec_model_create_kv", "spec_kv8_block_bytes", "spec_kv8_write", "spec_kv8_read"]
 
 RAGGED_CAP_ACCEPT, RAGGED_COMPACT = 1, 2
 
@@ -100,6 +100,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_kv4_attention": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, I32, P, I64, P, F32, I32, P, P,
                                      P, I64, P]),
         "spec_kv4_attention_workspace": (I64, [I32, I32, I32, I32, I32, I32, I32]),
+        "spec_kv8_block_bytes": (I64, [I32]),
+        "spec_kv8_write": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, I64, I64, P, P]),
+        "spec_kv8_read": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -471,13 +474,13 @@ _KV4_HEAD_DIM = {4608: 64, 8704: 128}  # by the bytes of a (page, kv head) block
 _KV4_WORKSPACE = {}  # bytes by device index and the arguments of spec_kv4_attention_workspace
 
 
-def _kv4_geometry(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor, row_off):
+def _kv4_geometry(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor, row_off,
+                  head_dims=_KV4_HEAD_DIM, block: str = "64 * head_dim + 512", make: str = "spec_kv4_pool"):
     """Checked (num_pages, n_kv_heads, head_dim, B, max_pages) of a call's pool and tables."""
     ps, ts, i32 = pool.shape, page_table.shape, torch.int32
-    hd = _KV4_HEAD_DIM.get(ps[-1]) if len(ps) == 3 else None
+    hd = head_dims.get(ps[-1]) if len(ps) == 3 else None
     if hd is None or pool.dtype is not torch.uint8 or not pool.is_contiguous():
-        raise ValueError("pool must be a contiguous uint8 [num_pages, n_kv_heads, 64 * head_dim + 512] tensor "
-                         "(spec_kv4_pool)")
+        raise ValueError(f"pool must be a contiguous uint8 [num_pages, n_kv_heads, {block}] tensor ({make})")
     B = start.numel()
     if start.dtype is not i32 or start.dim() != 1 or not start.is_contiguous():
         raise ValueError("start / kv_len must be a contiguous int32 tensor of shape (B,)")
@@ -612,3 +615,65 @@ def spec_kv4_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
               hd ** -0.5 if scale is None else scale, max_kv_len, pool.data_ptr(), out.data_ptr(),
               None if ws is None else ws.data_ptr(), size)
     return out
+
+
+# ------------------------------------------------------------- 8-bit paged KV cache
+_KV8_HEAD_DIM = {8256: 64, 16448: 128}  # by the bytes of a (page, kv head) block
+
+
+def spec_kv8_pool(num_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
+    """An empty 8-bit KV pool: uint8 [num_pages, n_kv_heads, 128 * head_dim + 64], pages of
+    64 tokens."""
+    block = load_library().spec_kv8_block_bytes(int(head_dim))
+    if block == 0:
+        raise ValueError("head_dim must be 64 or 128")
+    return torch.zeros(num_pages, n_kv_heads, block, dtype=torch.uint8, device=device)
+
+
+def _kv8_geometry(pool, start, page_table, row_off):
+    return _kv4_geometry(pool, start, page_table, row_off, _KV8_HEAD_DIM, "128 * head_dim + 64", "spec_kv8_pool")
+
+
+def spec_kv8_write(k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor,
+                   pool: torch.Tensor, row_off: Optional[torch.Tensor] = None) -> None:
+    """Quantise K/V rows into the 8-bit cache: k, v [B, n, n_kv_heads, head_dim] at positions
+    start[b] .. start[b] + n - 1 of page_table[b], or packed [rows, n_kv_heads, head_dim]
+    with sequence b's rows row_off[b] .. row_off[b + 1] - 1.  fp16 or bf16.  16 tokens share a
+    power-of-two scale: a write raises it where its rows need that (what the 16 held is
+    rounded to the coarser grid), and writing the first of the 16 starts them anew."""
+    lib = _lib or load_library()
+    P, H, hd, B, width = _kv8_geometry(pool, start, page_table, row_off)
+    dev, ragged = pool.device, row_off is not None
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError("k and v must have one shape and type")
+    total, n, ks = _kv4_rows(k, "k", B, H, hd, ragged, dev)
+    _, _, vs = _kv4_rows(v, "v", B, H, hd, ragged, dev)
+    _kv4_call(dev, lib.spec_kv8_write, B, n, total, row_off.data_ptr() if ragged else None, start.data_ptr(),
+              page_table.data_ptr(), width, P, H, hd, _KV4_DTYPE[k.dtype], k.data_ptr(), v.data_ptr(),
+              ks, vs, pool.data_ptr())
+
+
+def spec_kv8_read(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor, n: int,
+                  row_off: Optional[torch.Tensor] = None, dtype: torch.dtype = torch.float16, outs=None):
+    """K and V of n tokens per sequence from position start[b] on, as fp16 or bf16
+    [B, n, n_kv_heads, head_dim]; with row_off, n rows in all, [n, n_kv_heads, head_dim].
+    Rows of no sequence are left unwritten.  `outs`: preallocated (k, v)."""
+    lib = _lib or load_library()
+    P, H, hd, B, width = _kv8_geometry(pool, start, page_table, row_off)
+    dev, ragged = pool.device, row_off is not None
+    n = int(n)
+    if dtype not in _KV4_DTYPE:
+        raise ValueError("dtype must be torch.float16 or torch.bfloat16")
+    if n < 0:
+        raise ValueError("n must not be negative")
+    shape = (n, H, hd) if ragged else (B, n, H, hd)
+    if outs is None:
+        outs = (torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev))
+    k, v = outs
+    for t in (k, v):
+        if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"outs must be contiguous {dtype} tensors of shape {shape} on {dev}")
+    _kv4_call(dev, lib.spec_kv8_read, B, 0 if ragged else n, n if ragged else B * n,
+              row_off.data_ptr() if ragged else None, start.data_ptr(), page_table.data_ptr(), width, P,
+              H, hd, _KV4_DTYPE[dtype], pool.data_ptr(), k.data_ptr(), v.data_ptr())
+    return k, v
