@@ -360,7 +360,7 @@ spec_status spec_kv_write(spec_model* m, int32_t seq_id, int32_t n_tokens, const
  * No call allocates or keeps state, so calls may run on any streams at once; calls
  * that write cells another call uses need the caller's ordering.  Two rows of one
  * write must not map to the same cell.  The streams' device must be current. */
-typedef enum spec_dtype { SPEC_F16 = 0, SPEC_BF16 = 1 } spec_dtype;
+typedef enum spec_dtype { SPEC_F16 = 0, SPEC_BF16 = 1, SPEC_F32 = 2 /* logits of spec_sample only */ } spec_dtype;
 
 /* Bytes of one (page, kv head) block; 0 for an unsupported head_dim. */
 int64_t spec_kv4_block_bytes(int32_t head_dim);
@@ -437,6 +437,29 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
                           const int32_t* start, const int32_t* page_table, int32_t max_pages, int32_t num_pages,
                           int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* pool, void* k, void* v,
                           void* stream);
+
+/* Draw one token per row from logits, and give the distribution it was drawn from: a
+ * drafter's x_i and q_i of spec_verify_step.  logits: device [rows, V] of type dtype
+ * (SPEC_F16, SPEC_BF16 or SPEC_F32), rows row_stride >= V elements apart.  u [rows] fp32
+ * in [0, 1).  Row r uses setting r / rows_per_setting of temperature, top_k, top_p, min_p
+ * (device arrays; each may be NULL: temperature_all for every row, the others off).
+ * With x_v = (l_v - max l) / temperature and R_v = floor(2^40 e^x_v) (e^x to about 2^-42
+ * of itself), tokens ranked by logit (equal ones: the lower index first), the kept tokens
+ * are the shortest of: the first top_k (0 or >= V: off); the shortest prefix whose summed
+ * R reaches ceil(top_p * the top-k's sum) (1: off); those with R_v >= min_p * 2^40, i.e.
+ * p_v >= min_p * max p (0: off).
+ * tokens [rows]: the first token whose running sum of kept R, by index, exceeds
+ * floor(floor(2^24 u) Z / 2^24), Z the sum of all kept R.  probs (may be NULL): [rows, V]
+ * fp32, R_v / Z of kept tokens, else 0.  temperature 0: the first of the largest logits;
+ * u is not read.  A NaN logit counts as -infinity; several +infinity share the mass.  A
+ * row without a logit above -infinity, or whose setting or u is out of range
+ * (temperature below 0, in (0, 1e-6), infinite or NaN; top_k < 0; top_p outside (0, 1];
+ * min_p outside [0, 1]; u outside [0, 1)), gets token -1 and a row of zeros.
+ * No call allocates or keeps state.  V <= 393216, rows <= 2^24.  u may be NULL where
+ * temperature is NULL and temperature_all 0. */
+spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dtype, int64_t row_stride, const float* u,
+                        float temperature_all, const float* temperature, const int32_t* top_k, const float* top_p,
+                        const float* min_p, int32_t rows_per_setting, int32_t* tokens, float* probs, void* stream);
 
 /* Timing aid for long contexts: give each sequence (host ids) lens_host[b]
  * cached tokens with pseudo-random bf16 K/V (a hash of seed and position, scaled

@@ -17,6 +17,7 @@
 #include "kv4.h"
 #include "kv8.cuh"
 #include "kv8.h"
+#include "sample.h"
 #include "sampling.cuh"
 
 namespace spec {
@@ -1687,6 +1688,43 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
   p.v = v;
   p.pool = static_cast<const uint8_t*>(pool);
   CUDA_TRY(launch_kv8_read(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+// ------------------------------------------------------------ sampling from logits
+spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dtype, int64_t row_stride, const float* u,
+                        float temperature_all, const float* temperature, const int32_t* top_k, const float* top_p,
+                        const float* min_p, int32_t rows_per_setting, int32_t* tokens, float* probs, void* stream) {
+  if (rows < 0 || rows > (1 << 24)) return fail(SPEC_ERR_INVALID_ARG, "rows=%d outside 0..2^24", rows);
+  if (V < 1 || V > sample_max_vocab())
+    return fail(SPEC_ERR_INVALID_ARG, "V=%d outside 1..%d", V, sample_max_vocab());
+  if (dtype != SPEC_F16 && dtype != SPEC_BF16 && dtype != SPEC_F32)
+    return fail(SPEC_ERR_INVALID_ARG, "dtype must be SPEC_F16, SPEC_BF16 or SPEC_F32");
+  if (row_stride < V) return fail(SPEC_ERR_INVALID_ARG, "row_stride=%lld is below V=%d", (long long)row_stride, V);
+  if (rows_per_setting < 1) return fail(SPEC_ERR_INVALID_ARG, "rows_per_setting must be at least 1");
+  if (!temperature && !(temperature_all == 0.f || (temperature_all >= 1e-6f && std::isfinite(temperature_all))))
+    return fail(SPEC_ERR_INVALID_ARG, "temperature must be 0 or a finite number from 1e-6 on");
+  if (rows == 0) return SPEC_OK;
+  if (!logits || !tokens) return fail(SPEC_ERR_INVALID_ARG, "NULL argument");
+  if (!u && (temperature || temperature_all != 0.f)) return fail(SPEC_ERR_INVALID_ARG, "sampling needs uniforms u");
+  if (reinterpret_cast<uintptr_t>(logits) & (dtype == SPEC_F32 ? 3u : 1u))
+    return fail(SPEC_ERR_INVALID_ARG, "logits are not aligned to their type");
+  SampleParams p{};
+  p.logits = logits;
+  p.row_stride = row_stride;
+  p.rows = rows;
+  p.V = V;
+  p.dtype = dtype;
+  p.u = u;
+  p.temperature_all = temperature_all;
+  p.temperature = temperature;
+  p.top_k = top_k;
+  p.top_p = top_p;
+  p.min_p = min_p;
+  p.rows_per_setting = rows_per_setting;
+  p.tokens = tokens;
+  p.probs = probs;
+  CUDA_TRY(launch_sample(p, static_cast<cudaStream_t>(stream)));
   return SPEC_OK;
 }
 

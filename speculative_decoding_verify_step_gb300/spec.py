@@ -45,7 +45,8 @@ EXPORTS = ["spec_model_create", "spec_model_destroy", "spec_model_set_weight", "
            "spec_set_profiling", "spec_read_profile", "spec_accept_greedy_noalloc", "spec_verify_ragged",
            "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write",
            "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention", "spec_kv4_attention_workspace",
-           "spec_model_create_kv", "spec_kv8_block_bytes", "spec_kv8_write", "spec_kv8_read"]
+           "spec_model_create_kv", "spec_kv8_block_bytes", "spec_kv8_write", "spec_kv8_read",
+           "spec_sample"]
 
 RAGGED_CAP_ACCEPT, RAGGED_COMPACT = 1, 2
 
@@ -103,6 +104,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_kv8_block_bytes": (I64, [I32]),
         "spec_kv8_write": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, I64, I64, P, P]),
         "spec_kv8_read": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, P]),
+        "spec_sample": (I32, [I32, I32, P, I32, I64, P, F32, P, P, P, P, I32, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -677,3 +679,70 @@ def spec_kv8_read(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Ten
               row_off.data_ptr() if ragged else None, start.data_ptr(), page_table.data_ptr(), width, P,
               H, hd, _KV4_DTYPE[dtype], pool.data_ptr(), k.data_ptr(), v.data_ptr())
     return k, v
+
+
+# ------------------------------------------------------------- sampling from logits
+_SAMPLE_DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _setting(t, dtype, n: int, dev, what: str):
+    """None, or a contiguous [n] tensor of `dtype` on dev (a number counts for all)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        t = torch.as_tensor(t)
+        if t.dim() == 0:
+            t = t.expand(n)
+    if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        t = t.to(device=dev, dtype=dtype).contiguous()
+    if t.numel() != n:
+        raise ValueError(f"{what} must have {n} entries")
+    return t
+
+
+def spec_sample(logits: torch.Tensor, u: Optional[torch.Tensor] = None, temperature=1.0, top_k=None, top_p=None,
+                min_p=None, rows_per_setting: int = 1, return_probs: bool = False, outs=None):
+    """One token per row of logits [..., V] (fp32, bf16 or fp16; [rows, V] may be strided) from
+    uniforms u [...] in [0, 1), and with return_probs the distribution q it was drawn from: a
+    drafter's x and q of spec_verify_step.  temperature (0: the largest logit; u may be None),
+    top_k, top_p, min_p: a number for all rows, or one for each rows_per_setting rows (None:
+    off).  Returns (tokens int32 [...], probs fp32 [..., V] or None); a row without a logit
+    above -infinity, or with a setting or u out of range, gives -1 and zeros.  `outs`:
+    preallocated (tokens, probs or None)."""
+    lib = _lib or load_library()
+    dtype, shape, dev = _SAMPLE_DTYPE.get(logits.dtype), logits.shape, logits.device
+    if dtype is None or not logits.is_cuda or len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("logits must be a CUDA tensor [..., V] of type fp32, bf16 or fp16")
+    V, lead = shape[-1], shape[:-1]
+    rows = logits.numel() // V
+    if logits.is_contiguous():
+        stride = V
+    elif len(shape) == 2 and (logits.stride(1) == 1 or V == 1) and logits.stride(0) >= V:
+        stride = logits.stride(0)
+    else:
+        raise ValueError("each row of logits must be contiguous and, where rows are strided, logits [rows, V]")
+    if rows_per_setting < 1:
+        raise ValueError("rows_per_setting must be at least 1")
+    n = -(-rows // rows_per_setting)
+    t_all = 0.0
+    if isinstance(temperature, (int, float)):
+        t_all, temperature = float(temperature), None
+    else:
+        temperature = _setting(temperature, torch.float32, n, dev, "temperature")
+    u = _setting(u, torch.float32, rows, dev, "u")
+    top_k = _setting(top_k, torch.int32, n, dev, "top_k")
+    top_p = _setting(top_p, torch.float32, n, dev, "top_p")
+    min_p = _setting(min_p, torch.float32, n, dev, "min_p")
+    if outs is None:
+        outs = (torch.empty(lead, dtype=torch.int32, device=dev),
+                torch.empty(shape, dtype=torch.float32, device=dev) if return_probs else None)
+    tokens, probs = outs
+    if tokens.dtype is not torch.int32 or tokens.device != dev or tokens.shape != lead or not tokens.is_contiguous():
+        raise ValueError(f"tokens must be a contiguous int32 tensor of shape {tuple(lead)} on {dev}")
+    if probs is not None and (probs.dtype is not torch.float32 or probs.device != dev or probs.shape != shape
+                              or not probs.is_contiguous()):
+        raise ValueError(f"probs must be a contiguous fp32 tensor of shape {tuple(shape)} on {dev}")
+    ptr = [None if t is None else t.data_ptr() for t in (u, temperature, top_k, top_p, min_p, probs)]
+    _kv4_call(dev, lib.spec_sample, rows, V, logits.data_ptr(), dtype, stride, ptr[0], t_all, *ptr[1:5],
+              rows_per_setting, tokens.data_ptr(), ptr[5])
+    return tokens, probs
