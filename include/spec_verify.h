@@ -438,6 +438,21 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
                           int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* pool, void* k, void* v,
                           void* stream);
 
+/* Attention of the verify window over the cache: spec_kv4_attention's arguments and rules.
+ * weight (may be NULL): device [B, n_kv_heads, weight_len] fp32; weight[b, h, t] grows by
+ * the attention weights that the rows of sequence b's window give token t (positions below
+ * weight_len), summed over the window's rows and the query heads of kv head h: what
+ * spec_kv8_evict ranks by.  workspace: spec_kv8_attention_workspace() bytes for the same
+ * arguments (-1: a shape the call refuses), as there. */
+int64_t spec_kv8_attention_workspace(int32_t B, int32_t W, int32_t total_rows, int32_t n_heads, int32_t n_kv_heads,
+                                     int32_t head_dim, int32_t max_pages, int32_t with_weight);
+spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
+                               const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t n_heads,
+                               int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* q, int64_t q_stride,
+                               const int32_t* parent_host, float scale, int32_t max_kv_len, const void* pool,
+                               void* out, float* weight, int64_t weight_len, void* workspace, int64_t workspace_bytes,
+                               void* stream);
+
 /* Draw one token per row from logits, and give the distribution it was drawn from: a
  * drafter's x_i and q_i of spec_verify_step.  logits: device [rows, V] of type dtype
  * (SPEC_F16, SPEC_BF16 or SPEC_F32), rows row_stride >= V elements apart.  u [rows] fp32

@@ -1691,6 +1691,76 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
   return SPEC_OK;
 }
 
+int64_t spec_kv8_attention_workspace(int32_t B, int32_t W, int32_t total_rows, int32_t n_heads, int32_t n_kv_heads,
+                                     int32_t head_dim, int32_t max_pages, int32_t with_weight) {
+  // as ragged rows: any number of them
+  if (W < 1 || W > kMaxWidth ||
+      kv4_check(B, total_rows, W, &max_pages, max_pages, 1, n_kv_heads, head_dim, SPEC_F16) ||
+      kv4_check_window(B, W, n_heads, n_kv_heads, max_pages, 0))
+    return -1;
+  int sms = 0;
+  if (current_sm_count(&sms) != cudaSuccess) return -1;
+  return kv8_attention_workspace(W, n_heads, n_kv_heads, head_dim, total_rows, with_weight != 0, sms);
+}
+
+spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
+                               const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t n_heads,
+                               int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* q, int64_t q_stride,
+                               const int32_t* parent_host, float scale, int32_t max_kv_len, const void* pool,
+                               void* out, float* weight, int64_t weight_len, void* workspace, int64_t workspace_bytes,
+                               void* stream) {
+  if (W < 1 || W > kMaxWidth) return fail(SPEC_ERR_INVALID_ARG, "width %d outside 1..%d", W, kMaxWidth);
+  if (spec_status s = kv4_check(B, total_rows, W, row_off, max_pages, num_pages, n_kv_heads, head_dim, dtype)) return s;
+  if (spec_status s = kv4_check_window(B, W, n_heads, n_kv_heads, max_pages, max_kv_len)) return s;
+  if (!(std::fabs(scale) <= 1099511627776.f)) return fail(SPEC_ERR_INVALID_ARG, "|scale| must be at most 2^40");
+  if (weight && (weight_len < 1 || weight_len > (1ll << 40)))
+    return fail(SPEC_ERR_INVALID_ARG, "weight_len=%lld outside 1..2^40", (long long)weight_len);
+  int depth[16];
+  uint32_t anc[16];
+  if (parent_host) {
+    if (spec_status s = tree_masks(W, parent_host, depth, anc)) return s;
+  } else {
+    chain_masks(W, depth, anc);
+  }
+  if (total_rows == 0) return SPEC_OK;
+  if (!kv_len || !page_table) return fail(SPEC_ERR_INVALID_ARG, "kv_len or page_table is NULL");
+  if (spec_status s = kv4_check_ptr(q, "q")) return s;
+  if (spec_status s = kv4_check_ptr(out, "out")) return s;
+  if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
+  if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
+  if (reinterpret_cast<uintptr_t>(weight) & 3u) return fail(SPEC_ERR_INVALID_ARG, "weight must be 4-byte aligned");
+  if (spec_status s = kv4_check_stride(q_stride, (long long)n_heads * head_dim, "q_stride")) return s;
+  Kv8AttnParams p{};
+  p.q = q;
+  p.q_row_stride = q_stride;
+  p.out = out;
+  p.bf16 = dtype == SPEC_BF16;
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.page_table = page_table;
+  p.kv_len = kv_len;
+  p.row_off = row_off;
+  p.B = B;
+  p.W = W;
+  p.total_rows = total_rows;
+  p.Hq = n_heads;
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.scale = scale;
+  for (int j = 0; j < 16; ++j) p.anc[j] = j < W ? anc[j] : 0u;
+  p.kv_len_hint = kv4_len_hint(max_pages, max_kv_len, W);
+  p.weight = weight;
+  p.weight_len = weight_len;
+  CUDA_TRY(current_sm_count(&p.sm_count));
+  const long long need = kv8_attention_workspace(W, n_heads, n_kv_heads, head_dim, total_rows, weight != nullptr, p.sm_count);
+  if (workspace_bytes < need)
+    return fail(SPEC_ERR_INVALID_ARG, "workspace_bytes=%lld, %lld needed", (long long)workspace_bytes, need);
+  p.workspace = static_cast<float*>(workspace);
+  CUDA_TRY(launch_kv8_attention(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
 // ------------------------------------------------------------ sampling from logits
 spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dtype, int64_t row_stride, const float* u,
                         float temperature_all, const float* temperature, const int32_t* top_k, const float* top_p,

@@ -46,7 +46,7 @@ EXPORTS = ["spec_model_create", "spec_model_destroy", "spec_model_set_weight", "
            "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write",
            "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention", "spec_kv4_attention_workspace",
            "spec_model_create_kv", "spec_kv8_block_bytes", "spec_kv8_write", "spec_kv8_read",
-           "spec_sample"]
+           "spec_kv8_attention", "spec_kv8_attention_workspace", "spec_sample"]
 
 RAGGED_CAP_ACCEPT, RAGGED_COMPACT = 1, 2
 
@@ -104,6 +104,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_kv8_block_bytes": (I64, [I32]),
         "spec_kv8_write": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, I64, I64, P, P]),
         "spec_kv8_read": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, P]),
+        "spec_kv8_attention_workspace": (I64, [I32, I32, I32, I32, I32, I32, I32, I32]),
+        "spec_kv8_attention": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, I32, P, I64, P, F32, I32, P, P,
+                                     P, I64, P, I64, P]),
         "spec_sample": (I32, [I32, I32, P, I32, I64, P, F32, P, P, P, P, I32, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -621,6 +624,7 @@ def spec_kv4_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
 
 # ------------------------------------------------------------- 8-bit paged KV cache
 _KV8_HEAD_DIM = {8256: 64, 16448: 128}  # by the bytes of a (page, kv head) block
+_KV8_WORKSPACE = {}  # bytes by device index and the arguments of spec_kv8_attention_workspace
 
 
 def spec_kv8_pool(num_pages: int, n_kv_heads: int, head_dim: int, device="cuda") -> torch.Tensor:
@@ -679,6 +683,58 @@ def spec_kv8_read(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Ten
               row_off.data_ptr() if ragged else None, start.data_ptr(), page_table.data_ptr(), width, P,
               H, hd, _KV4_DTYPE[dtype], pool.data_ptr(), k.data_ptr(), v.data_ptr())
     return k, v
+
+
+def _kv8_weight(weight: torch.Tensor, what: str, B: int, H: int, dev) -> int:
+    """Tokens of a checked weight tensor."""
+    s = weight.shape
+    if (weight.dtype is not torch.float32 or weight.device != dev or len(s) != 3 or s[0] != B or s[1] != H or s[2] < 1
+            or not weight.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous fp32 tensor of shape ({B}, {H}, tokens) on {dev}")
+    return s[2]
+
+
+def spec_kv8_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                       row_off: Optional[torch.Tensor] = None, max_width: Optional[int] = None,
+                       parent: Optional[Sequence[int]] = None, scale: Optional[float] = None, max_kv_len: int = 0,
+                       out: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of verify windows over the 8-bit cache: spec_kv4_attention's arguments and
+    rules.  weight [B, n_kv_heads, tokens] fp32: grows by the attention weight that each token
+    gets, summed over the window's rows and the query heads of a kv head (for spec_kv8_evict)."""
+    lib = _lib or load_library()
+    P, H, hd, B, width = _kv8_geometry(pool, kv_len, page_table, row_off)
+    dev, ragged = pool.device, row_off is not None
+    total, W, qs = _kv4_rows(q, "q", B, None, hd, ragged, dev)
+    Hq = q.shape[-2]
+    if ragged:
+        W = max_width if max_width is not None else max(1, min(16, 64 // max(1, Hq // H)))
+        if not 1 <= W <= 16:
+            raise ValueError(f"max_width {W} outside 1..16")
+    elif max_width is not None and max_width < W:
+        raise ValueError(f"q has {W} rows per sequence, more than max_width {max_width}")
+    par = None
+    if parent is not None:
+        if len(parent) < W:
+            raise ValueError(f"parent must have {W} entries")
+        par = _i32_host(parent)
+    T = 0 if weight is None else _kv8_weight(weight, "weight", B, H, dev)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.dtype != q.dtype or out.device != dev or out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
+    key = (dev.index, B, W, total, Hq, H, hd, width, int(T > 0))
+    size = _KV8_WORKSPACE.get(key)
+    if size is None:
+        if len(_KV8_WORKSPACE) > 4096:
+            _KV8_WORKSPACE.clear()
+        with torch.cuda.device(dev):
+            size = _KV8_WORKSPACE[key] = lib.spec_kv8_attention_workspace(*key[1:])
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size > 0 else None
+    _kv4_call(dev, lib.spec_kv8_attention, B, W, total, row_off.data_ptr() if ragged else None, kv_len.data_ptr(),
+              page_table.data_ptr(), width, P, Hq, H, hd, _KV4_DTYPE[q.dtype], q.data_ptr(), qs, par,
+              hd ** -0.5 if scale is None else scale, max_kv_len, pool.data_ptr(), out.data_ptr(),
+              None if weight is None else weight.data_ptr(), T, None if ws is None else ws.data_ptr(), size)
+    return out
 
 
 # ------------------------------------------------------------- sampling from logits
