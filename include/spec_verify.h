@@ -453,6 +453,23 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
                                void* out, float* weight, int64_t weight_len, void* workspace, int64_t workspace_bytes,
                                void* stream);
 
+/* Cut caches down to `keep` tokens.  Of sequence b's n = min(kv_len[b], 64 * max_pages,
+ * weight_len) tokens, m = min(n, keep) stay for each kv head h: the last `recent` (0..keep),
+ * and of the others those of the largest weight[b, h, .] (equal ones: the earlier token; NaN
+ * counts as the smallest).  Outputs: new_len [B] = m; kept [B, n_kv_heads, keep] = their
+ * positions, rising, -1 behind the last; weight_out [B, n_kv_heads, weight_out_len] = their
+ * weights, zeros behind (weight_out_len >= keep); and their K and V in cells 0..m-1 of
+ * dst_table [B, dst_pages] (64 * dst_pages >= keep), as if the held values were written
+ * there in one call.  The pages of dst_table are pages of the same pool, named once, that
+ * page_table does not name in this call (a page shared with another sequence stays as it is;
+ * the caller frees the old ones).  Positions without a cell move as zeros; tokens whose
+ * destination is no page are dropped.  Keys keep the rotation they were written with. */
+spec_status spec_kv8_evict(int32_t B, const int32_t* kv_len, const int32_t* page_table, int32_t max_pages,
+                           const int32_t* dst_table, int32_t dst_pages, int32_t num_pages, int32_t n_kv_heads,
+                           int32_t head_dim, int32_t keep, int32_t recent, const float* weight, int64_t weight_len,
+                           void* pool, int32_t* new_len, int32_t* kept, float* weight_out, int64_t weight_out_len,
+                           void* stream);
+
 /* Draw one token per row from logits, and give the distribution it was drawn from: a
  * drafter's x_i and q_i of spec_verify_step.  logits: device [rows, V] of type dtype
  * (SPEC_F16, SPEC_BF16 or SPEC_F32), rows row_stride >= V elements apart.  u [rows] fp32

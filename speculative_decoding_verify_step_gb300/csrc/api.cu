@@ -1761,6 +1761,51 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
   return SPEC_OK;
 }
 
+spec_status spec_kv8_evict(int32_t B, const int32_t* kv_len, const int32_t* page_table, int32_t max_pages,
+                           const int32_t* dst_table, int32_t dst_pages, int32_t num_pages, int32_t n_kv_heads,
+                           int32_t head_dim, int32_t keep, int32_t recent, const float* weight, int64_t weight_len,
+                           void* pool, int32_t* new_len, int32_t* kept, float* weight_out, int64_t weight_out_len,
+                           void* stream) {
+  if (spec_status s = kv4_check(B, 0, 0, nullptr, max_pages, num_pages, n_kv_heads, head_dim, SPEC_F16)) return s;
+  if (keep < 1 || keep > (1 << 24)) return fail(SPEC_ERR_INVALID_ARG, "keep=%d outside 1..2^24", keep);
+  if (recent < 0 || recent > keep) return fail(SPEC_ERR_INVALID_ARG, "recent=%d outside 0..keep=%d", recent, keep);
+  if (dst_pages < 1 || dst_pages > (1 << 24) || (long long)dst_pages * kPage < keep)
+    return fail(SPEC_ERR_INVALID_ARG, "dst_pages=%d do not hold keep=%d tokens (or exceed 2^24)", dst_pages, keep);
+  if (weight_len < 1 || weight_len > (1ll << 30))
+    return fail(SPEC_ERR_INVALID_ARG, "weight_len=%lld outside 1..2^30", (long long)weight_len);
+  if (weight_out_len < keep || weight_out_len > (1ll << 30))
+    return fail(SPEC_ERR_INVALID_ARG, "weight_out_len=%lld outside keep=%d..2^30", (long long)weight_out_len, keep);
+  if (!kv_len || !page_table || !dst_table || !weight || !new_len || !kept || !weight_out)
+    return fail(SPEC_ERR_INVALID_ARG, "NULL argument");
+  if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
+  if ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(weight_out)) & 3u)
+    return fail(SPEC_ERR_INVALID_ARG, "weight and weight_out must be 4-byte aligned");
+  const long long groups = (long long)B * n_kv_heads;
+  if (weight < weight_out + groups * weight_out_len && weight_out < weight + groups * weight_len)
+    return fail(SPEC_ERR_INVALID_ARG, "weight_out overlaps weight");
+  Kv8EvictParams p{};
+  p.pool = static_cast<uint8_t*>(pool);
+  p.kv_len = kv_len;
+  p.page_table = page_table;
+  p.dst_table = dst_table;
+  p.weight = weight;
+  p.new_len = new_len;
+  p.kept = kept;
+  p.weight_out = weight_out;
+  p.weight_len = weight_len;
+  p.weight_out_len = weight_out_len;
+  p.B = B;
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.max_pages = max_pages;
+  p.dst_pages = dst_pages;
+  p.num_pages = num_pages;
+  p.keep = keep;
+  p.recent = recent;
+  CUDA_TRY(launch_kv8_evict(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
 // ------------------------------------------------------------ sampling from logits
 spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dtype, int64_t row_stride, const float* u,
                         float temperature_all, const float* temperature, const int32_t* top_k, const float* top_p,

@@ -1,0 +1,312 @@
+// Eviction from the 8-bit paged cache by accumulated attention weight.
+//
+// Of the n tokens of a sequence and kv head, m = min(keep, n) stay: the last `recent`, and
+// of the others those of the largest weight, the earlier of equal ones.  They move, in
+// order, to cells 0..m-1 of the destination table's pages; a destination sub-block gets the
+// least exponents that hold its tokens, as if the held values were written there.
+//
+// Two kernels.  The first takes one CTA per (sequence, kv head): its weights, as integers
+// that order like them, come into shared memory once (up to 48 K tokens; of longer ones
+// they are read from L2 again) and a radix select of 11, 11 and 10 bits finds the
+// threshold.  11 bits, because weights spread over exponents: with 8 most lanes of a warp
+// would add to the same counter.  Warps own runs of neighbouring tokens, so the tokens that
+// stay come out in order from two scans of 32 counts.  The second kernel takes one warp per
+// destination sub-block and head.  A token's K is one run of bytes, its V one byte of each
+// word of a run four times as long (four tokens share the words), so V is read up to four
+// times over where neighbours do not stay together.
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kv4.cuh"
+#include "kv8.cuh"
+#include "kv8.h"
+#include "launch.cuh"
+
+namespace spec {
+
+namespace {
+
+constexpr int kPickThreads = 1024;
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kPickKeys = 48 * 1024;  // weights held in shared memory
+
+// Orders like the weight; NaN lowest, -0 as 0.
+SPEC_DEVICE_INLINE uint32_t weight_key(float w) {
+  if (!(w == w)) return 0u;
+  const uint32_t b = __float_as_uint(w + 0.f);
+  return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+SPEC_DEVICE_INLINE int seq_tokens(const Kv8EvictParams& p, int b) {
+  const long long cap = min((long long)p.max_pages * kPage, p.weight_len);
+  return (int)max(0ll, min((long long)p.kv_len[b], cap));
+}
+
+// grid (Hkv, B)
+__global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_constant__ Kv8EvictParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ unsigned int hist[2048];
+  __shared__ unsigned int wsum[kPickWarps], weq[kPickWarps];
+  __shared__ unsigned int s_bin, s_above;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long group = (long long)b * p.Hkv + h;
+  const float* w = p.weight + group * p.weight_len;
+  int32_t* kept = p.kept + group * p.keep;
+  float* wout = p.weight_out + group * p.weight_out_len;
+  const int n = seq_tokens(p, b), m = min(n, p.keep);
+  if (h == 0 && tid == 0) p.new_len[b] = m;
+  for (long long i = m + tid; i < p.weight_out_len; i += kPickThreads) wout[i] = 0.f;
+  for (int i = m + tid; i < p.keep; i += kPickThreads) kept[i] = -1;
+  if (n == m) {
+    for (int i = tid; i < m; i += kPickThreads) {
+      kept[i] = i;
+      wout[i] = w[i];
+    }
+    return;
+  }
+  const int last = n - min(p.recent, m);   // tokens [last, n) stay anyway
+  const unsigned need = (unsigned)(m - (n - last));
+  const bool held = n <= kPickKeys;
+  const auto key_at = [&](int i) { return held ? keys[i] : weight_key(w[i]); };
+  uint32_t t = 0xffffffffu;                // threshold: keys above it stay, and `eq` of those equal to it
+  unsigned eq = 0;
+  if (need > 0) {
+    if (held)
+      for (int i = tid; i < n; i += kPickThreads) keys[i] = weight_key(w[i]);
+    uint32_t prefix = 0, mask = 0;
+    unsigned left = need;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const uint32_t digit = pass == 2 ? 1023u : 2047u;
+      hist[tid] = hist[tid + kPickThreads] = 0;
+      __syncthreads();
+      for (int i = tid; i < last; i += kPickThreads) {
+        const uint32_t k = key_at(i);
+        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+      }
+      __syncthreads();
+      // bins from the top: thread i has bins 2047 - 2 i and 2046 - 2 i
+      const unsigned c0 = hist[2047 - 2 * tid], c1 = hist[2046 - 2 * tid];
+      unsigned inc = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) wsum[warp] = inc;
+      __syncthreads();
+      unsigned before = inc - c0 - c1;
+      for (int i = 0; i < warp; ++i) before += wsum[i];
+      if (before < left && left <= before + c0) {
+        s_bin = 2047 - 2 * tid;
+        s_above = before;
+      } else if (before + c0 < left && left <= before + c0 + c1) {
+        s_bin = 2046 - 2 * tid;
+        s_above = before + c0;
+      }
+      __syncthreads();
+      prefix |= s_bin << shift;
+      mask |= digit << shift;
+      left -= s_above;
+    }
+    t = prefix;
+    eq = left;
+  }
+  // A warp's run of neighbouring tokens: counts, then places.
+  const int run = ((n + kPickWarps - 1) / kPickWarps + 31) & ~31;
+  const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
+  // 2: stays whatever the ties, 1: equal to the threshold
+  const auto kind = [&](int i) {
+    if (i >= last) return 2;
+    if (need == 0) return 0;
+    const uint32_t k = key_at(i);
+    return k > t ? 2 : k == t ? 1 : 0;
+  };
+  unsigned gt = 0, ties = 0;
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const int k = i0 + lane < r1 ? kind(i0 + lane) : 0;
+    gt += __popc(__ballot_sync(0xffffffffu, k == 2));
+    ties += __popc(__ballot_sync(0xffffffffu, k == 1));
+  }
+  __syncthreads();
+  if (lane == 0) wsum[warp] = gt, weq[warp] = ties;
+  __syncthreads();
+  unsigned gt0 = 0, eq0 = 0;
+  for (int i = 0; i < warp; ++i) gt0 += wsum[i], eq0 += weq[i];
+  for (int i0 = r0; i0 < r1; i0 += 32) {
+    const int i = i0 + lane;
+    const int k = i < r1 ? kind(i) : 0;
+    const unsigned bg = __ballot_sync(0xffffffffu, k == 2), be = __ballot_sync(0xffffffffu, k == 1);
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned ge = eq0 + __popc(be & below), gg = gt0 + __popc(bg & below);
+    if (k == 2 || (k == 1 && ge < eq)) {
+      const unsigned at = gg + min(ge, eq);
+      kept[at] = i;
+      wout[at] = w[i];
+    }
+    gt0 += __popc(bg);
+    eq0 += __popc(be);
+  }
+}
+
+// c * 2^d as two exact factors that fp16 has, for |d| <= 23.
+struct Shift2 {
+  __half2 a, b;
+  SPEC_DEVICE_INLINE explicit Shift2(int d)
+      : a(__float2half2_rn(kv8_pow2(d / 2))), b(__float2half2_rn(kv8_pow2(d - d / 2))) {}
+  SPEC_DEVICE_INLINE uint32_t operator()(uint32_t x) const { return kv8_mul2(kv8_mul2(x, a), b); }
+};
+
+// Largest magnitude (a code) of four words.
+SPEC_DEVICE_INLINE uint32_t max_code(uint4 v) {
+  uint32_t m = __vmaxu4(__vmaxu4(v.x & 0x7f7f7f7fu, v.y & 0x7f7f7f7fu), __vmaxu4(v.z & 0x7f7f7f7fu, v.w & 0x7f7f7f7fu));
+  m = __vmaxu4(m, m >> 16);
+  return max(m & 0xffu, (m >> 8) & 0xffu);
+}
+SPEC_DEVICE_INLINE float code_value(uint32_t code) {
+  const uint32_t y = kv8_lo(code);
+  return __half2float(__ushort_as_half((unsigned short)y));
+}
+
+constexpr int kMoveWarps = 4;
+
+// One warp per (sequence, destination sub-block, kv head), heads fastest.
+template <int HD>
+__global__ void __launch_bounds__(kMoveWarps * 32) kv8_move_kernel(const __grid_constant__ Kv8EvictParams p,
+                                                                   long long total) {
+  constexpr int SUB = kv8_sub_bytes(HD), BLOCK = kv8_block_bytes(HD), N = HD / 32, CH = HD / 16;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  const int subs = (p.keep + kSub - 1) / kSub;
+  pdl_wait();
+  pdl_launch_dependents();
+  for (long long x = (long long)blockIdx.x * kMoveWarps + (threadIdx.x >> 5); x < total;
+       x += (long long)gridDim.x * kMoveWarps) {
+    const int h = (int)(x % p.Hkv);
+    const long long y = x / p.Hkv;
+    const int s = (int)(y % subs), b = (int)(y / subs);
+    const int m = min(seq_tokens(p, b), p.keep);
+    if (s * kSub >= m) continue;
+    const int dpage = s / 4 < p.dst_pages ? p.dst_table[(long long)b * p.dst_pages + s / 4] : -1;
+    if (dpage < 0 || dpage >= p.num_pages) continue;
+    uint8_t* const dst = p.pool + ((long long)dpage * p.Hkv + h) * BLOCK + (s & 3) * SUB;
+    // lane t < 16: token t of the sub-block: its cell (page * 64 + token of the page), or -1
+    long long cell = -1;
+    uint32_t par = 0;
+    if (lane < kSub && s * kSub + lane < m) {
+      const int i = p.kept[((long long)b * p.Hkv + h) * p.keep + s * kSub + lane];
+      const int pg = p.page_table[(long long)b * p.max_pages + i / kPage];
+      if (pg >= 0 && pg < p.num_pages) {
+        cell = (long long)pg * kPage + i % kPage;
+        par = *reinterpret_cast<const uint32_t*>(p.pool + ((long long)pg * p.Hkv + h) * BLOCK + (i % kPage / kSub) * SUB +
+                                                 2 * kSub * HD);
+      }
+    }
+    const auto source = [&](long long cl) { return p.pool + ((cl >> 6) * p.Hkv + h) * BLOCK + ((cl & 63) >> 4) * SUB; };
+    int e[2];
+    {  // K: chunk id % CH of token id / CH
+      uint4 v[N];
+      int es[N];
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int id = lane + 32 * i, t = id / CH, j = id % CH;
+        const long long cl = __shfl_sync(0xffffffffu, cell, t);
+        es[i] = kv8_exp(__shfl_sync(0xffffffffu, par, t), 0);
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (cl >= 0) v[i] = *reinterpret_cast<const uint4*>(source(cl) + kv8_k_chunk<HD>((int)(cl & 15), j));
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) a = fmaxf(a, code_value(max_code(v[i])) * kv8_pow2(es[i]));
+      e[0] = kv8_needed_exp(warp_max(a));
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int id = lane + 32 * i, t = id / CH, j = id % CH;
+        const Shift2 f(es[i] - e[0]);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = kv8_codes(f(kv8_lo(w[k])), f(kv8_hi(w[k])));
+        *reinterpret_cast<uint4*>(dst + kv8_k_chunk<HD>(t, j)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    {  // V: this lane's dims of tokens 2c, 2c + 1, 2c + 8, 2c + 9
+      uint4 v[4][N];
+      int es[4], sel[4];
+      float a = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 2 * c + (i & 1) + (i >> 1) * 8;
+        const long long cl = __shfl_sync(0xffffffffu, cell, t);
+        es[i] = kv8_exp(__shfl_sync(0xffffffffu, par, t), 1);
+        const int ts = (int)(cl & 15), from = (lane & ~3) | ((ts & 7) >> 1);
+        sel[i] = (ts >> 3) * 2 + (ts & 1);           // the token's byte of a word
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          v[i][j] = make_uint4(0u, 0u, 0u, 0u);
+          if (cl >= 0) v[i][j] = *reinterpret_cast<const uint4*>(source(cl) + kv8_v_chunk<HD>(j, from));
+        }
+      }
+      uint32_t b4[4][N];                             // that byte of each of a chunk's words
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t pr = sel[i] | (sel[i] + 4) << 4;
+        uint32_t mc = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const uint32_t lo = __byte_perm(v[i][j].x, v[i][j].y, pr), hi = __byte_perm(v[i][j].z, v[i][j].w, pr);
+          b4[i][j] = __byte_perm(lo, hi, 0x5410);
+          mc = __vmaxu4(mc, b4[i][j] & 0x7f7f7f7fu);
+        }
+        a = fmaxf(a, code_value(max_code(make_uint4(mc, 0u, 0u, 0u))) * kv8_pow2(es[i]));
+      }
+      e[1] = kv8_needed_exp(warp_max(a));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Shift2 f(es[i] - e[1]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) b4[i][j] = kv8_codes(f(kv8_lo(b4[i][j])), f(kv8_hi(b4[i][j])));
+      }
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {                // dim 4 j + k of the four tokens
+          const uint32_t pr = k | (k + 4) << 4;
+          o[k] = __byte_perm(__byte_perm(b4[0][j], b4[1][j], pr), __byte_perm(b4[2][j], b4[3][j], pr), 0x5410);
+        }
+        *reinterpret_cast<uint4*>(dst + kv8_v_chunk<HD>(j, lane)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    if (lane == 0) *reinterpret_cast<uint4*>(dst + 2 * kSub * HD) = make_uint4(kv8_param_word(e[0], e[1]), 0u, 0u, 0u);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_evict(const Kv8EvictParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1ull)) {
+    e = cudaFuncSetAttribute(kv8_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPickKeys * 4);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(1ull << (dev & 63), std::memory_order_release);
+  }
+  const long long most = std::min((long long)p.max_pages * kPage, p.weight_len);
+  const size_t smem = (size_t)std::min<long long>(most, kPickKeys) * 4;
+  e = launch_k(kv8_pick_kernel, dim3(p.Hkv, p.B), dim3(kPickThreads), smem, st, p);
+  if (e != cudaSuccess) return e;
+  const long long total = (long long)p.B * p.Hkv * ((p.keep + kSub - 1) / kSub);
+  const long long ctas = (total + kMoveWarps - 1) / kMoveWarps;
+  const unsigned grid = (unsigned)std::min<long long>(ctas, 1ll << 30);
+  return p.hd == 128 ? launch_k(kv8_move_kernel<128>, dim3(grid), dim3(kMoveWarps * 32), 0, st, p, total)
+                     : launch_k(kv8_move_kernel<64>, dim3(grid), dim3(kMoveWarps * 32), 0, st, p, total);
+}
+
+}  // namespace spec

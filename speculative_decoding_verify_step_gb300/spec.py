@@ -46,7 +46,7 @@ EXPORTS = ["spec_model_create", "spec_model_destroy", "spec_model_set_weight", "
            "spec_adjust_probs", "spec_verify_tree_sampled", "spec_accept_tree_probs", "spec_kv_write",
            "spec_kv4_block_bytes", "spec_kv4_write", "spec_kv4_read", "spec_kv4_attention", "spec_kv4_attention_workspace",
            "spec_model_create_kv", "spec_kv8_block_bytes", "spec_kv8_write", "spec_kv8_read",
-           "spec_kv8_attention", "spec_kv8_attention_workspace", "spec_sample"]
+           "spec_kv8_attention", "spec_kv8_attention_workspace", "spec_kv8_evict", "spec_sample"]
 
 RAGGED_CAP_ACCEPT, RAGGED_COMPACT = 1, 2
 
@@ -107,6 +107,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_kv8_attention_workspace": (I64, [I32, I32, I32, I32, I32, I32, I32, I32]),
         "spec_kv8_attention": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, I32, P, I64, P, F32, I32, P, P,
                                      P, I64, P, I64, P]),
+        "spec_kv8_evict": (I32, [I32, P, P, I32, P, I32, I32, I32, I32, I32, I32, P, I64, P, P, P, P, I64, P]),
         "spec_sample": (I32, [I32, I32, P, I32, I64, P, F32, P, P, P, P, I32, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -735,6 +736,37 @@ def spec_kv8_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
               hd ** -0.5 if scale is None else scale, max_kv_len, pool.data_ptr(), out.data_ptr(),
               None if weight is None else weight.data_ptr(), T, None if ws is None else ws.data_ptr(), size)
     return out
+
+
+def spec_kv8_evict(pool: torch.Tensor, weight: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor,
+                   dst_table: torch.Tensor, keep: int, recent: int = 0, outs=None):
+    """Cut the caches down to `keep` tokens per sequence and kv head: the last `recent`, and the
+    others of the largest accumulated weight [B, n_kv_heads, tokens] (spec_kv8_attention).  They
+    move, in order, to the pages of dst_table (pages of the same pool that page_table does not
+    name).  Returns (new_len [B], kept positions [B, n_kv_heads, keep] with -1 behind the last,
+    their weights with zeros behind, as many tokens as weight has or `keep`); `outs`:
+    preallocated."""
+    lib = _lib or load_library()
+    P, H, hd, B, width = _kv8_geometry(pool, kv_len, page_table, None)
+    dev, keep, recent = pool.device, int(keep), int(recent)
+    T = _kv8_weight(weight, "weight", B, H, dev)
+    if (dst_table.dtype is not torch.int32 or dst_table.dim() != 2 or dst_table.shape[0] != B or dst_table.device != dev
+            or not dst_table.is_contiguous()):
+        raise ValueError(f"dst_table must be a contiguous int32 tensor of shape ({B}, pages) on {dev}")
+    if keep < 1 or not 0 <= recent <= keep:
+        raise ValueError("keep must be at least 1 and recent between 0 and keep")
+    if outs is None:
+        outs = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, H, keep, dtype=torch.int32, device=dev),
+                torch.empty(B, H, max(T, keep), dtype=torch.float32, device=dev))
+    new_len, kept, wout = outs
+    for t, shape, what in ((new_len, (B,), "new_len"), (kept, (B, H, keep), "kept")):
+        if t.dtype is not torch.int32 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape} on {dev}")
+    To = _kv8_weight(wout, "the weights' output", B, H, dev)
+    _kv4_call(dev, lib.spec_kv8_evict, B, kv_len.data_ptr(), page_table.data_ptr(), width, dst_table.data_ptr(),
+              dst_table.shape[1], P, H, hd, keep, recent, weight.data_ptr(), T, pool.data_ptr(), new_len.data_ptr(),
+              kept.data_ptr(), wout.data_ptr(), To)
+    return new_len, kept, wout
 
 
 # ------------------------------------------------------------- sampling from logits
