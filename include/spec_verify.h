@@ -420,8 +420,10 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
  * of 2^-6 * 2^e and above).  So what a cache holds may depend, by that much, on how
  * its writes were split, and a write touches whole sub-blocks: within a call, and in
  * calls that may overlap, a sub-block's rows belong to one sequence and one call.
+ * (Writing later tokens of a sub-block whose first token never was written takes e
+ * from the bytes there: 0 in zeroed memory.)
  * Rows, positions, row_off, start, page_table, dtype, strides, streams and positions
- * without a cell are as in spec_kv4_write.  Bytes that were never written may hold
+ * without a cell are as in spec_kv4_write.  Codes that were never written may be
  * anything: they have no effect on tokens that were. */
 int64_t spec_kv8_block_bytes(int32_t head_dim);
 

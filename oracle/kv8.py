@@ -31,11 +31,13 @@ def e4m3(y):
 
 
 class HeldSeq:
-    """K or V of one kv head of one sequence: y [tokens, hd] held values, e [tokens / 16]."""
+    """K or V of one kv head of one sequence: y [tokens, hd] held values, e [tokens / 16]
+    (`e`: what the memory says before any write; it counts where a sub-block's first token is
+    not the first that is written)."""
 
-    def __init__(self, tokens, hd):
+    def __init__(self, tokens, hd, e=0):
         self.y = np.zeros((tokens, hd))
-        self.e = np.full(tokens // SUB, MIN_EXP)
+        self.e = np.full(tokens // SUB, e)
 
     def write(self, start, x):
         """Rows x at positions start, start + 1, ...: those below 0 or past the end have no cell."""

@@ -777,10 +777,10 @@ def _setting(t, dtype, n: int, dev, what: str):
     """None, or a contiguous [n] tensor of `dtype` on dev (a number counts for all)."""
     if t is None:
         return None
+    if isinstance(t, (int, float)):
+        return torch.full((n,), t, dtype=dtype, device=dev)  # no copy from the host: calls can be captured
     if not isinstance(t, torch.Tensor):
         t = torch.as_tensor(t)
-        if t.dim() == 0:
-            t = t.expand(n)
     if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
         t = t.to(device=dev, dtype=dtype).contiguous()
     if t.numel() != n:
