@@ -17,11 +17,18 @@
 // 2^-42: about 2^-42 of the mass, for 40 instructions and no fp64 (which runs at 1/64 of
 // fp32's rate here).
 //
-// A row is one thread-block cluster, its slices in shared memory, read from HBM once.
-// top_k needs no masses: a histogram of counts over bins 1/16 wide in x finds the bin of
-// the k-th token, a histogram over that bin's logits (as ordered integers) the logit; few
-// rows need a third.  top_p does the same with masses, over what top_k left.  Bins go
-// through distributed shared memory, each CTA adding up its share of them.
+// A row is one thread-block cluster, its slices in shared memory, read from HBM once.  What
+// can be kept is mostly a few hundred tokens, and is found without a mass per token:
+//   top_k   the k-th largest of the threads' own maxima is a lower bound of the k-th logit;
+//           a histogram of those maxima, in bins 1/16 wide in x, gives its bin
+//   min_p   x >= log(min_p)
+//   top_p   (alone) all masses, their exact sum, and a histogram of masses cut to 2^-16:
+//           the first bin where even those reach top_p of the sum
+// The tokens down to that bin, the candidates, go to one CTA, which sorts them and takes
+// every decision on its own, exactly.  Where there are more than 1024 of them (or top_k is
+// above 512), or rows have no limit at all, the whole cluster works on with histograms of
+// exact counts and masses, first of x, then of the logits (as ordered integers) of one bin.
+// Bins go through distributed shared memory, each CTA adding up its share of them.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,6 +52,8 @@ constexpr int kBins = kThreads;          // a thread per bin
 constexpr int kMaxCluster = 8;
 constexpr int kMaxSlice = 48 * 1024;     // logits of a CTA (shared memory)
 constexpr float kBinsPerUnit = 16.f;     // bins of x in the first histogram
+constexpr int kCand = 1024;              // candidates that one CTA sorts
+constexpr int kCandK = kCand / 2;        // largest top_k that is tried so
 
 // 2^(-i/1024) in units of 2^-62, by the exponential series.
 struct Pow2Table {
@@ -66,15 +75,25 @@ constexpr Pow2Table make_pow2_table() {
 }
 __device__ const Pow2Table kPow2 = make_pow2_table();
 
-struct Shared {
-  unsigned long long pow2[1024];
+struct Bins {
   unsigned int cnt[kBins], m0[kBins], m1[kBins], m2[kBins];  // this CTA's histogram; a mass in three parts
   unsigned int gc[kBins];                                    // the cluster's
   unsigned long long gm[kBins];
+};
+struct Candidates {
+  unsigned long long key[kCand], mass[kCand];
+};
+struct Shared {
+  unsigned long long pow2[1024];
+  union {
+    Bins h;
+    Candidates c;
+  };
   unsigned long long part[8][kMaxCluster];                   // exchanges: one value of each CTA
   unsigned long long warp[kWarps], warp2[kWarps];
   unsigned long long found, tau;
   int pick;
+  unsigned int cand;                                         // candidates, in the first CTA
 };
 
 // A mass <= 2^40 in parts of 14, 13 and 14 bits: over a slice's at most 48 * 1024 tokens
@@ -184,7 +203,7 @@ SPEC_DEVICE_INLINE float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
-  extern __shared__ __align__(16) float smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -204,21 +223,22 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const bool bad = !(temp == 0.f || (temp >= 1e-6f && temp < INFINITY)) || K < 0 || !(TP > 0.f && TP <= 1.f) ||
                    !(MP >= 0.f && MP <= 1.f) || !(u >= 0.f && u < 1.f);
 
-  // The slice, in 16-byte loads where the row's address lets them; local index i lies at
-  // val[i], val chosen so that those loads are stored aligned.
+  // The slice, as it is, in 16-byte copies (its place in shared memory is as far off a 16-byte
+  // boundary as its address), and the thread's largest logit.
   constexpr int PER = 16 / sizeof(T);
   const T* src = static_cast<const T*>(p.logits) + row * p.row_stride + s0;
-  const int head = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(src) & 15)) & 15) / (int)sizeof(T));
-  float* const val = smem + ((4 - (head & 3)) & 3);
+  const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
+  const int head = min(n, ((16 - off) & 15) / (int)sizeof(T));
+  T* const val = reinterpret_cast<T*>(smem + off);
+  const auto logit = [&](int i) { return clean(to_f32(val[i])); };
   const int vecs = (n - head) / PER, tail0 = head + vecs * PER;
-  float mx = -INFINITY;
-  auto put = [&](int i, float x) {
-    x = clean(x);
-    val[i] = x;
-    mx = fmaxf(mx, x);
+  float own = -INFINITY;
+  auto put = [&](int i) {
+    val[i] = src[i];
+    own = fmaxf(own, clean(to_f32(val[i])));
   };
-  if (tid < head) put(tid, to_f32(src[tid]));
-  if (tid < n - tail0) put(tail0 + tid, to_f32(src[tail0 + tid]));
+  if (tid < head) put(tid);
+  if (tid < n - tail0) put(tail0 + tid);
   constexpr int UN = 4;  // loads in flight
   for (int j0 = tid; j0 < vecs; j0 += UN * kThreads) {
     uint4 w[UN];
@@ -228,17 +248,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < UN; ++k)
       if (j0 + k * kThreads < vecs) {
+        reinterpret_cast<uint4*>(val + head)[j0 + k * kThreads] = w[k];
         const T* e = reinterpret_cast<const T*>(&w[k]);
-        float4* dst = reinterpret_cast<float4*>(val + head + (j0 + k * kThreads) * PER);
 #pragma unroll
-        for (int i = 0; i < PER / 4; ++i) {
-          const float4 f = make_float4(clean(to_f32(e[4 * i])), clean(to_f32(e[4 * i + 1])), clean(to_f32(e[4 * i + 2])),
-                                       clean(to_f32(e[4 * i + 3])));
-          dst[i] = f;
-          mx = fmaxf(fmaxf(fmaxf(mx, f.x), fmaxf(f.y, f.z)), f.w);
-        }
+        for (int i = 0; i < PER; ++i) own = fmaxf(own, to_f32(e[i]));  // fmaxf passes over NaN
       }
   }
+  own = clean(own);  // -0 as 0
 
   // Exchange number xchg: one 64-bit value of every CTA, read after a cluster barrier.  A
   // number comes up again only after at least six barriers.
@@ -246,7 +262,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   auto give = [&](unsigned long long v) {
     if (tid < cs) *cluster.map_shared_rank(&sh.part[xchg][rank], tid) = v;
   };
-  mx = warp_max(mx);
+  if (tid == 0) sh.cand = 0;
+  float mx = warp_max(own);
   if (lane == 0) sh.warp[warp] = __float_as_uint(mx);
   __syncthreads();
   for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, __uint_as_float((uint32_t)sh.warp[i]));
@@ -262,16 +279,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       for (int i = tid; i < n; i += kThreads) probs[i] = q(i);
   };
 
+  auto zero_probs = [&] {
+    if (!probs) return;
+    const int h = min(n, (int)((16 - (reinterpret_cast<uintptr_t>(probs) & 15)) & 15) / 4), vec = (n - h) / 4;
+    if (tid < h) probs[tid] = 0.f;
+    for (int i = tid; i < vec; i += kThreads) reinterpret_cast<float4*>(probs + h)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (tid < n - h - vec * 4) probs[h + vec * 4 + tid] = 0.f;
+  };
+
   if (bad || mx == -INFINITY) {  // nothing to draw from
     if (rank == 0 && tid == 0) p.tokens[row] = -1;
-    fill([](int) { return 0.f; });
+    zero_probs();
     cluster.sync();
     return;
   }
   if (temp == 0.f) {  // the first of the largest logits
     int first = V;
     for (int i = tid; i < n; i += kThreads)
-      if (val[i] == mx) {
+      if (logit(i) == mx) {
         first = s0 + i;
         break;
       }
@@ -297,65 +322,67 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   R.bin = kBinsPerUnit / temp;
   R.pow2 = sh.pow2;
 
+  // The cluster's bins, from every CTA's (cnt alone, summed in 64 bits, or with masses), into gc
+  // and gm of all; each CTA adds up its share.
+  enum { kCounts, kMasses };
+  auto reduce_bins = [&](int what) {
+    cluster.sync();
+    const int share = kBins / cs, b = rank * share + tid;
+    if (tid < share) {
+      unsigned long long gc = 0, gm = 0;
+      for (int r = 0; r < cs; ++r) {
+        const Shared* o = cluster.map_shared_rank(&sh, r);
+        gc += o->h.cnt[b];
+        if (what == kMasses) gm += joined(o->h.m0[b], o->h.m1[b], o->h.m2[b]);
+      }
+      for (int r = 0; r < cs; ++r) {
+        Shared* o = cluster.map_shared_rank(&sh, r);
+        o->h.gc[b] = (unsigned)gc;
+        o->h.gm[b] = what == kMasses ? gm : gc;
+      }
+    }
+    cluster.sync();
+  };
+  auto sum_given = [&] {
+    unsigned long long s = 0;
+    for (int r = 0; r < cs; ++r) s += sh.part[xchg][r];
+    xchg = xchg == 7 ? 1 : xchg + 1;
+    return s;
+  };
   // One histogram pass over the slice's tokens that `cls` gives a bin >= 0; the cluster's
   // bins end up in gc and gm, and the sum of all masses that cls found in `total`.
   auto histogram = [&](bool masses, unsigned long long& total, auto cls) {
-    sh.cnt[tid] = sh.m0[tid] = sh.m1[tid] = sh.m2[tid] = 0;
+    sh.h.cnt[tid] = sh.h.m0[tid] = sh.h.m1[tid] = sh.h.m2[tid] = 0;
     __syncthreads();
     unsigned long long sum = 0;
     for (int i = tid; i < n; i += kThreads) {
       unsigned long long m = 0;
-      const int b = cls(i, val[i], m);
+      const int b = cls(i, logit(i), m);
       sum += m;
       if (b >= 0) {
-        atomicAdd(&sh.cnt[b], 1u);
+        atomicAdd(&sh.h.cnt[b], 1u);
         if (masses) {
-          atomicAdd(&sh.m0[b], (unsigned)m & 0x3fffu);
-          atomicAdd(&sh.m1[b], (unsigned)(m >> 14) & 0x1fffu);
-          atomicAdd(&sh.m2[b], (unsigned)(m >> 27));
+          atomicAdd(&sh.h.m0[b], (unsigned)m & 0x3fffu);
+          atomicAdd(&sh.h.m1[b], (unsigned)(m >> 14) & 0x1fffu);
+          atomicAdd(&sh.h.m2[b], (unsigned)(m >> 27));
         }
       }
     }
-    if (masses) {
-      sum = block_sum64(sum, sh.warp);
-      give(sum);
-    } else {
-      __syncthreads();
-    }
-    cluster.sync();
-    // this CTA's share of the bins, added up and sent to all
-    const int share = kBins / cs, b = rank * share + tid;
-    if (tid < share) {
-      unsigned int gc = 0;
-      unsigned long long gm = 0;
-      for (int r = 0; r < cs; ++r) {
-        const Shared* o = cluster.map_shared_rank(&sh, r);
-        gc += o->cnt[b];
-        if (masses) gm += joined(o->m0[b], o->m1[b], o->m2[b]);
-      }
-      for (int r = 0; r < cs; ++r) {
-        Shared* o = cluster.map_shared_rank(&sh, r);
-        o->gc[b] = gc;
-        o->gm[b] = gm;
-      }
-    }
-    cluster.sync();
-    if (masses) {
-      total = 0;
-      for (int r = 0; r < cs; ++r) total += sh.part[xchg][r];
-      xchg = xchg == 7 ? 1 : xchg + 1;
-    }
+    if (masses) give(block_sum64(sum, sh.warp));
+    reduce_bins(masses ? kMasses : kCounts);
+    if (masses) total = sum_given();
   };
 
   // The first bin where the running measure (counts, or masses), `base` so far, reaches
-  // `target`.
+  // `target`; -1: none does.
   struct Found {
     int bin;
     unsigned int count;
     unsigned long long size, above;  // the bin's measure; base and what lies above the bin
   };
   auto find = [&](bool by_mass, unsigned long long base, unsigned long long target) {
-    const unsigned long long mine = by_mass ? sh.gm[tid] : (unsigned long long)sh.gc[tid];
+    const unsigned long long mine = by_mass ? sh.h.gm[tid] : (unsigned long long)sh.h.gc[tid];
+    if (tid == 0) sh.pick = -1;
     const unsigned long long before = base + block_before64(mine, sh.warp);
     if (before < target && target <= before + mine) {
       sh.pick = tid;
@@ -364,8 +391,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     __syncthreads();
     Found f;
     f.bin = sh.pick;
-    f.count = sh.gc[f.bin];
-    f.size = by_mass ? sh.gm[f.bin] : f.count;
+    f.count = sh.h.gc[max(f.bin, 0)];
+    f.size = by_mass ? sh.h.gm[max(f.bin, 0)] : f.count;
     f.above = sh.found;
     __syncthreads();
     return f;
@@ -418,7 +445,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       const unsigned long long m = R.mass(key_logit(lo));
       need = (need + m - 1) / m;
     }
-    const auto tied = [&](int i) { return order_key(val[i]) == lo && in.has(lo, s0 + i) ? 1ull : 0ull; };
+    const auto tied = [&](int i) { return order_key(logit(i)) == lo && in.has(lo, s0 + i) ? 1ull : 0ull; };
     // the slice in runs of neighbouring tokens, one per thread
     const int run = (n + kThreads - 1) / kThreads, i0 = min(n, tid * run), i1 = min(n, i0 + run);
     unsigned long long k = 0;
@@ -441,10 +468,152 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     return Kept{lo, cut};
   };
 
+  const bool k_on = K >= 1 && K < V, p_on = TP < 1.f;
+  const unsigned long long least = __float2ull_ru(MP * 1099511627776.f);
+  auto kept_share = [](unsigned long long m, float inv) {
+    // 24 bits of m are enough: from 2^32 on its last nine are less than 2^-23 of it
+    return (m >> 32 ? (float)(uint32_t)(m >> 9) * 512.f : (float)(uint32_t)m) * inv;
+  };
+  // t = floor(floor(2^24 u) Z / 2^24)
+  auto draw_target = [&](unsigned long long Z) {
+    const unsigned long long m24 = (unsigned long long)(u * 16777216.f);
+    return (__umul64hi(m24, Z) << 40) | ((m24 * Z) >> 24);
+  };
+
+  // Candidates to the token and the row's distribution, by one CTA: M <= kCand keys (order of
+  // the logit, then the lower index first) in any order.
+  auto finish = [&](int M) {
+    int P = 64;
+    while (P < M) P *= 2;
+    // bitonic sort of a[0..P), the largest first; a pair per thread, and pairs up to 32 apart are a
+    // warp's own
+    auto sort = [&](unsigned long long* a) {
+      for (int k = 2; k <= P; k *= 2)
+        for (int j = k / 2; j > 0; j /= 2) {
+          if (j >= 32) __syncthreads();
+          else __syncwarp();
+          if (tid < P / 2) {
+            const int i = 2 * tid - (tid & (j - 1));
+            const unsigned long long x = a[i], y = a[i + j];
+            if ((x < y) == ((i & k) == 0)) a[i] = y, a[i + j] = x;
+          }
+        }
+      __syncthreads();
+    };
+    // a thread's two neighbours of the sums over a[0..P)
+    auto sums = [&](unsigned long long x, unsigned long long y, unsigned long long& before, unsigned long long& mid) {
+      before = block_before64(x + y, sh.warp);
+      mid = before + x;
+    };
+    unsigned long long* const key = sh.c.key;
+    for (int i = M + tid; i < P; i += kThreads) key[i] = 0ull;
+    __syncthreads();
+    sort(key);
+    const int i0 = 2 * tid, i1 = 2 * tid + 1;
+    auto mass_of = [&](int i) { return i < M ? R.mass(key_logit((uint32_t)(key[i] >> 32))) : 0ull; };
+    const unsigned long long m0 = mass_of(i0), m1 = mass_of(i1);
+    if (i0 < P) sh.c.mass[i0] = m0, sh.c.mass[i1] = m1;
+    unsigned long long b0, b1;  // masses before either
+    sums(m0, m1, b0, b1);
+    const unsigned nk = k_on ? (unsigned)min(K, M) : (unsigned)M;
+    unsigned long long tau = ~0ull;
+    if (p_on) {
+      if (k_on) {
+        if (i0 == (int)nk - 1) sh.found = b0 + m0;
+        if (i1 == (int)nk - 1) sh.found = b1 + m1;
+        __syncthreads();
+        if (tid == 0) sh.tau = max(1ull, (unsigned long long)ceil(__dmul_rn((double)TP, (double)sh.found)));
+        __syncthreads();
+      }
+      tau = sh.tau;
+    }
+    // a rank is kept if it is among the top_k, what lies before it falls short of tau, and its mass suffices
+    const bool keep0 = i0 < (int)nk && b0 < tau && m0 >= least, keep1 = i1 < (int)nk && b1 < tau && m1 >= least;
+    const int kept_n = __syncthreads_count(keep0) + __syncthreads_count(keep1);
+    if (i0 == kept_n - 1) sh.found = b0 + m0;
+    if (i1 == kept_n - 1) sh.found = b1 + m1;
+    __syncthreads();
+    const unsigned long long Z = sh.found, t = draw_target(Z);
+    if (p.probs) {
+      const float inv = 1.f / (float)Z;
+      if (keep0) p.probs[row * V + (0xffffffffu - (uint32_t)key[i0])] = kept_share(m0, inv);
+      if (keep1) p.probs[row * V + (0xffffffffu - (uint32_t)key[i1])] = kept_share(m1, inv);
+    }
+    // by index: the low halves of the keys fall as the index rises
+    __syncthreads();
+    P = 64;
+    while (P < kept_n) P *= 2;
+    if (i0 < P) {
+      const unsigned long long x = keep0 ? key[i0] << 32 | (unsigned)i0 : 0ull, y = keep1 ? key[i1] << 32 | (unsigned)i1 : 0ull;
+      key[i0] = x, key[i1] = y;
+    }
+    __syncthreads();
+    sort(key);
+    auto mass_at_rank = [&](int i) { return i < kept_n ? sh.c.mass[(uint32_t)key[i]] : 0ull; };
+    const unsigned long long x0 = mass_at_rank(i0), x1 = mass_at_rank(i1);
+    sums(x0, x1, b0, b1);
+    if (x0 && b0 <= t && t < b0 + x0) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(key[i0] >> 32));
+    if (x1 && b1 <= t && t < b1 + x1) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(key[i1] >> 32));
+  };
+
+  // The last bin of the first histogram that kept tokens can fall into, or -1: not known.
+  int last_bin = -1;
+  unsigned long long S = 0;  // all masses, where top_p counts them
+  if (k_on && K <= kCandK) {
+    sh.h.cnt[tid] = 0;
+    __syncthreads();
+    if (2 * K <= cs * kThreads) {
+      atomicAdd(&sh.h.cnt[R.bin_of(own)], 1u);
+    } else {
+      for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.h.cnt[R.bin_of(logit(i))], 1u);
+    }
+    reduce_bins(kCounts);
+    last_bin = find(false, 0ull, (unsigned long long)K).bin;
+  } else if (!k_on && p_on) {
+    sh.h.cnt[tid] = 0;
+    __syncthreads();
+    unsigned long long sum = 0;
+    for (int i = tid; i < n; i += kThreads) {
+      const float x = logit(i);
+      const unsigned long long m = R.mass(x);
+      sum += m;
+      if (m >> 24) atomicAdd(&sh.h.cnt[R.bin_of(x)], (unsigned)(m >> 24));
+    }
+    give(block_sum64(sum, sh.warp));
+    reduce_bins(kCounts);
+    S = sum_given();
+    if (tid == 0) sh.tau = max(1ull, (unsigned long long)ceil(__dmul_rn((double)TP, (double)S)));  // fp64: one warp's
+    __syncthreads();
+    last_bin = find(true, 0ull, (sh.tau >> 24) + 1ull).bin;
+  }
+  if (least > 0 && !(k_on && p_on)) {  // (top_p counts all of the top_k)
+    const int b = (int)fminf(-logf(MP) * kBinsPerUnit + 1.f, (float)(kBins - 1));
+    if (last_bin < 0 || b < last_bin) last_bin = b;
+  }
+  if (last_bin >= 0) {
+    Shared* const first = cluster.map_shared_rank(&sh, 0);
+    cluster.sync();  // the bins have been read: candidates take their place
+    for (int i = tid; i < n; i += kThreads) {
+      const float x = logit(i);
+      if (R.bin_of(x) <= last_bin) {
+        const unsigned at = atomicAdd(&first->cand, 1u);
+        if (at < kCand) first->c.key[at] = (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
+      }
+    }
+    cluster.sync();
+    const int M = (int)first->cand;
+    if (M <= kCand) {
+      zero_probs();
+      cluster.sync();  // M has been read, and the zeros lie before the kept tokens' shares
+      if (rank != 0) return;
+      finish(M);
+      return;
+    }
+    cluster.sync();  // bins may follow
+  }
+
   const Kept everything{0u, V};
   Kept kept = everything;
-  const bool k_on = K >= 1 && K < V, p_on = TP < 1.f;
-  unsigned long long S = 0;
   if (k_on) {
     histogram(false, S, [&](int, float x, unsigned long long&) { return R.bin_of(x); });
     kept = select(false, (unsigned long long)K, everything);
@@ -464,12 +633,10 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     __syncthreads();
     kept = select(true, sh.tau, in);
   }
-  const unsigned long long least = __float2ull_ru(MP * 1099511627776.f);
-
   // The kept masses: a warp's sum over its run of neighbouring tokens, then the cluster's.
   const int run = ((n + kWarps - 1) / kWarps + 31) & ~31;
   auto mass_at = [&](int i) -> unsigned long long {
-    const float x = val[i];
+    const float x = logit(i);
     if (!kept.has(order_key(x), s0 + i)) return 0ull;
     const unsigned long long m = R.mass(x);
     return m >= least ? m : 0ull;
@@ -492,10 +659,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     if (r < rank) before += v;
     Z += v;
   }
-  // t = floor(floor(2^24 u) Z / 2^24)
-  const unsigned long long m24 = (unsigned long long)(u * 16777216.f);
-  const unsigned long long hi64 = __umul64hi(m24, Z), lo64 = m24 * Z;
-  const unsigned long long t = (hi64 << 40) | (lo64 >> 24);
+  const unsigned long long t = draw_target(Z);
   if (before <= t && t < before + mine) {
     int w = 0;
     unsigned long long at = before;
@@ -516,11 +680,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   }
   if (probs) {
     const float inv = 1.f / (float)Z;
-    fill([&](int i) {
-      const unsigned long long m = mass_at(i);
-      // 24 bits of m are enough: from 2^32 on its last nine are less than 2^-23 of it
-      return (m >> 32 ? (float)(uint32_t)(m >> 9) * 512.f : (float)(uint32_t)m) * inv;
-    });
+    fill([&](int i) { return kept_share(mass_at(i), inv); });
   }
   cluster.sync();  // no CTA leaves while another may still write to it
 }
@@ -532,7 +692,7 @@ cudaError_t launch_t(const SampleParams& p, int cs, size_t smem, cudaStream_t st
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1ull)) {
-    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 4 + 16);
+    e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * (int)sizeof(T) + 32);
     if (e != cudaSuccess) return e;
     done.fetch_or(1ull << (dev & 63), std::memory_order_release);
   }
@@ -547,7 +707,7 @@ cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   // the narrowest cluster whose CTAs have at most 4096 tokens, or the widest
   int cs = 1;
   while (cs < kMaxCluster && (p.V + cs - 1) / cs > 4096) cs *= 2;
-  const size_t smem = (size_t)((p.V + cs - 1) / cs) * 4 + 16;
+  const size_t smem = (size_t)((p.V + cs - 1) / cs) * (p.dtype == 2 ? 4 : 2) + 32;
   switch (p.dtype) {
     case 0: return launch_t<__half>(p, cs, smem, st);
     case 1: return launch_t<__nv_bfloat16>(p, cs, smem, st);
