@@ -12,23 +12,24 @@
 // The mass has 40 bits behind the point, where fp32's e^x has 24: a draw from a row of
 // 128256 tokens compares u Z with running sums whose neighbours lie as near as the tails'
 // masses, and masses good to 2^-24 move one draw in some ten thousand to another token.
-// l - m and its product with log2(e) / T are pairs of floats, a table holds 2^(-i/1024) to
-// 62 bits, and the rest, below 2^-11, is three terms of a series in whole numbers of
-// 2^-42: about 2^-42 of the mass, for 40 instructions and no fp64 (which runs at 1/64 of
-// fp32's rate here).
+// l - m, its product with log2(e) / T, 2^(-i/256) (a table) and what is left of the
+// exponential are pairs of floats, good to about 2^-42, and the mass is taken from the last
+// pair in two parts of 20 bits: 45 instructions, nearly all fp32, which runs at twice the
+// integer pipe's rate here.  (With a table in whole numbers and 64-bit shifts the same took
+// 150 issue cycles; fp64 runs at 1/64 of fp32's rate.)
 //
 // A row is one thread-block cluster, its slices in shared memory, read from HBM once.  What
-// can be kept is mostly a few hundred tokens, and is found without a mass per token:
+// can be kept is often a few hundred tokens, and is found without a mass per token:
 //   top_k   the k-th largest of the threads' own maxima is a lower bound of the k-th logit;
 //           a histogram of those maxima, in bins 1/16 wide in x, gives its bin
 //   min_p   x >= log(min_p)
-//   top_p   (alone) all masses, their exact sum, and a histogram of masses cut to 2^-16:
-//           the first bin where even those reach top_p of the sum
-// The tokens down to that bin, the candidates, go to one CTA, which sorts them and takes
+//   top_p   (alone) the histogram of all masses, in the same bins
+// The tokens down to that bin, the candidates, go to one CTA, which ranks them and takes
 // every decision on its own, exactly.  Where there are more than 1024 of them (or top_k is
-// above 512), or rows have no limit at all, the whole cluster works on with histograms of
-// exact counts and masses, first of x, then of the logits (as ordered integers) of one bin.
-// Bins go through distributed shared memory, each CTA adding up its share of them.
+// above 512) only the threshold's bin goes to that CTA, which sends back the threshold, and
+// all CTAs sum up what is kept; a bin of more than 1024 tokens is first cut finer, by
+// histograms over its logits (as ordered integers).  Bins go through distributed shared
+// memory, each CTA adding up its share of them.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,27 +50,28 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = kThreads;          // a thread per bin
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;          // of few rows; 8 else (portable)
 constexpr int kMaxSlice = 48 * 1024;     // logits of a CTA (shared memory)
 constexpr float kBinsPerUnit = 16.f;     // bins of x in the first histogram
+constexpr int kBatch = 4;                // tokens of a thread under way at once
 constexpr int kCand = 1024;              // candidates that one CTA sorts
 constexpr int kCandK = kCand / 2;        // largest top_k that is tried so
 
-// 2^(-i/1024) in units of 2^-62, by the exponential series.
+// 2^(-i/256) as a pair of floats, by the exponential series.
 struct Pow2Table {
-  unsigned long long v[1024];
+  float2 v[256];
 };
 constexpr Pow2Table make_pow2_table() {
   Pow2Table t{};
-  for (int i = 0; i < 1024; ++i) {
-    const double x = -0.69314718055994530942 * i / 1024.0;
-    double term = 1.0, sum = 0.0;
+  for (int i = 0; i < 256; ++i) {
+    const double x = -0.69314718055994530942 * i / 256.0;
+    double term = 1.0, sum = 1.0;
     for (int k = 1; k < 30; ++k) {
       term *= x / k;
       sum += term;
     }
-    // 1 + sum in whole numbers: the one is exact, and i = 0 gives 2^62
-    t.v[i] = (1ull << 62) - (unsigned long long)(-sum * 4611686018427387904.0);
+    t.v[i].x = (float)sum;
+    t.v[i].y = (float)(sum - (double)t.v[i].x);
   }
   return t;
 }
@@ -84,14 +86,14 @@ struct Candidates {
   unsigned long long key[kCand], mass[kCand];
 };
 struct Shared {
-  unsigned long long pow2[1024];
+  float2 pow2[256];
   union {
     Bins h;
     Candidates c;
   };
   unsigned long long part[8][kMaxCluster];                   // exchanges: one value of each CTA
   unsigned long long warp[kWarps], warp2[kWarps];
-  unsigned long long found, tau;
+  unsigned long long found, tau, upto;
   int pick;
   unsigned int cand;                                         // candidates, in the first CTA
 };
@@ -115,35 +117,42 @@ struct Row {
   bool inf;          // the largest logit is +infinity: such tokens share all mass
   float ch, cl;      // log2(e) / T
   float bin;         // kBinsPerUnit / T
-  const unsigned long long* pow2;
+  const float2* pow2;
 
   SPEC_DEVICE_INLINE float dist(float l) const { return inf ? (l == INFINITY ? 0.f : INFINITY) : mx - l; }
   // Bin of x: never falls as l falls.
   SPEC_DEVICE_INLINE int bin_of(float l) const { return (int)fminf(dist(l) * bin, (float)(kBins - 1)); }
 
-  SPEC_DEVICE_INLINE unsigned long long mass(float l) const {
+  // R = a 2^20 + b, |b| <= 2^19.  Without a branch, so that several can be under way.
+  SPEC_DEVICE_INLINE void mass_parts(float l, int& a, int& b) const {
     const float dh = dist(l);
     const float yh = dh * ch;
-    if (!(yh < 41.f)) return 0ull;  // 2^-41 and less: no mass
-    float dl = 0.f;
-    if (!inf) {  // what dh lost
-      const float bb = dh - mx;
-      dl = (mx - (dh - bb)) - (l + bb);
-    }
+    const float bb = dh - mx;
+    const float dl = inf ? 0.f : (mx - (dh - bb)) - (l + bb);  // what dh lost
     const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
-    const float t = fmaf(yh, 1024.f, 12582912.f);
-    const int k = __float_as_int(t) - 0x4b400000;          // 1024 y, rounded
-    const float fh = fmaf(t - 12582912.f, -0.0009765625f, yh);
-    // r = -(fh + yl) ln 2 as a pair, e^r - 1 = r + r^2 (1/2 + r/6)
+    const float t = fmaf(yh, 256.f, 12582912.f);
+    const int k = __float_as_int(t) - 0x4b400000;           // 256 y, rounded
+    const float fh = fmaf(t - 12582912.f, -0.00390625f, yh);
+    // r = -(fh + yl) ln 2 as a pair, e^r - 1 = r + r^2 (1/2 + r/6 + r^2/24), |r| < 2^-9
     const float rh = fh * -0.693147182464599609375f;
     const float rl = fmaf(fh, -0.693147182464599609375f, -rh) +
                      fmaf(yl, -0.693147182464599609375f, fh * 1.90465429995776804525e-9f);
-    const float q = rh * rh * fmaf(rh, 0.16666667f, 0.5f) + rl;
-    const int s = __float2int_rn(rh * 4398046511104.f) +
-                  (__float_as_int(fmaf(q, 4398046511104.f, 12582912.f)) - 0x4b400000);
-    const unsigned long long p = pow2[k & 1023];
-    const unsigned long long w = p + (((long long)(int)((p >> 32) + ((p >> 31) & 1ull)) * s) >> 10);
-    return w >> (22 + (k >> 10));
+    const float q = fmaf(rh * rh, fmaf(rh, fmaf(rh, 0.0416666667f, 0.16666667f), 0.5f), rl);
+    // 2^(-i/256) (1 + rh + q) as a pair, times 2^-n
+    const float2 p = pow2[k & 255];
+    const float z = p.x * rh;
+    const float lo = fmaf(p.x, q, fmaf(p.x, rh, -z) + fmaf(p.y, rh, p.y));
+    const float s = __uint_as_float((127u - (uint32_t)(k >> 8)) << 23);
+    const float wh = (p.x + z) * s, wl = ((z - ((p.x + z) - p.x)) + lo) * s;
+    const float ta = fmaf(wh, 1048576.f, 8388608.f);        // 2^20 w, rounded
+    const bool some = yh < 41.f;                            // 2^-41 and less: no mass
+    a = some ? __float_as_int(ta) - 0x4b000000 : 0;
+    b = some ? __float_as_int(__fadd_rd((fmaf(ta - 8388608.f, -9.5367431640625e-7f, wh) + wl) * 1099511627776.f, 12582912.f)) - 0x4b400000 : 0;
+  }
+  SPEC_DEVICE_INLINE unsigned long long mass(float l) const {
+    int a, b;
+    mass_parts(l, a, b);
+    return (unsigned long long)(((long long)a << 20) + b);
   }
 };
 
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const int V = p.V, set = (int)(row / p.rows_per_setting);
   const int slice = (V + cs - 1) / cs, s0 = min(V, rank * slice), n = min(V, s0 + slice) - s0;
 
-  for (int i = tid; i < 1024; i += kThreads) sh.pow2[i] = kPow2.v[i];
+  if (tid < 256) sh.pow2[tid] = kPow2.v[tid];
   pdl_wait();
   pdl_launch_dependents();
 
@@ -276,6 +285,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   float* const probs = p.probs ? p.probs + row * V + s0 : nullptr;
   auto fill = [&](auto q) {
     if (probs)
+#pragma unroll 4
       for (int i = tid; i < n; i += kThreads) probs[i] = q(i);
   };
 
@@ -355,16 +365,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     sh.h.cnt[tid] = sh.h.m0[tid] = sh.h.m1[tid] = sh.h.m2[tid] = 0;
     __syncthreads();
     unsigned long long sum = 0;
-    for (int i = tid; i < n; i += kThreads) {
-      unsigned long long m = 0;
-      const int b = cls(i, logit(i), m);
-      sum += m;
-      if (b >= 0) {
-        atomicAdd(&sh.h.cnt[b], 1u);
-        if (masses) {
-          atomicAdd(&sh.h.m0[b], (unsigned)m & 0x3fffu);
-          atomicAdd(&sh.h.m1[b], (unsigned)(m >> 14) & 0x1fffu);
-          atomicAdd(&sh.h.m2[b], (unsigned)(m >> 27));
+    for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
+      unsigned long long m[kBatch];
+      int b[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * kThreads;
+        m[k] = 0ull;
+        b[k] = cls(min(i, n - 1), logit(min(i, n - 1)), m[k]);
+        if (i >= n) m[k] = 0ull, b[k] = -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        sum += m[k];
+        if (b[k] >= 0) {
+          atomicAdd(&sh.h.cnt[b[k]], 1u);
+          if (masses) {
+            atomicAdd(&sh.h.m0[b[k]], (unsigned)m[k] & 0x3fffu);
+            atomicAdd(&sh.h.m1[b[k]], (unsigned)(m[k] >> 14) & 0x1fffu);
+            atomicAdd(&sh.h.m2[b[k]], (unsigned)(m[k] >> 27));
+          }
         }
       }
     }
@@ -379,6 +399,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     int bin;
     unsigned int count;
     unsigned long long size, above;  // the bin's measure; base and what lies above the bin
+    unsigned int upto;               // tokens of the histogram down to the bin
   };
   auto find = [&](bool by_mass, unsigned long long base, unsigned long long target) {
     const unsigned long long mine = by_mass ? sh.h.gm[tid] : (unsigned long long)sh.h.gc[tid];
@@ -388,8 +409,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       sh.pick = tid;
       sh.found = before;
     }
+    const unsigned long long upto = sh.h.gc[tid] + block_before64(sh.h.gc[tid], sh.warp);
+    if (tid == sh.pick) sh.upto = upto;
     __syncthreads();
     Found f;
+    f.upto = (unsigned)sh.upto;
     f.bin = sh.pick;
     f.count = sh.h.gc[max(f.bin, 0)];
     f.size = by_mass ? sh.h.gm[max(f.bin, 0)] : f.count;
@@ -398,48 +422,137 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     return f;
   };
 
-  // The least and the largest key whose distance falls into bin b of the first histogram.
+  // The least key in a bin of the first histogram up to b: 32 tries at a time.
+  auto first_key = [&](int b) {
+    uint32_t a = order_key(-INFINITY), z = order_key(R.inf ? INFINITY : R.mx);  // z is in bin 0
+    while (a < z) {
+      const uint32_t step = (z - a) / 32 + 1;
+      const unsigned long long m = (unsigned long long)a + (unsigned long long)lane * step;
+      const unsigned in = __ballot_sync(0xffffffffu, m >= z || R.bin_of(key_logit((uint32_t)m)) <= b);
+      const int l = in ? __ffs(in) - 1 : 32;
+      const unsigned long long hi = (unsigned long long)a + (unsigned long long)l * step;
+      if (l > 0) a = a + (uint32_t)(l - 1) * step + 1u;
+      if (hi < z) z = (uint32_t)hi;
+    }
+    return z;
+  };
   auto bin_bounds = [&](int b, uint32_t& lo, uint32_t& hi) {
-    const uint32_t highest = order_key(R.inf ? INFINITY : R.mx), lowest = order_key(-INFINITY);
-    uint32_t a = lowest, z = highest;
-    while (a < z) {
-      const uint32_t m = a + (z - a) / 2;
-      if (R.bin_of(key_logit(m)) <= b) z = m;
-      else a = m + 1;
-    }
-    lo = a;
-    z = highest;
-    while (a < z) {
-      const uint32_t m = a + (z - a + 1) / 2;
-      if (R.bin_of(key_logit(m)) >= b) a = m;
-      else z = m - 1;
-    }
-    hi = a;
+    lo = first_key(b);
+    hi = b > 0 ? first_key(b - 1) - 1u : order_key(R.inf ? INFINITY : R.mx);
   };
 
-  // The shortest prefix (by rank) of the tokens of `in` whose measure reaches target; their
-  // first histogram has been taken.
-  auto select = [&](bool by_mass, unsigned long long target, const Kept& in) -> Kept {
-    Found f = find(by_mass, 0ull, target);
+  Shared* const first = cluster.map_shared_rank(&sh, 0);
+  // How many of the row's tokens `is` picks; if at most kCand, their keys (order of the logit,
+  // then the lower index first) go to the first CTA, in any order.
+  auto gather = [&](auto is) {
+    unsigned mine = 0;
+#pragma unroll 4
+    for (int i = tid; i < n; i += kThreads) mine += is(i, logit(i)) ? 1u : 0u;
+    give(block_sum64(mine, sh.warp));
+    cluster.sync();  // and the bins have been read: candidates take their place
+    const unsigned long long M = sum_given();
+    if (M <= kCand) {
+      if (mine)
+        for (int i = tid; i < n; i += kThreads) {
+          const float x = logit(i);
+          if (is(i, x))
+            first->c.key[atomicAdd(&first->cand, 1u)] =
+                (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
+        }
+      cluster.sync();
+    }
+    return (int)M;
+  };
+  // In the first CTA: M <= kCand keys of c.key sorted, the largest first; thread i gets those at
+  // 2 i and 2 i + 1 (0 behind the last).  Bitonic: partners up to 32 apart are in one warp and are
+  // exchanged in registers.
+  auto sorted = [&](int M, unsigned long long& x0, unsigned long long& x1) {
+    int P = 64;
+    while (P < M) P *= 2;
+    const int e = 2 * tid;
+    x0 = e < M ? sh.c.key[e] : 0ull, x1 = e + 1 < M ? sh.c.key[e + 1] : 0ull;
+    const auto order = [](unsigned long long& hi, unsigned long long& lo, bool down) {
+      if ((hi < lo) == down) {
+        const unsigned long long t = hi;
+        hi = lo, lo = t;
+      }
+    };
+    const bool on = e < ((M + 63) & ~63) || P > 64;  // warps without a key sort nothing while that is all
+    __syncthreads();
+    for (int k = 2; k <= P; k *= 2) {
+      const bool down = (e & k) == 0;
+      for (int j = k / 2; j >= 64; j /= 2) {
+        sh.c.key[e] = x0, sh.c.key[e + 1] = x1;
+        __syncthreads();
+        const unsigned long long y0 = sh.c.key[e ^ j], y1 = sh.c.key[(e + 1) ^ j];
+        const bool first_half = (e & j) == 0;
+        x0 = (x0 > y0) == (first_half == down) ? x0 : y0;
+        x1 = (x1 > y1) == (first_half == down) ? x1 : y1;
+        __syncthreads();
+      }
+      if (on) {
+        for (int j = min(k / 2, 32); j >= 2; j /= 2) {
+          const unsigned long long y0 = __shfl_xor_sync(0xffffffffu, x0, j / 2), y1 = __shfl_xor_sync(0xffffffffu, x1, j / 2);
+          const bool first_half = (e & j) == 0;
+          x0 = (x0 > y0) == (first_half == down) ? x0 : y0;
+          x1 = (x1 > y1) == (first_half == down) ? x1 : y1;
+        }
+        order(x0, x1, down);
+      }
+    }
+  };
+
+  // The shortest prefix (by rank) of the tokens of `in` whose measure reaches target, from the
+  // bin of their first histogram that holds its end.
+  auto select = [&](bool by_mass, unsigned long long target, const Kept& in, Found f) -> Kept {
     uint32_t lo, hi;
     bin_bounds(f.bin, lo, hi);
     while (true) {
-      if (f.count == 1 || f.above + f.size == target) return lo > in.t ? Kept{lo, V} : in;  // all of the bin
-      if (lo == hi) break;
-      const uint32_t span = hi - lo, l = lo, h = hi;
-      const int sft = max(0, 32 - __clz(span) - 9);  // span >> sft < 512
+      if (f.above + f.size == target) return lo > in.t ? Kept{lo, V} : in;  // all of the bin
+      const uint32_t l = lo, h = hi;
+      const auto inside = [&](int i, float x) {
+        const uint32_t key = order_key(x);
+        return key >= l && key <= h && in.has(key, s0 + i);
+      };
+      if (f.count <= kCand) {
+        const int M = gather(inside);  // (top_p's bins leave out tokens of no mass, which lie inside too)
+        if (M <= kCand) {
+          if (rank == 0) {
+            unsigned long long x[2], m[2], before;
+            sorted(M, x[0], x[1]);
+            const auto measure = [&](unsigned long long key) {
+              return key == 0ull ? 0ull : by_mass ? R.mass(key_logit((uint32_t)(key >> 32))) : 1ull;
+            };
+            m[0] = measure(x[0]), m[1] = measure(x[1]);
+            before = f.above + block_before64(m[0] + m[1], sh.warp);
+            // the candidate whose measure completes the target is the last one kept
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (before < target && target <= before + m[i])
+                for (int r = 0; r < cs; ++r) cluster.map_shared_rank(&sh, r)->found = x[i];
+              before += m[i];
+            }
+            if (tid == 0) sh.cand = 0;
+          }
+          cluster.sync();
+          const unsigned long long end = sh.found;
+          __syncthreads();
+          return Kept{(uint32_t)(end >> 32), (int)(0xffffffffu - (uint32_t)end)};
+        }
+      }
+      if (l == h) break;
+      const int sft = max(0, 32 - __clz(h - l) - 9);  // (h - l) >> sft < 512
       unsigned long long sum;
       histogram(by_mass, sum, [&](int i, float x, unsigned long long& m) {
-        const uint32_t key = order_key(x);
-        if (key < l || key > h || !in.has(key, s0 + i)) return -1;
+        if (!inside(i, x)) return -1;
         if (by_mass) m = R.mass(x);
-        return (int)((h - key) >> sft);
+        return (int)((h - order_key(x)) >> sft);
       });
       f = find(by_mass, f.above, target);
       hi = h - ((uint32_t)f.bin << sft);
       lo = hi - l < (1u << sft) ? l : hi - ((1u << sft) - 1u);
     }
-    // equal logits: as many of the first as are needed
+    // many equal logits: as many of the first as are needed
     unsigned long long need = target - f.above;
     if (by_mass) {
       const unsigned long long m = R.mass(key_logit(lo));
@@ -454,14 +567,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     unsigned long long mine = 0;
     for (int i = 0; i < kWarps; ++i) mine += sh.warp[i];
     give(mine);
-    if (tid == 0) sh.pick = V;
     cluster.sync();
     for (int r = 0; r < rank; ++r) b += sh.part[xchg][r];
     xchg = xchg == 7 ? 1 : xchg + 1;
     if (b < need && need <= b + k)
       for (int i = i0; i < i1; ++i)
         if (tied(i) && ++b == need)
-          for (int r = 0; r < cs; ++r) *cluster.map_shared_rank(&sh.pick, r) = s0 + i;
+          for (int r = 0; r < cs; ++r) cluster.map_shared_rank(&sh, r)->pick = s0 + i;
     cluster.sync();
     const int cut = sh.pick;
     __syncthreads();
@@ -480,170 +592,135 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     return (__umul64hi(m24, Z) << 40) | ((m24 * Z) >> 24);
   };
 
-  // Candidates to the token and the row's distribution, by one CTA: M <= kCand keys (order of
-  // the logit, then the lower index first) in any order.
-  auto finish = [&](int M) {
-    int P = 64;
-    while (P < M) P *= 2;
-    // bitonic sort of a[0..P), the largest first; a pair per thread, and pairs up to 32 apart are a
-    // warp's own
-    auto sort = [&](unsigned long long* a) {
-      for (int k = 2; k <= P; k *= 2)
-        for (int j = k / 2; j > 0; j /= 2) {
-          if (j >= 32) __syncthreads();
-          else __syncwarp();
-          if (tid < P / 2) {
-            const int i = 2 * tid - (tid & (j - 1));
-            const unsigned long long x = a[i], y = a[i + j];
-            if ((x < y) == ((i & k) == 0)) a[i] = y, a[i + j] = x;
-          }
-        }
-      __syncthreads();
-    };
-    // a thread's two neighbours of the sums over a[0..P)
-    auto sums = [&](unsigned long long x, unsigned long long y, unsigned long long& before, unsigned long long& mid) {
-      before = block_before64(x + y, sh.warp);
-      mid = before + x;
-    };
-    unsigned long long* const key = sh.c.key;
-    for (int i = M + tid; i < P; i += kThreads) key[i] = 0ull;
+  // tau = ceil(top_p * sum) into sh.tau, by one thread: fp64 is slow here.
+  auto set_tau = [&](unsigned long long sum) {
+    if (tid == 0) sh.tau = max(1ull, (unsigned long long)ceil(__dmul_rn((double)TP, (double)sum)));
     __syncthreads();
-    sort(key);
+  };
+  // In the first CTA: M <= kCand candidates, all that can be kept, of which top_k leaves the
+  // first nk, to the token and the row's distribution.  counted: sh.tau is top_p's target
+  // already.
+  auto finish = [&](int M, int nk, bool counted) {
+    unsigned long long x0, x1;
+    sorted(M, x0, x1);
     const int i0 = 2 * tid, i1 = 2 * tid + 1;
-    auto mass_of = [&](int i) { return i < M ? R.mass(key_logit((uint32_t)(key[i] >> 32))) : 0ull; };
-    const unsigned long long m0 = mass_of(i0), m1 = mass_of(i1);
-    if (i0 < P) sh.c.mass[i0] = m0, sh.c.mass[i1] = m1;
-    unsigned long long b0, b1;  // masses before either
-    sums(m0, m1, b0, b1);
-    const unsigned nk = k_on ? (unsigned)min(K, M) : (unsigned)M;
-    unsigned long long tau = ~0ull;
-    if (p_on) {
-      if (k_on) {
-        if (i0 == (int)nk - 1) sh.found = b0 + m0;
-        if (i1 == (int)nk - 1) sh.found = b1 + m1;
-        __syncthreads();
-        if (tid == 0) sh.tau = max(1ull, (unsigned long long)ceil(__dmul_rn((double)TP, (double)sh.found)));
-        __syncthreads();
-      }
-      tau = sh.tau;
+    const unsigned long long m0 = x0 ? R.mass(key_logit((uint32_t)(x0 >> 32))) : 0ull;
+    const unsigned long long m1 = x1 ? R.mass(key_logit((uint32_t)(x1 >> 32))) : 0ull;
+    const unsigned long long b0 = block_before64(m0 + m1, sh.warp), b1 = b0 + m0;
+    if (p_on && !counted) {
+      if (i0 == nk - 1) sh.found = b0 + m0;
+      if (i1 == nk - 1) sh.found = b1 + m1;
+      __syncthreads();
+      set_tau(sh.found);
     }
+    const unsigned long long tau = p_on ? sh.tau : ~0ull;
     // a rank is kept if it is among the top_k, what lies before it falls short of tau, and its mass suffices
-    const bool keep0 = i0 < (int)nk && b0 < tau && m0 >= least, keep1 = i1 < (int)nk && b1 < tau && m1 >= least;
+    const bool keep0 = i0 < nk && b0 < tau && m0 >= least, keep1 = i1 < nk && b1 < tau && m1 >= least;
     const int kept_n = __syncthreads_count(keep0) + __syncthreads_count(keep1);
     if (i0 == kept_n - 1) sh.found = b0 + m0;
     if (i1 == kept_n - 1) sh.found = b1 + m1;
+    // now by index (the low halves of the keys fall as it rises), with the rank to find the mass by
+    if (i0 < kCand) {
+      sh.c.key[i0] = keep0 ? x0 << 32 | (unsigned)i0 : 0ull, sh.c.key[i1] = keep1 ? x1 << 32 | (unsigned)i1 : 0ull;
+      sh.c.mass[i0] = m0, sh.c.mass[i1] = m1;
+    }
     __syncthreads();
     const unsigned long long Z = sh.found, t = draw_target(Z);
     if (p.probs) {
       const float inv = 1.f / (float)Z;
-      if (keep0) p.probs[row * V + (0xffffffffu - (uint32_t)key[i0])] = kept_share(m0, inv);
-      if (keep1) p.probs[row * V + (0xffffffffu - (uint32_t)key[i1])] = kept_share(m1, inv);
+      if (keep0) p.probs[row * V + (0xffffffffu - (uint32_t)x0)] = kept_share(m0, inv);
+      if (keep1) p.probs[row * V + (0xffffffffu - (uint32_t)x1)] = kept_share(m1, inv);
     }
-    // by index: the low halves of the keys fall as the index rises
-    __syncthreads();
-    P = 64;
-    while (P < kept_n) P *= 2;
-    if (i0 < P) {
-      const unsigned long long x = keep0 ? key[i0] << 32 | (unsigned)i0 : 0ull, y = keep1 ? key[i1] << 32 | (unsigned)i1 : 0ull;
-      key[i0] = x, key[i1] = y;
-    }
-    __syncthreads();
-    sort(key);
-    auto mass_at_rank = [&](int i) { return i < kept_n ? sh.c.mass[(uint32_t)key[i]] : 0ull; };
-    const unsigned long long x0 = mass_at_rank(i0), x1 = mass_at_rank(i1);
-    sums(x0, x1, b0, b1);
-    if (x0 && b0 <= t && t < b0 + x0) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(key[i0] >> 32));
-    if (x1 && b1 <= t && t < b1 + x1) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(key[i1] >> 32));
+    sorted(kept_n, x0, x1);
+    const unsigned long long y0 = x0 ? sh.c.mass[(uint32_t)x0] : 0ull, y1 = x1 ? sh.c.mass[(uint32_t)x1] : 0ull;
+    const unsigned long long c0 = block_before64(y0 + y1, sh.warp), c1 = c0 + y0;
+    if (c0 <= t && t < c0 + y0) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(x0 >> 32));
+    if (c1 <= t && t < c1 + y1) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(x1 >> 32));
   };
 
-  // The last bin of the first histogram that kept tokens can fall into, or -1: not known.
-  int last_bin = -1;
-  unsigned long long S = 0;  // all masses, where top_p counts them
-  if (k_on && K <= kCandK) {
-    sh.h.cnt[tid] = 0;
-    __syncthreads();
-    if (2 * K <= cs * kThreads) {
-      atomicAdd(&sh.h.cnt[R.bin_of(own)], 1u);
-    } else {
-      for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.h.cnt[R.bin_of(logit(i))], 1u);
-    }
-    reduce_bins(kCounts);
-    last_bin = find(false, 0ull, (unsigned long long)K).bin;
-  } else if (!k_on && p_on) {
-    sh.h.cnt[tid] = 0;
-    __syncthreads();
-    unsigned long long sum = 0;
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = logit(i);
-      const unsigned long long m = R.mass(x);
-      sum += m;
-      if (m >> 24) atomicAdd(&sh.h.cnt[R.bin_of(x)], (unsigned)(m >> 24));
-    }
-    give(block_sum64(sum, sh.warp));
-    reduce_bins(kCounts);
-    S = sum_given();
-    if (tid == 0) sh.tau = max(1ull, (unsigned long long)ceil(__dmul_rn((double)TP, (double)S)));  // fp64: one warp's
-    __syncthreads();
-    last_bin = find(true, 0ull, (sh.tau >> 24) + 1ull).bin;
-  }
-  if (least > 0 && !(k_on && p_on)) {  // (top_p counts all of the top_k)
-    const int b = (int)fminf(-logf(MP) * kBinsPerUnit + 1.f, (float)(kBins - 1));
-    if (last_bin < 0 || b < last_bin) last_bin = b;
-  }
-  if (last_bin >= 0) {
-    Shared* const first = cluster.map_shared_rank(&sh, 0);
-    cluster.sync();  // the bins have been read: candidates take their place
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = logit(i);
-      if (R.bin_of(x) <= last_bin) {
-        const unsigned at = atomicAdd(&first->cand, 1u);
-        if (at < kCand) first->c.key[at] = (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
-      }
-    }
-    cluster.sync();
-    const int M = (int)first->cand;
-    if (M <= kCand) {
-      zero_probs();
-      cluster.sync();  // M has been read, and the zeros lie before the kept tokens' shares
-      if (rank != 0) return;
-      finish(M);
-      return;
-    }
-    cluster.sync();  // bins may follow
-  }
-
-  const Kept everything{0u, V};
-  Kept kept = everything;
-  if (k_on) {
-    histogram(false, S, [&](int, float x, unsigned long long&) { return R.bin_of(x); });
-    kept = select(false, (unsigned long long)K, everything);
-  }
-  if (p_on) {
+  Kept kept{0u, V};          // what no limit has cut yet
+  int last_bin = kBins;      // the last bin of the first histogram that kept tokens can fall into; kBins: any
+  bool k_done = !k_on;       // top_k is in `kept`
+  bool counted = false;      // all masses of `kept` were summed up: sh.tau is set,
+  Found f{};                 // and this is where they reach it
+  const auto count_tokens = [&] {
+    unsigned long long none;
+    histogram(false, none, [&](int, float x, unsigned long long&) { return R.bin_of(x); });
+    return find(false, 0ull, (unsigned long long)K);
+  };
+  const auto count_masses = [&] {
     const Kept in = kept;
     // Without top_k, tokens with x below log((1 - top_p) / V) - 1 hold less than 1 - top_p of
     // the mass together, so the prefix ends above them: they are summed up, but have no bin.
     const int far = k_on ? kBins : (int)fminf((logf((float)V / (1.f - TP)) + 1.f) * kBinsPerUnit, (float)kBins);
+    unsigned long long S;
     histogram(true, S, [&](int i, float x, unsigned long long& m) {
-      if (!in.has(order_key(x), s0 + i)) return -1;
-      m = R.mass(x);
+      m = in.has(order_key(x), s0 + i) ? R.mass(x) : 0ull;
       const int b = R.bin_of(x);
       return b <= far && m > 0ull ? b : -1;
     });
-    if (tid == 0) sh.tau = max(1ull, (unsigned long long)ceil(__dmul_rn((double)TP, (double)S)));  // fp64: one warp's
-    __syncthreads();
-    kept = select(true, sh.tau, in);
+    set_tau(S);
+    f = find(true, 0ull, sh.tau);
+    counted = true;
+  };
+  if (k_on) {
+    if (K <= kCandK && 2 * K <= cs * kThreads) {
+      sh.h.cnt[tid] = 0;
+      __syncthreads();
+      atomicAdd(&sh.h.cnt[R.bin_of(own)], 1u);
+      reduce_bins(kCounts);
+      last_bin = find(false, 0ull, (unsigned long long)K).bin;
+    } else {
+      const Found at = count_tokens();
+      if (at.upto <= kCand) last_bin = at.bin;
+      else kept = select(false, (unsigned long long)K, kept, at), k_done = true;
+    }
   }
+  if (p_on && last_bin == kBins) {
+    count_masses();
+    if (f.upto <= kCand) last_bin = f.bin;
+  }
+  if (least > 0 && (k_done || !p_on))  // (top_p counts all of the top_k)
+    last_bin = min(last_bin, (int)fminf(-logf(MP) * kBinsPerUnit + 1.f, (float)(kBins - 1)));
+  if (last_bin < kBins) {
+    const Kept in = kept;
+    const int M = gather([&](int i, float x) { return R.bin_of(x) <= last_bin && in.has(order_key(x), s0 + i); });
+    if (M <= kCand) {
+      zero_probs();
+      cluster.sync();  // the zeros lie before the kept tokens' shares
+      if (rank == 0) finish(M, k_done ? M : min(K, M), counted);
+      return;
+    }
+    if (!k_done) kept = select(false, (unsigned long long)K, kept, count_tokens());
+    if (p_on && !counted) count_masses();
+  }
+  if (p_on) kept = select(true, sh.tau, kept, f);
+
   // The kept masses: a warp's sum over its run of neighbouring tokens, then the cluster's.
   const int run = ((n + kWarps - 1) / kWarps + 31) & ~31;
   auto mass_at = [&](int i) -> unsigned long long {
     const float x = logit(i);
-    if (!kept.has(order_key(x), s0 + i)) return 0ull;
     const unsigned long long m = R.mass(x);
-    return m >= least ? m : 0ull;
+    return kept.has(order_key(x), s0 + i) && m >= least ? m : 0ull;
   };
   const int w0 = min(n, warp * run), w1 = min(n, w0 + run);
   unsigned long long sum = 0;
-  for (int i = w0 + lane; i < w1; i += 32) sum += mass_at(i);
+  for (int i0 = w0 + lane; i0 < w1; i0 += 32 * kBatch) {
+    bool some = false;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int i = i0 + 32 * k;
+      some |= i < w1 && kept.has(order_key(logit(min(i, n - 1))), s0 + i);
+    }
+    if (some) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + 32 * k;
+        const unsigned long long m = mass_at(min(i, n - 1));
+        sum += i < w1 ? m : 0ull;
+      }
+    }
+  }
   sum = warp_sum64(sum);
   __syncthreads();
   if (lane == 0) sh.warp2[warp] = sum;
@@ -686,32 +763,38 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 }
 
 template <typename T>
-cudaError_t launch_t(const SampleParams& p, int cs, size_t smem, cudaStream_t st) {
+cudaError_t launch_t(const SampleParams& p, int cs, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (!(done.load(std::memory_order_acquire) >> (dev & 63) & 1ull)) {
     e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * (int)sizeof(T) + 32);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     done.fetch_or(1ull << (dev & 63), std::memory_order_release);
   }
+  const size_t smem = (size_t)((p.V + cs - 1) / cs) * sizeof(T) + 32;
   return launch_k_cluster(sample_kernel<T>, dim3((unsigned)(p.rows * cs)), dim3(kThreads), smem, st, dim3(cs, 1, 1), p);
+}
+
+// CTAs of a row.
+int cluster_size(int rows, int V) {
+  int cs = 1;
+  while (cs < 8 && (V + cs - 1) / cs > 4096) cs *= 2;
+  return cs == 8 && rows <= 8 && V > 8 * 4096 ? 16 : cs;
 }
 
 }  // namespace
 
-int sample_max_vocab() { return kMaxCluster * kMaxSlice; }
+int sample_max_vocab() { return 8 * kMaxSlice; }
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
-  // the narrowest cluster whose CTAs have at most 4096 tokens, or the widest
-  int cs = 1;
-  while (cs < kMaxCluster && (p.V + cs - 1) / cs > 4096) cs *= 2;
-  const size_t smem = (size_t)((p.V + cs - 1) / cs) * (p.dtype == 2 ? 4 : 2) + 32;
+  const int cs = cluster_size(p.rows, p.V);
   switch (p.dtype) {
-    case 0: return launch_t<__half>(p, cs, smem, st);
-    case 1: return launch_t<__nv_bfloat16>(p, cs, smem, st);
-    default: return launch_t<float>(p, cs, smem, st);
+    case 0: return launch_t<__half>(p, cs, st);
+    case 1: return launch_t<__nv_bfloat16>(p, cs, st);
+    default: return launch_t<float>(p, cs, st);
   }
 }
 
