@@ -98,14 +98,22 @@ struct Shared {
   unsigned int cand;                                         // candidates, in the first CTA
 };
 
-// A mass <= 2^40 in parts of 14, 13 and 14 bits: over a slice's at most 48 * 1024 tokens
-// each part's sum stays below 2^30.
+// A mass <= 2^40, as a 2^20 + b, in parts of 14, 13 and 14 bits: over a slice's at most 48 * 1024
+// tokens each part's sum stays below 2^30.
+struct Parts {
+  unsigned lo, mid, hi;
+  SPEC_DEVICE_INLINE Parts(int a, int b) {
+    const unsigned v = (unsigned)((b >> 14) + (a << 6));
+    lo = (unsigned)b & 0x3fffu, mid = v & 0x1fffu, hi = v >> 13;
+  }
+};
 SPEC_DEVICE_INLINE unsigned long long joined(unsigned a, unsigned b, unsigned c) {
   return (unsigned long long)a + ((unsigned long long)b << 14) + ((unsigned long long)c << 27);
 }
+SPEC_DEVICE_INLINE unsigned long long whole(long long a, long long b) { return (unsigned long long)((a << 20) + b); }
 
-SPEC_DEVICE_INLINE uint32_t order_key(float l) {  // orders like l
-  const uint32_t b = __float_as_uint(l);
+SPEC_DEVICE_INLINE uint32_t order_key(float l) {  // orders like l, -0 as 0
+  const uint32_t b = __float_as_uint(l + 0.f);
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 SPEC_DEVICE_INLINE float key_logit(uint32_t key) {
@@ -113,22 +121,22 @@ SPEC_DEVICE_INLINE float key_logit(uint32_t key) {
 }
 
 struct Row {
-  float mx;          // largest logit; 0 where that is +infinity
-  bool inf;          // the largest logit is +infinity: such tokens share all mass
+  float mx;          // largest logit, finite
   float ch, cl;      // log2(e) / T
   float bin;         // kBinsPerUnit / T
   const float2* pow2;
 
-  SPEC_DEVICE_INLINE float dist(float l) const { return inf ? (l == INFINITY ? 0.f : INFINITY) : mx - l; }
   // Bin of x: never falls as l falls.
-  SPEC_DEVICE_INLINE int bin_of(float l) const { return (int)fminf(dist(l) * bin, (float)(kBins - 1)); }
+  SPEC_DEVICE_INLINE int bin_of(float l) const {
+    return __float_as_int(__fadd_rd(fminf((mx - l) * bin, (float)(kBins - 1)), 8388608.f)) - 0x4b000000;
+  }
 
   // R = a 2^20 + b, |b| <= 2^19.  Without a branch, so that several can be under way.
   SPEC_DEVICE_INLINE void mass_parts(float l, int& a, int& b) const {
-    const float dh = dist(l);
+    const float dh = mx - l;
     const float yh = dh * ch;
     const float bb = dh - mx;
-    const float dl = inf ? 0.f : (mx - (dh - bb)) - (l + bb);  // what dh lost
+    const float dl = (mx - (dh - bb)) - (l + bb);           // what dh lost
     const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
     const float t = fmaf(yh, 256.f, 12582912.f);
     const int k = __float_as_int(t) - 0x4b400000;           // 256 y, rounded
@@ -142,7 +150,7 @@ struct Row {
     const float2 p = pow2[k & 255];
     const float z = p.x * rh;
     const float lo = fmaf(p.x, q, fmaf(p.x, rh, -z) + fmaf(p.y, rh, p.y));
-    const float s = __uint_as_float((127u - (uint32_t)(k >> 8)) << 23);
+    const float s = __int_as_float(0x3f800000 - (k & ~255) * 32768);
     const float wh = (p.x + z) * s, wl = ((z - ((p.x + z) - p.x)) + lo) * s;
     const float ta = fmaf(wh, 1048576.f, 8388608.f);        // 2^20 w, rounded
     const bool some = yh < 41.f;                            // 2^-41 and less: no mass
@@ -152,7 +160,7 @@ struct Row {
   SPEC_DEVICE_INLINE unsigned long long mass(float l) const {
     int a, b;
     mass_parts(l, a, b);
-    return (unsigned long long)(((long long)a << 20) + b);
+    return whole(a, b);
   }
 };
 
@@ -191,11 +199,11 @@ SPEC_DEVICE_INLINE unsigned long long block_before64(unsigned long long v, unsig
   return s;
 }
 
-// What is kept: logits above the threshold key, and of those equal to it the tokens up to cut.
+// What is kept: logits above the threshold, and of those equal to it the tokens up to cut.
 struct Kept {
-  uint32_t t;
+  float t;
   int cut;
-  SPEC_DEVICE_INLINE bool has(uint32_t key, int v) const { return key > t || (key == t && v <= cut); }
+  SPEC_DEVICE_INLINE bool has(float l, int v) const { return l > t || (l == t && v <= cut); }
 };
 
 template <typename T>
@@ -207,8 +215,14 @@ SPEC_DEVICE_INLINE float to_f32<__half>(__half x) { return __half2float(x); }
 template <>
 SPEC_DEVICE_INLINE float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
 
-// A stored logit: NaN counts as -infinity, and -0 as 0.
-SPEC_DEVICE_INLINE float clean(float x) { return x == x ? x + 0.f : -INFINITY; }
+template <typename T>
+SPEC_DEVICE_INLINE T from_f32(float x);
+template <>
+SPEC_DEVICE_INLINE float from_f32<float>(float x) { return x; }
+template <>
+SPEC_DEVICE_INLINE __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <>
+SPEC_DEVICE_INLINE __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
@@ -239,12 +253,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15);
   const int head = min(n, ((16 - off) & 15) / (int)sizeof(T));
   T* const val = reinterpret_cast<T*>(smem + off);
-  const auto logit = [&](int i) { return clean(to_f32(val[i])); };
+  const auto logit = [&](int i) { return fmaxf(to_f32(val[i]), -INFINITY); };  // NaN counts as -infinity
   const int vecs = (n - head) / PER, tail0 = head + vecs * PER;
   float own = -INFINITY;
   auto put = [&](int i) {
     val[i] = src[i];
-    own = fmaxf(own, clean(to_f32(val[i])));
+    own = fmaxf(own, to_f32(val[i]));  // fmaxf passes over NaN
   };
   if (tid < head) put(tid);
   if (tid < n - tail0) put(tail0 + tid);
@@ -260,10 +274,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         reinterpret_cast<uint4*>(val + head)[j0 + k * kThreads] = w[k];
         const T* e = reinterpret_cast<const T*>(&w[k]);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) own = fmaxf(own, to_f32(e[i]));  // fmaxf passes over NaN
+        for (int i = 0; i < PER; ++i) own = fmaxf(own, to_f32(e[i]));
       }
   }
-  own = clean(own);  // -0 as 0
 
   // Exchange number xchg: one 64-bit value of every CTA, read after a cluster barrier.  A
   // number comes up again only after at least six barriers.
@@ -325,8 +338,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   }
 
   Row R;
-  R.inf = mx == INFINITY;
-  R.mx = R.inf ? 0.f : mx;
+  if (mx == INFINITY) {  // such tokens share all mass: 0 for them, and nothing for the others
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) val[i] = from_f32<T>(logit(i) == INFINITY ? 0.f : -INFINITY);
+    own = own == INFINITY ? 0.f : -INFINITY;
+    mx = 0.f;
+    __syncthreads();
+  }
+  R.mx = mx;
   R.ch = __fdiv_rn(1.44269502162933349609375f, temp);   // log2(e) is this + 1.92596299e-8
   R.cl = __fdiv_rn(fmaf(-R.ch, temp, 1.44269502162933349609375f) + 1.92596299112661746887e-8f, temp);
   R.bin = kBinsPerUnit / temp;
@@ -359,35 +378,38 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     xchg = xchg == 7 ? 1 : xchg + 1;
     return s;
   };
-  // One histogram pass over the slice's tokens that `cls` gives a bin >= 0; the cluster's
-  // bins end up in gc and gm, and the sum of all masses that cls found in `total`.
+  // One histogram pass over the slice's tokens that `cls` gives a bin >= 0, with their masses
+  // a 2^20 + b; the cluster's bins end up in gc and gm, and the sum of all masses in `total`.
   auto histogram = [&](bool masses, unsigned long long& total, auto cls) {
     sh.h.cnt[tid] = sh.h.m0[tid] = sh.h.m1[tid] = sh.h.m2[tid] = 0;
     __syncthreads();
-    unsigned long long sum = 0;
+    long long sum_a = 0, sum_b = 0;
     for (int i0 = tid; i0 < n; i0 += kBatch * kThreads) {
-      unsigned long long m[kBatch];
-      int b[kBatch];
+      int a[kBatch], m[kBatch], bin[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + k * kThreads;
-        m[k] = 0ull;
-        b[k] = cls(min(i, n - 1), logit(min(i, n - 1)), m[k]);
-        if (i >= n) m[k] = 0ull, b[k] = -1;
+        const int i = min(i0 + k * kThreads, n - 1);
+        a[k] = m[k] = 0;
+        bin[k] = cls(i, logit(i), a[k], m[k]);
+        if (i0 + k * kThreads >= n) a[k] = m[k] = 0, bin[k] = -1;
       }
+      int ta = 0, tb = 0;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        sum += m[k];
-        if (b[k] >= 0) {
-          atomicAdd(&sh.h.cnt[b[k]], 1u);
+        ta += a[k], tb += m[k];
+        if (bin[k] >= 0) {
+          atomicAdd(&sh.h.cnt[bin[k]], 1u);
           if (masses) {
-            atomicAdd(&sh.h.m0[b[k]], (unsigned)m[k] & 0x3fffu);
-            atomicAdd(&sh.h.m1[b[k]], (unsigned)(m[k] >> 14) & 0x1fffu);
-            atomicAdd(&sh.h.m2[b[k]], (unsigned)(m[k] >> 27));
+            const Parts q(a[k], m[k]);
+            atomicAdd(&sh.h.m0[bin[k]], q.lo);
+            atomicAdd(&sh.h.m1[bin[k]], q.mid);
+            atomicAdd(&sh.h.m2[bin[k]], q.hi);
           }
         }
       }
+      sum_a += ta, sum_b += tb;
     }
+    const unsigned long long sum = whole(sum_a, sum_b);
     if (masses) give(block_sum64(sum, sh.warp));
     reduce_bins(masses ? kMasses : kCounts);
     if (masses) total = sum_given();
@@ -424,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 
   // The least key in a bin of the first histogram up to b: 32 tries at a time.
   auto first_key = [&](int b) {
-    uint32_t a = order_key(-INFINITY), z = order_key(R.inf ? INFINITY : R.mx);  // z is in bin 0
+    uint32_t a = order_key(-INFINITY), z = order_key(R.mx);  // z is in bin 0
     while (a < z) {
       const uint32_t step = (z - a) / 32 + 1;
       const unsigned long long m = (unsigned long long)a + (unsigned long long)lane * step;
@@ -438,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   };
   auto bin_bounds = [&](int b, uint32_t& lo, uint32_t& hi) {
     lo = first_key(b);
-    hi = b > 0 ? first_key(b - 1) - 1u : order_key(R.inf ? INFINITY : R.mx);
+    hi = b > 0 ? first_key(b - 1) - 1u : order_key(R.mx);
   };
 
   Shared* const first = cluster.map_shared_rank(&sh, 0);
@@ -508,11 +530,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     uint32_t lo, hi;
     bin_bounds(f.bin, lo, hi);
     while (true) {
-      if (f.above + f.size == target) return lo > in.t ? Kept{lo, V} : in;  // all of the bin
+      if (f.above + f.size == target) return key_logit(lo) > in.t ? Kept{key_logit(lo), V} : in;  // all of the bin
       const uint32_t l = lo, h = hi;
+      // by keys: as floats, 0 would lie in a range that ends at -0
       const auto inside = [&](int i, float x) {
         const uint32_t key = order_key(x);
-        return key >= l && key <= h && in.has(key, s0 + i);
+        return key >= l && key <= h && in.has(x, s0 + i);
       };
       if (f.count <= kCand) {
         const int M = gather(inside);  // (top_p's bins leave out tokens of no mass, which lie inside too)
@@ -537,15 +560,15 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
           cluster.sync();
           const unsigned long long end = sh.found;
           __syncthreads();
-          return Kept{(uint32_t)(end >> 32), (int)(0xffffffffu - (uint32_t)end)};
+          return Kept{key_logit((uint32_t)(end >> 32)), (int)(0xffffffffu - (uint32_t)end)};
         }
       }
       if (l == h) break;
       const int sft = max(0, 32 - __clz(h - l) - 9);  // (h - l) >> sft < 512
       unsigned long long sum;
-      histogram(by_mass, sum, [&](int i, float x, unsigned long long& m) {
+      histogram(by_mass, sum, [&](int i, float x, int& a, int& b) {
         if (!inside(i, x)) return -1;
-        if (by_mass) m = R.mass(x);
+        if (by_mass) R.mass_parts(x, a, b);
         return (int)((h - order_key(x)) >> sft);
       });
       f = find(by_mass, f.above, target);
@@ -558,7 +581,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       const unsigned long long m = R.mass(key_logit(lo));
       need = (need + m - 1) / m;
     }
-    const auto tied = [&](int i) { return order_key(logit(i)) == lo && in.has(lo, s0 + i) ? 1ull : 0ull; };
+    const float tie = key_logit(lo);
+    const auto tied = [&](int i) { return logit(i) == tie && in.has(tie, s0 + i) ? 1ull : 0ull; };
     // the slice in runs of neighbouring tokens, one per thread
     const int run = (n + kThreads - 1) / kThreads, i0 = min(n, tid * run), i1 = min(n, i0 + run);
     unsigned long long k = 0;
@@ -577,7 +601,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     cluster.sync();
     const int cut = sh.pick;
     __syncthreads();
-    return Kept{lo, cut};
+    return Kept{tie, cut};
   };
 
   const bool k_on = K >= 1 && K < V, p_on = TP < 1.f;
@@ -638,14 +662,14 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     if (c1 <= t && t < c1 + y1) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(x1 >> 32));
   };
 
-  Kept kept{0u, V};          // what no limit has cut yet
+  Kept kept{-INFINITY, V};   // what no limit has cut yet
   int last_bin = kBins;      // the last bin of the first histogram that kept tokens can fall into; kBins: any
   bool k_done = !k_on;       // top_k is in `kept`
   bool counted = false;      // all masses of `kept` were summed up: sh.tau is set,
   Found f{};                 // and this is where they reach it
   const auto count_tokens = [&] {
     unsigned long long none;
-    histogram(false, none, [&](int, float x, unsigned long long&) { return R.bin_of(x); });
+    histogram(false, none, [&](int, float x, int&, int&) { return R.bin_of(x); });
     return find(false, 0ull, (unsigned long long)K);
   };
   const auto count_masses = [&] {
@@ -654,10 +678,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     // the mass together, so the prefix ends above them: they are summed up, but have no bin.
     const int far = k_on ? kBins : (int)fminf((logf((float)V / (1.f - TP)) + 1.f) * kBinsPerUnit, (float)kBins);
     unsigned long long S;
-    histogram(true, S, [&](int i, float x, unsigned long long& m) {
-      m = in.has(order_key(x), s0 + i) ? R.mass(x) : 0ull;
-      const int b = R.bin_of(x);
-      return b <= far && m > 0ull ? b : -1;
+    histogram(true, S, [&](int i, float x, int& a, int& b) {
+      R.mass_parts(x, a, b);
+      const int bin = R.bin_of(x);
+      const bool is = in.has(x, s0 + i);
+      a = is ? a : 0, b = is ? b : 0;
+      return bin <= far && (a | b) != 0 ? bin : -1;
     });
     set_tau(S);
     f = find(true, 0ull, sh.tau);
@@ -684,7 +710,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     last_bin = min(last_bin, (int)fminf(-logf(MP) * kBinsPerUnit + 1.f, (float)(kBins - 1)));
   if (last_bin < kBins) {
     const Kept in = kept;
-    const int M = gather([&](int i, float x) { return R.bin_of(x) <= last_bin && in.has(order_key(x), s0 + i); });
+    const int M = gather([&](int i, float x) { return R.bin_of(x) <= last_bin && in.has(x, s0 + i); });
     if (M <= kCand) {
       zero_probs();
       cluster.sync();  // the zeros lie before the kept tokens' shares
@@ -698,29 +724,40 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 
   // The kept masses: a warp's sum over its run of neighbouring tokens, then the cluster's.
   const int run = ((n + kWarps - 1) / kWarps + 31) & ~31;
-  auto mass_at = [&](int i) -> unsigned long long {
+  const bool limit = least > 0;
+  const auto parts_at = [&](int i, int& a, int& b) {
     const float x = logit(i);
-    const unsigned long long m = R.mass(x);
-    return kept.has(order_key(x), s0 + i) && m >= least ? m : 0ull;
+    R.mass_parts(x, a, b);
+    const bool is = kept.has(x, s0 + i) && (!limit || whole(a, b) >= least);
+    a = is ? a : 0, b = is ? b : 0;
+  };
+  const auto mass_at = [&](int i) {
+    int a, b;
+    parts_at(i, a, b);
+    return whole(a, b);
   };
   const int w0 = min(n, warp * run), w1 = min(n, w0 + run);
-  unsigned long long sum = 0;
+  long long sum_a = 0, sum_b = 0;
   for (int i0 = w0 + lane; i0 < w1; i0 += 32 * kBatch) {
     bool some = false;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + 32 * k;
-      some |= i < w1 && kept.has(order_key(logit(min(i, n - 1))), s0 + i);
+      some |= i < w1 && kept.has(logit(min(i, n - 1)), s0 + i);
     }
     if (some) {
+      int ta = 0, tb = 0;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + 32 * k;
-        const unsigned long long m = mass_at(min(i, n - 1));
-        sum += i < w1 ? m : 0ull;
+        int a, b;
+        parts_at(min(i, n - 1), a, b);
+        ta += i < w1 ? a : 0, tb += i < w1 ? b : 0;
       }
+      sum_a += ta, sum_b += tb;
     }
   }
+  unsigned long long sum = whole(sum_a, sum_b);
   sum = warp_sum64(sum);
   __syncthreads();
   if (lane == 0) sh.warp2[warp] = sum;
