@@ -1839,6 +1839,7 @@ spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dty
   p.rows_per_setting = rows_per_setting;
   p.tokens = tokens;
   p.probs = probs;
+  CUDA_TRY(current_sm_count(&p.sm_count));
   CUDA_TRY(launch_sample(p, static_cast<cudaStream_t>(stream)));
   return SPEC_OK;
 }

@@ -82,15 +82,10 @@ struct Bins {
   unsigned int gc[kBins];                                    // the cluster's
   unsigned long long gm[kBins];
 };
-struct Candidates {
-  unsigned long long key[kCand], mass[kCand];
-};
 struct Shared {
   float2 pow2[256];
-  union {
-    Bins h;
-    Candidates c;
-  };
+  Bins h;
+  unsigned long long key[kCand];                             // candidates (the first CTA's)
   unsigned long long part[8][kMaxCluster];                   // exchanges: one value of each CTA
   unsigned long long warp[kWarps], warp2[kWarps];
   unsigned long long found, tau, upto;
@@ -236,6 +231,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const int slice = (V + cs - 1) / cs, s0 = min(V, rank * slice), n = min(V, s0 + slice) - s0;
 
   if (tid < 256) sh.pow2[tid] = kPow2.v[tid];
+  if (tid == 0) sh.cand = 0;
+  cluster_arrive();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_launch_dependents();
 
@@ -284,16 +281,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   auto give = [&](unsigned long long v) {
     if (tid < cs) *cluster.map_shared_rank(&sh.part[xchg][rank], tid) = v;
   };
-  if (tid == 0) sh.cand = 0;
-  float mx = warp_max(own);
+  float mx = warp_max(own);  // this CTA's, for now
   if (lane == 0) sh.warp[warp] = __float_as_uint(mx);
   __syncthreads();
   for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, __uint_as_float((uint32_t)sh.warp[i]));
-  cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
-  give(__float_as_uint(mx));
-  cluster.sync();
-  for (int r = 0; r < cs; ++r) mx = fmaxf(mx, __uint_as_float((uint32_t)sh.part[0][r]));
-  ++xchg;
+  cluster_wait();
 
   float* const probs = p.probs ? p.probs + row * V + s0 : nullptr;
   auto fill = [&](auto q) {
@@ -310,41 +302,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     if (tid < n - h - vec * 4) probs[h + vec * 4 + tid] = 0.f;
   };
 
-  if (bad || mx == -INFINITY) {  // nothing to draw from
-    if (rank == 0 && tid == 0) p.tokens[row] = -1;
-    zero_probs();
-    cluster.sync();
-    return;
-  }
-  if (temp == 0.f) {  // the first of the largest logits
-    int first = V;
-    for (int i = tid; i < n; i += kThreads)
-      if (logit(i) == mx) {
-        first = s0 + i;
-        break;
-      }
-    first = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
-    __syncthreads();
-    if (lane == 0) sh.warp[warp] = first;
-    __syncthreads();
-    for (int i = 0; i < kWarps; ++i) first = min(first, (int)sh.warp[i]);
-    give(first);
-    cluster.sync();
-    for (int r = 0; r < cs; ++r) first = min(first, (int)sh.part[xchg][r]);
-    if (rank == 0 && tid == 0) p.tokens[row] = first;
-    fill([&](int i) { return s0 + i == first ? 1.f : 0.f; });
-    cluster.sync();
-    return;
-  }
-
   Row R;
-  if (mx == INFINITY) {  // such tokens share all mass: 0 for them, and nothing for the others
-    __syncthreads();
-    for (int i = tid; i < n; i += kThreads) val[i] = from_f32<T>(logit(i) == INFINITY ? 0.f : -INFINITY);
-    own = own == INFINITY ? 0.f : -INFINITY;
-    mx = 0.f;
-    __syncthreads();
-  }
   R.mx = mx;
   R.ch = __fdiv_rn(1.44269502162933349609375f, temp);   // log2(e) is this + 1.92596299e-8
   R.cl = __fdiv_rn(fmaf(-R.ch, temp, 1.44269502162933349609375f) + 1.92596299112661746887e-8f, temp);
@@ -464,6 +422,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   };
 
   Shared* const first = cluster.map_shared_rank(&sh, 0);
+  const auto key_of = [&](int i, float x) { return (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i)); };
   // How many of the row's tokens `is` picks; if at most kCand, their keys (order of the logit,
   // then the lower index first) go to the first CTA, in any order.
   auto gather = [&](auto is) {
@@ -471,15 +430,13 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
 #pragma unroll 4
     for (int i = tid; i < n; i += kThreads) mine += is(i, logit(i)) ? 1u : 0u;
     give(block_sum64(mine, sh.warp));
-    cluster.sync();  // and the bins have been read: candidates take their place
+    cluster.sync();
     const unsigned long long M = sum_given();
     if (M <= kCand) {
       if (mine)
         for (int i = tid; i < n; i += kThreads) {
           const float x = logit(i);
-          if (is(i, x))
-            first->c.key[atomicAdd(&first->cand, 1u)] =
-                (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
+          if (is(i, x)) first->key[atomicAdd(&first->cand, 1u)] = key_of(i, x);
         }
       cluster.sync();
     }
@@ -492,7 +449,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     int P = 64;
     while (P < M) P *= 2;
     const int e = 2 * tid;
-    x0 = e < M ? sh.c.key[e] : 0ull, x1 = e + 1 < M ? sh.c.key[e + 1] : 0ull;
+    x0 = e < M ? sh.key[e] : 0ull, x1 = e + 1 < M ? sh.key[e + 1] : 0ull;
     const auto order = [](unsigned long long& hi, unsigned long long& lo, bool down) {
       if ((hi < lo) == down) {
         const unsigned long long t = hi;
@@ -504,9 +461,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     for (int k = 2; k <= P; k *= 2) {
       const bool down = (e & k) == 0;
       for (int j = k / 2; j >= 64; j /= 2) {
-        sh.c.key[e] = x0, sh.c.key[e + 1] = x1;
+        sh.key[e] = x0, sh.key[e + 1] = x1;
         __syncthreads();
-        const unsigned long long y0 = sh.c.key[e ^ j], y1 = sh.c.key[(e + 1) ^ j];
+        const unsigned long long y0 = sh.key[e ^ j], y1 = sh.key[(e + 1) ^ j];
         const bool first_half = (e & j) == 0;
         x0 = (x0 > y0) == (first_half == down) ? x0 : y0;
         x1 = (x1 > y1) == (first_half == down) ? x1 : y1;
@@ -625,8 +582,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   // first nk, to the token and the row's distribution.  counted: sh.tau is top_p's target
   // already.
   auto finish = [&](int M, int nk, bool counted) {
+    unsigned long long* const mass = reinterpret_cast<unsigned long long*>(&sh.h);  // by rank; the bins are done with
+    static_assert(sizeof(Bins) >= kCand * sizeof(unsigned long long), "masses of candidates");
     unsigned long long x0, x1;
     sorted(M, x0, x1);
+    if (tid == 0) sh.found = x0;
+    __syncthreads();
+    R.mx = key_logit((uint32_t)(sh.found >> 32));
+    if (M == 0) {  // no logit above -infinity
+      if (tid == 0) p.tokens[row] = -1;
+      return;
+    }
     const int i0 = 2 * tid, i1 = 2 * tid + 1;
     const unsigned long long m0 = x0 ? R.mass(key_logit((uint32_t)(x0 >> 32))) : 0ull;
     const unsigned long long m1 = x1 ? R.mass(key_logit((uint32_t)(x1 >> 32))) : 0ull;
@@ -645,8 +611,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     if (i1 == kept_n - 1) sh.found = b1 + m1;
     // now by index (the low halves of the keys fall as it rises), with the rank to find the mass by
     if (i0 < kCand) {
-      sh.c.key[i0] = keep0 ? x0 << 32 | (unsigned)i0 : 0ull, sh.c.key[i1] = keep1 ? x1 << 32 | (unsigned)i1 : 0ull;
-      sh.c.mass[i0] = m0, sh.c.mass[i1] = m1;
+      sh.key[i0] = keep0 ? x0 << 32 | (unsigned)i0 : 0ull, sh.key[i1] = keep1 ? x1 << 32 | (unsigned)i1 : 0ull;
+      mass[i0] = m0, mass[i1] = m1;
     }
     __syncthreads();
     const unsigned long long Z = sh.found, t = draw_target(Z);
@@ -656,11 +622,92 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       if (keep1) p.probs[row * V + (0xffffffffu - (uint32_t)x1)] = kept_share(m1, inv);
     }
     sorted(kept_n, x0, x1);
-    const unsigned long long y0 = x0 ? sh.c.mass[(uint32_t)x0] : 0ull, y1 = x1 ? sh.c.mass[(uint32_t)x1] : 0ull;
+    const unsigned long long y0 = x0 ? mass[(uint32_t)x0] : 0ull, y1 = x1 ? mass[(uint32_t)x1] : 0ull;
     const unsigned long long c0 = block_before64(y0 + y1, sh.warp), c1 = c0 + y0;
     if (c0 <= t && t < c0 + y0) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(x0 >> 32));
     if (c1 <= t && t < c1 + y1) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(x1 >> 32));
   };
+
+  // A small top_k: every CTA's tokens down to the bin of its own threads' k-th largest maximum
+  // hold its k first, so all CTAs' such tokens hold the row's, and nothing else has to be known
+  // before they are sent.  (Tokens at -infinity have no mass and are left out; a row with
+  // +infinity goes the long way.)
+  if (!bad && temp > 0.f && k_on && 2 * K <= kThreads && K * cs <= kCand * 5 / 8) {
+    sh.h.cnt[tid] = 0;
+    __syncthreads();
+    atomicAdd(&sh.h.cnt[R.bin_of(own)], 1u);
+    __syncthreads();
+    const unsigned here = sh.h.cnt[tid];
+    const unsigned long long above = block_before64(here, sh.warp);
+    if (above < (unsigned long long)K && (unsigned long long)K <= above + here) sh.pick = tid;
+    __syncthreads();
+    const int bin = sh.pick;
+    unsigned mine = 0;
+    if (mx < INFINITY) {
+#pragma unroll 4
+      for (int i = tid; i < n; i += kThreads) {
+        const float x = logit(i);
+        if (x > -INFINITY && R.bin_of(x) <= bin) {
+          const unsigned at = atomicAdd(&first->cand, 1u);
+          if (at < kCand) first->key[at] = key_of(i, x);
+          ++mine;
+        }
+      }
+    } else {
+      mine = kCand + 1;
+    }
+    give(block_sum64(mine, sh.warp));
+    zero_probs();
+    cluster.sync();
+    const unsigned long long M = sum_given();
+    if (M <= kCand) {
+      if (rank == 0) finish((int)M, min(K, (int)M), false);
+      return;
+    }
+    cluster.sync();
+    if (rank == 0 && tid == 0) sh.cand = 0;
+  }
+
+  // The row's largest logit.
+  give(__float_as_uint(mx));
+  cluster.sync();
+  for (int r = 0; r < cs; ++r) mx = fmaxf(mx, __uint_as_float((uint32_t)sh.part[xchg][r]));
+  ++xchg;
+  if (bad || mx == -INFINITY) {  // nothing to draw from
+    if (rank == 0 && tid == 0) p.tokens[row] = -1;
+    zero_probs();
+    cluster.sync();
+    return;
+  }
+  if (temp == 0.f) {  // the first of the largest logits
+    int first = V;
+    for (int i = tid; i < n; i += kThreads)
+      if (logit(i) == mx) {
+        first = s0 + i;
+        break;
+      }
+    first = (int)__reduce_min_sync(0xffffffffu, (unsigned)first);
+    __syncthreads();
+    if (lane == 0) sh.warp[warp] = first;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) first = min(first, (int)sh.warp[i]);
+    give(first);
+    cluster.sync();
+    for (int r = 0; r < cs; ++r) first = min(first, (int)sh.part[xchg][r]);
+    if (rank == 0 && tid == 0) p.tokens[row] = first;
+    fill([&](int i) { return s0 + i == first ? 1.f : 0.f; });
+    cluster.sync();
+    return;
+  }
+
+  if (mx == INFINITY) {  // such tokens share all mass: 0 for them, and nothing for the others
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) val[i] = from_f32<T>(logit(i) == INFINITY ? 0.f : -INFINITY);
+    own = own == INFINITY ? 0.f : -INFINITY;
+    mx = 0.f;
+    __syncthreads();
+  }
+  R.mx = mx;
 
   Kept kept{-INFINITY, V};   // what no limit has cut yet
   int last_bin = kBins;      // the last bin of the first histogram that kept tokens can fall into; kBins: any
@@ -815,10 +862,11 @@ cudaError_t launch_t(const SampleParams& p, int cs, cudaStream_t st) {
   return launch_k_cluster(sample_kernel<T>, dim3((unsigned)(p.rows * cs)), dim3(kThreads), smem, st, dim3(cs, 1, 1), p);
 }
 
-// CTAs of a row.
-int cluster_size(int rows, int V) {
+// CTAs of a row: as many as keep two per SM busy, with 4096 tokens or more each and their logits
+// in half an SM's shared memory; twice the portable size for a few rows.
+int cluster_size(int rows, int V, int elem, int sm_count) {
   int cs = 1;
-  while (cs < 8 && (V + cs - 1) / cs > 4096) cs *= 2;
+  while (cs < 8 && V > 4096 * cs && ((long long)rows * cs < 2 * sm_count || (V + cs - 1) / cs * elem > 84 * 1024)) cs *= 2;
   return cs == 8 && rows <= 8 && V > 8 * 4096 ? 16 : cs;
 }
 
@@ -827,7 +875,7 @@ int cluster_size(int rows, int V) {
 int sample_max_vocab() { return 8 * kMaxSlice; }
 
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
-  const int cs = cluster_size(p.rows, p.V);
+  const int cs = cluster_size(p.rows, p.V, p.dtype == 2 ? 4 : 2, p.sm_count);
   switch (p.dtype) {
     case 0: return launch_t<__half>(p, cs, st);
     case 1: return launch_t<__nv_bfloat16>(p, cs, st);

@@ -19,6 +19,7 @@ struct SampleParams {
   int rows_per_setting;
   int32_t* tokens;           // [rows]
   float* probs;              // [rows, V] or null
+  int sm_count;              // launch shape only
 };
 int sample_max_vocab();
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st);
