@@ -90,7 +90,8 @@ struct Shared {
   unsigned long long warp[kWarps], warp2[kWarps];
   unsigned long long found, tau, upto;
   int pick;
-  unsigned int cand;                                         // candidates, in the first CTA
+  unsigned int cand[2];                                      // candidates in the first CTA, of this and the next time
+  unsigned int picked, place;                                // candidates of this CTA, and their place there
 };
 
 // A mass <= 2^40, as a 2^20 + b, in parts of 14, 13 and 14 bits: over a slice's at most 48 * 1024
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   const int slice = (V + cs - 1) / cs, s0 = min(V, rank * slice), n = min(V, s0 + slice) - s0;
 
   if (tid < 256) sh.pow2[tid] = kPow2.v[tid];
-  if (tid == 0) sh.cand = 0;
+  if (tid < 2) sh.cand[tid] = 0;
   cluster_arrive();  // waited for before the first access to another CTA's shared memory
   pdl_wait();
   pdl_launch_dependents();
@@ -314,20 +315,17 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   enum { kCounts, kMasses };
   auto reduce_bins = [&](int what) {
     cluster.sync();
-    const int share = kBins / cs, b = rank * share + tid;
-    if (tid < share) {
-      unsigned long long gc = 0, gm = 0;
-      for (int r = 0; r < cs; ++r) {
-        const Shared* o = cluster.map_shared_rank(&sh, r);
-        gc += o->h.cnt[b];
-        if (what == kMasses) gm += joined(o->h.m0[b], o->h.m1[b], o->h.m2[b]);
-      }
-      for (int r = 0; r < cs; ++r) {
-        Shared* o = cluster.map_shared_rank(&sh, r);
-        o->h.gc[b] = (unsigned)gc;
-        o->h.gm[b] = what == kMasses ? gm : gc;
-      }
+    // a thread for each bin of this CTA's share and each CTA: neighbours add up
+    const int r = tid % cs, bin = rank * (kBins / cs) + tid / cs;
+    Shared* const o = cluster.map_shared_rank(&sh, r);
+    unsigned long long gc = o->h.cnt[bin], gm = 0;
+    if (what == kMasses) gm = joined(o->h.m0[bin], o->h.m1[bin], o->h.m2[bin]);
+    for (int k = cs / 2; k > 0; k /= 2) {
+      gc += __shfl_xor_sync(0xffffffffu, gc, k);
+      gm += __shfl_xor_sync(0xffffffffu, gm, k);
     }
+    o->h.gc[bin] = (unsigned)gc;
+    o->h.gm[bin] = what == kMasses ? gm : gc;
     cluster.sync();
   };
   auto sum_given = [&] {
@@ -422,27 +420,42 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   };
 
   Shared* const first = cluster.map_shared_rank(&sh, 0);
-  const auto key_of = [&](int i, float x) { return (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i)); };
-  // How many of the row's tokens `is` picks; if at most kCand, their keys (order of the logit,
-  // then the lower index first) go to the first CTA, in any order.
-  auto gather = [&](auto is) {
-    unsigned mine = 0;
+  // The keys of this CTA's tokens that `is` picks (order of the logit, then the lower index
+  // first) into the first CTA's list, in any order, as far as it and this CTA's own list, in the
+  // bins' place, go; how many there were.
+  unsigned long long* const local = reinterpret_cast<unsigned long long*>(&sh.h);
+  static_assert(sizeof(Bins) >= kCand * sizeof(unsigned long long), "lists in the bins' place");
+  int sent = 0;
+  auto send = [&](auto is) {
+    __syncthreads();  // the bins have been read
+    if (tid == 0) sh.picked = 0, sh.cand[(sent + 1) & 1] = 0;
+    __syncthreads();
 #pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) mine += is(i, logit(i)) ? 1u : 0u;
-    give(block_sum64(mine, sh.warp));
-    cluster.sync();
-    const unsigned long long M = sum_given();
-    if (M <= kCand) {
-      if (mine)
-        for (int i = tid; i < n; i += kThreads) {
-          const float x = logit(i);
-          if (is(i, x)) first->key[atomicAdd(&first->cand, 1u)] = key_of(i, x);
-        }
-      cluster.sync();
+    for (int i = tid; i < n; i += kThreads) {
+      const float x = logit(i);
+      if (is(i, x)) {
+        const unsigned at = atomicAdd(&sh.picked, 1u);
+        if (at < kCand) local[at] = (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
+      }
     }
-    return (int)M;
+    __syncthreads();
+    const unsigned mine = sh.picked;
+    if (mine > 0 && mine <= kCand) {
+      if (tid == 0) sh.place = atomicAdd(&first->cand[sent & 1], mine);
+      __syncthreads();
+      const unsigned at = sh.place;
+      for (int i = tid; i < mine && at + i < kCand; i += kThreads) first->key[at + i] = local[i];
+    }
+    ++sent;
+    return mine;
   };
-  // In the first CTA: M <= kCand keys of c.key sorted, the largest first; thread i gets those at
+  // All CTAs' such tokens: how many there were, and, if at most kCand, all their keys.
+  auto gather = [&](auto is) {
+    give(send(is));
+    cluster.sync();
+    return sum_given();
+  };
+  // In the first CTA: M <= kCand of its keys sorted, the largest first; thread i gets those at
   // 2 i and 2 i + 1 (0 behind the last).  Bitonic: partners up to 32 apart are in one warp and are
   // exchanged in registers.
   auto sorted = [&](int M, unsigned long long& x0, unsigned long long& x1) {
@@ -495,11 +508,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         return key >= l && key <= h && in.has(x, s0 + i);
       };
       if (f.count <= kCand) {
-        const int M = gather(inside);  // (top_p's bins leave out tokens of no mass, which lie inside too)
+        const unsigned long long M = gather(inside);  // (top_p's bins leave out tokens of no mass, which lie inside too)
         if (M <= kCand) {
           if (rank == 0) {
             unsigned long long x[2], m[2], before;
-            sorted(M, x[0], x[1]);
+            sorted((int)M, x[0], x[1]);
             const auto measure = [&](unsigned long long key) {
               return key == 0ull ? 0ull : by_mass ? R.mass(key_logit((uint32_t)(key >> 32))) : 1ull;
             };
@@ -512,7 +525,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
                 for (int r = 0; r < cs; ++r) cluster.map_shared_rank(&sh, r)->found = x[i];
               before += m[i];
             }
-            if (tid == 0) sh.cand = 0;
           }
           cluster.sync();
           const unsigned long long end = sh.found;
@@ -642,21 +654,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     if (above < (unsigned long long)K && (unsigned long long)K <= above + here) sh.pick = tid;
     __syncthreads();
     const int bin = sh.pick;
-    unsigned mine = 0;
-    if (mx < INFINITY) {
-#pragma unroll 4
-      for (int i = tid; i < n; i += kThreads) {
-        const float x = logit(i);
-        if (x > -INFINITY && R.bin_of(x) <= bin) {
-          const unsigned at = atomicAdd(&first->cand, 1u);
-          if (at < kCand) first->key[at] = key_of(i, x);
-          ++mine;
-        }
-      }
-    } else {
-      mine = kCand + 1;
-    }
-    give(block_sum64(mine, sh.warp));
+    give(mx == INFINITY ? kCand + 1 : send([&](int, float x) { return x > -INFINITY && R.bin_of(x) <= bin; }));
     zero_probs();
     cluster.sync();
     const unsigned long long M = sum_given();
@@ -664,8 +662,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       if (rank == 0) finish((int)M, min(K, (int)M), false);
       return;
     }
-    cluster.sync();
-    if (rank == 0 && tid == 0) sh.cand = 0;
   }
 
   // The row's largest logit.
@@ -757,11 +753,11 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     last_bin = min(last_bin, (int)fminf(-logf(MP) * kBinsPerUnit + 1.f, (float)(kBins - 1)));
   if (last_bin < kBins) {
     const Kept in = kept;
-    const int M = gather([&](int i, float x) { return R.bin_of(x) <= last_bin && in.has(x, s0 + i); });
+    const unsigned long long M = gather([&](int i, float x) { return R.bin_of(x) <= last_bin && in.has(x, s0 + i); });
     if (M <= kCand) {
       zero_probs();
       cluster.sync();  // the zeros lie before the kept tokens' shares
-      if (rank == 0) finish(M, k_done ? M : min(K, M), counted);
+      if (rank == 0) finish((int)M, k_done ? (int)M : min(K, (int)M), counted);
       return;
     }
     if (!k_done) kept = select(false, (unsigned long long)K, kept, count_tokens());
