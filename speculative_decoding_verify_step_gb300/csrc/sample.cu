@@ -276,6 +276,19 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       }
   }
 
+  // f(i, logit of i) for all of the slice, a thread's tokens in 16-byte pieces.
+  const auto each = [&](auto f) {
+    if (tid < head) f(tid, logit(tid));
+    if (tid < n - tail0) f(tail0 + tid, logit(tail0 + tid));
+#pragma unroll 2
+    for (int j = tid; j < vecs; j += kThreads) {
+      const uint4 w = reinterpret_cast<const uint4*>(val + head)[j];
+      const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) f(head + j * PER + i, fmaxf(to_f32(e[i]), -INFINITY));
+    }
+  };
+
   // Exchange number xchg: one 64-bit value of every CTA, read after a cluster barrier.  A
   // number comes up again only after at least six barriers.
   int xchg = 0;
@@ -420,24 +433,22 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   };
 
   Shared* const first = cluster.map_shared_rank(&sh, 0);
-  // The keys of this CTA's tokens that `is` picks (order of the logit, then the lower index
-  // first) into the first CTA's list, in any order, as far as it and this CTA's own list, in the
+  // The keys of this CTA's tokens from least_l on that `is` picks (order of the logit, then the
+  // lower index first) into the first CTA's list, in any order, as far as it and this CTA's own list, in the
   // bins' place, go; how many there were.
   unsigned long long* const local = reinterpret_cast<unsigned long long*>(&sh.h);
   static_assert(sizeof(Bins) >= kCand * sizeof(unsigned long long), "lists in the bins' place");
   int sent = 0;
-  auto send = [&](auto is) {
+  auto send = [&](float least_l, auto is) {
     __syncthreads();  // the bins have been read
     if (tid == 0) sh.picked = 0, sh.cand[(sent + 1) & 1] = 0;
     __syncthreads();
-#pragma unroll 4
-    for (int i = tid; i < n; i += kThreads) {
-      const float x = logit(i);
-      if (is(i, x)) {
+    each([&](int i, float x) {
+      if (x >= least_l && is(i, x)) {
         const unsigned at = atomicAdd(&sh.picked, 1u);
         if (at < kCand) local[at] = (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
       }
-    }
+    });
     __syncthreads();
     const unsigned mine = sh.picked;
     if (mine > 0 && mine <= kCand) {
@@ -450,8 +461,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     return mine;
   };
   // All CTAs' such tokens: how many there were, and, if at most kCand, all their keys.
-  auto gather = [&](auto is) {
-    give(send(is));
+  auto gather = [&](float least_l, auto is) {
+    give(send(least_l, is));
     cluster.sync();
     return sum_given();
   };
@@ -508,7 +519,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         return key >= l && key <= h && in.has(x, s0 + i);
       };
       if (f.count <= kCand) {
-        const unsigned long long M = gather(inside);  // (top_p's bins leave out tokens of no mass, which lie inside too)
+        const unsigned long long M = gather(key_logit(lo), inside);  // (top_p's bins leave out tokens of no mass, which lie inside too)
         if (M <= kCand) {
           if (rank == 0) {
             unsigned long long x[2], m[2], before;
@@ -653,8 +664,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     const unsigned long long above = block_before64(here, sh.warp);
     if (above < (unsigned long long)K && (unsigned long long)K <= above + here) sh.pick = tid;
     __syncthreads();
-    const int bin = sh.pick;
-    give(mx == INFINITY ? kCand + 1 : send([&](int, float x) { return x > -INFINITY && R.bin_of(x) <= bin; }));
+    const float least_l = fmaxf(key_logit(first_key(sh.pick)), -3.402823466e38f);
+    give(mx == INFINITY ? kCand + 1 : send(least_l, [](int, float) { return true; }));
     zero_probs();
     cluster.sync();
     const unsigned long long M = sum_given();
@@ -753,7 +764,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     last_bin = min(last_bin, (int)fminf(-logf(MP) * kBinsPerUnit + 1.f, (float)(kBins - 1)));
   if (last_bin < kBins) {
     const Kept in = kept;
-    const unsigned long long M = gather([&](int i, float x) { return R.bin_of(x) <= last_bin && in.has(x, s0 + i); });
+    const unsigned long long M = gather(key_logit(first_key(last_bin)), [&](int i, float x) { return in.has(x, s0 + i); });
     if (M <= kCand) {
       zero_probs();
       cluster.sync();  // the zeros lie before the kept tokens' shares
@@ -781,24 +792,39 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   };
   const int w0 = min(n, warp * run), w1 = min(n, w0 + run);
   long long sum_a = 0, sum_b = 0;
-  for (int i0 = w0 + lane; i0 < w1; i0 += 32 * kBatch) {
-    bool some = false;
+  const auto add = [&](int i, bool on) {
+    int a, b;
+    parts_at(i, a, b);
+    sum_a += on ? a : 0, sum_b += on ? b : 0;
+  };
+  if (kept.t == -INFINITY) {
+    for (int i0 = w0 + lane; i0 < w1; i0 += 32 * kBatch)
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + 32 * k;
-      some |= i < w1 && kept.has(logit(min(i, n - 1)), s0 + i);
-    }
-    if (some) {
-      int ta = 0, tb = 0;
+      for (int k = 0; k < kBatch; ++k) add(min(i0 + 32 * k, n - 1), i0 + 32 * k < w1);
+  } else {
+    // kept tokens are lined up first, so that no lane works out a mass that is not wanted
+    static_assert(kCand * 2 / kWarps >= 63 + 64, "queues in the candidates' place");
+    int* const queue = reinterpret_cast<int*>(sh.key) + warp * (kCand * 2 / kWarps);
+    int waiting = 0;
+    __syncthreads();
+    for (int i0 = w0; i0 < w1; i0 += 32 * 2) {
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int i = i0 + 32 * k;
-        int a, b;
-        parts_at(min(i, n - 1), a, b);
-        ta += i < w1 ? a : 0, tb += i < w1 ? b : 0;
+      for (int k = 0; k < 2; ++k) {
+        const int i = i0 + 32 * k + lane;
+        const bool is = i < w1 && kept.has(logit(min(i, n - 1)), s0 + i);
+        const unsigned m = __ballot_sync(0xffffffffu, is);
+        if (is) queue[waiting + __popc(m & ((1u << lane) - 1u))] = i;
+        waiting += __popc(m);
       }
-      sum_a += ta, sum_b += tb;
+      if (waiting >= 64) {
+        __syncwarp();
+        waiting -= 64;
+        add(queue[waiting + lane], true), add(queue[waiting + 32 + lane], true);
+        __syncwarp();
+      }
     }
+    __syncwarp();
+    for (int k = lane; k < waiting; k += 32) add(queue[k], true);
   }
   unsigned long long sum = whole(sum_a, sum_b);
   sum = warp_sum64(sum);
