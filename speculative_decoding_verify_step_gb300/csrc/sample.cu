@@ -160,25 +160,25 @@ struct Row {
   }
 };
 
+// Most of the kernel runs once per row, so its time is much that of fetching its instructions: what
+// is used in several places is a function, and loops without parallel work are not unrolled.
+
 SPEC_DEVICE_INLINE unsigned long long warp_sum64(unsigned long long v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-SPEC_DEVICE_INLINE unsigned long long block_sum64(unsigned long long v, unsigned long long* w) {
+__device__ __noinline__ unsigned long long block_sum64(unsigned long long v, unsigned long long* w) {
   v = warp_sum64(v);
   __syncthreads();
   if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = v;
   __syncthreads();
-  unsigned long long s = 0;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) s += w[i];
-  return s;
+  return warp_sum64((threadIdx.x & 31) < kWarps ? w[threadIdx.x & 31] : 0ull);
 }
 
 // Sum over the CTA's threads before this one.
-SPEC_DEVICE_INLINE unsigned long long block_before64(unsigned long long v, unsigned long long* w) {
+__device__ __noinline__ unsigned long long block_before64(unsigned long long v, unsigned long long* w) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned long long inc = v;
 #pragma unroll
@@ -189,10 +189,49 @@ SPEC_DEVICE_INLINE unsigned long long block_before64(unsigned long long v, unsig
   __syncthreads();
   if (lane == 31) w[warp] = inc;
   __syncthreads();
-  unsigned long long s = inc - v;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) s += i < warp ? w[i] : 0ull;
-  return s;
+  return warp_sum64(lane < warp ? w[lane] : 0ull) + inc - v;
+}
+
+// M <= kCand keys sorted, the largest first: thread i gets those at 2 i and 2 i + 1 (0 behind the
+// last).  Bitonic: partners up to 32 apart are in one warp and are exchanged in registers.
+struct Two {
+  unsigned long long x0, x1;
+};
+__device__ __noinline__ Two sorted_keys(unsigned long long* key, int M) {
+  int P = 64;
+  while (P < M) P *= 2;
+  const int e = 2 * threadIdx.x;
+  unsigned long long x0 = e < M ? key[e] : 0ull, x1 = e + 1 < M ? key[e + 1] : 0ull;
+  const bool on = P > 64 || threadIdx.x < 32;  // the first warp holds all, if they are few
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 2; k <= P; k *= 2) {
+    const bool down = (e & k) == 0;
+    int j = k / 2;
+#pragma unroll 1
+    for (; j >= 64; j /= 2) {
+      key[e] = x0, key[e + 1] = x1;
+      __syncthreads();
+      const unsigned long long y0 = key[e ^ j], y1 = key[(e + 1) ^ j];
+      const bool most = ((e & j) == 0) == down;
+      x0 = (x0 > y0) == most ? x0 : y0;
+      x1 = (x1 > y1) == most ? x1 : y1;
+      __syncthreads();
+    }
+    if (on) {
+#pragma unroll 1
+      for (; j >= 2; j /= 2) {
+        const unsigned long long y0 = __shfl_xor_sync(0xffffffffu, x0, j / 2), y1 = __shfl_xor_sync(0xffffffffu, x1, j / 2);
+        const bool most = ((e & j) == 0) == down;
+        x0 = (x0 > y0) == most ? x0 : y0;
+        x1 = (x1 > y1) == most ? x1 : y1;
+      }
+      const unsigned long long y0 = x0;
+      x0 = (x0 > x1) == down ? x0 : x1;
+      x1 = (y0 > x1) == down ? x1 : y0;
+    }
+  }
+  return Two{x0, x1};
 }
 
 // What is kept: logits above the threshold, and of those equal to it the tokens up to cut.
@@ -221,7 +260,7 @@ template <>
 SPEC_DEVICE_INLINE __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -276,16 +315,26 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       }
   }
 
-  // f(i, logit of i) for all of the slice, a thread's tokens in 16-byte pieces.
-  const auto each = [&](auto f) {
-    if (tid < head) f(tid, logit(tid));
-    if (tid < n - tail0) f(tail0 + tid, logit(tail0 + tid));
-#pragma unroll 2
+  // f(i, logit of i) for the slice's tokens from least_l on, read in 16-byte pieces.
+  const auto each_from = [&](float least_l, auto f) {
+    const auto one = [&](int i, unsigned hits) {  // tokens i + the places of the bits of hits
+#pragma unroll 1
+      for (; hits; hits &= hits - 1) {
+        const int at = i + __ffs(hits) - 1;
+        f(at, logit(at));
+      }
+    };
+    // what lies around the pieces: the first threads before, the last ones behind them
+    const int i = tid < kThreads / 2 ? tid : tail0 + (kThreads - 1 - tid);
+    one(i, (tid < head || (tid >= kThreads / 2 && i < n)) && logit(i) >= least_l ? 1u : 0u);
+#pragma unroll 1
     for (int j = tid; j < vecs; j += kThreads) {
       const uint4 w = reinterpret_cast<const uint4*>(val + head)[j];
       const T* e = reinterpret_cast<const T*>(&w);
+      unsigned m = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) f(head + j * PER + i, fmaxf(to_f32(e[i]), -INFINITY));
+      for (int k = 0; k < PER; ++k) m |= to_f32(e[k]) >= least_l ? 1u << k : 0u;
+      one(head + j * PER, m);
     }
   };
 
@@ -443,8 +492,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     __syncthreads();  // the bins have been read
     if (tid == 0) sh.picked = 0, sh.cand[(sent + 1) & 1] = 0;
     __syncthreads();
-    each([&](int i, float x) {
-      if (x >= least_l && is(i, x)) {
+    each_from(least_l, [&](int i, float x) {
+      if (is(i, x)) {
         const unsigned at = atomicAdd(&sh.picked, 1u);
         if (at < kCand) local[at] = (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
       }
@@ -466,45 +515,6 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
     cluster.sync();
     return sum_given();
   };
-  // In the first CTA: M <= kCand of its keys sorted, the largest first; thread i gets those at
-  // 2 i and 2 i + 1 (0 behind the last).  Bitonic: partners up to 32 apart are in one warp and are
-  // exchanged in registers.
-  auto sorted = [&](int M, unsigned long long& x0, unsigned long long& x1) {
-    int P = 64;
-    while (P < M) P *= 2;
-    const int e = 2 * tid;
-    x0 = e < M ? sh.key[e] : 0ull, x1 = e + 1 < M ? sh.key[e + 1] : 0ull;
-    const auto order = [](unsigned long long& hi, unsigned long long& lo, bool down) {
-      if ((hi < lo) == down) {
-        const unsigned long long t = hi;
-        hi = lo, lo = t;
-      }
-    };
-    const bool on = e < ((M + 63) & ~63) || P > 64;  // warps without a key sort nothing while that is all
-    __syncthreads();
-    for (int k = 2; k <= P; k *= 2) {
-      const bool down = (e & k) == 0;
-      for (int j = k / 2; j >= 64; j /= 2) {
-        sh.key[e] = x0, sh.key[e + 1] = x1;
-        __syncthreads();
-        const unsigned long long y0 = sh.key[e ^ j], y1 = sh.key[(e + 1) ^ j];
-        const bool first_half = (e & j) == 0;
-        x0 = (x0 > y0) == (first_half == down) ? x0 : y0;
-        x1 = (x1 > y1) == (first_half == down) ? x1 : y1;
-        __syncthreads();
-      }
-      if (on) {
-        for (int j = min(k / 2, 32); j >= 2; j /= 2) {
-          const unsigned long long y0 = __shfl_xor_sync(0xffffffffu, x0, j / 2), y1 = __shfl_xor_sync(0xffffffffu, x1, j / 2);
-          const bool first_half = (e & j) == 0;
-          x0 = (x0 > y0) == (first_half == down) ? x0 : y0;
-          x1 = (x1 > y1) == (first_half == down) ? x1 : y1;
-        }
-        order(x0, x1, down);
-      }
-    }
-  };
-
   // The shortest prefix (by rank) of the tokens of `in` whose measure reaches target, from the
   // bin of their first histogram that holds its end.
   auto select = [&](bool by_mass, unsigned long long target, const Kept& in, Found f) -> Kept {
@@ -523,7 +533,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         if (M <= kCand) {
           if (rank == 0) {
             unsigned long long x[2], m[2], before;
-            sorted((int)M, x[0], x[1]);
+            const Two k = sorted_keys(sh.key, (int)M);
+            x[0] = k.x0, x[1] = k.x1;
             const auto measure = [&](unsigned long long key) {
               return key == 0ull ? 0ull : by_mass ? R.mass(key_logit((uint32_t)(key >> 32))) : 1ull;
             };
@@ -607,8 +618,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
   auto finish = [&](int M, int nk, bool counted) {
     unsigned long long* const mass = reinterpret_cast<unsigned long long*>(&sh.h);  // by rank; the bins are done with
     static_assert(sizeof(Bins) >= kCand * sizeof(unsigned long long), "masses of candidates");
-    unsigned long long x0, x1;
-    sorted(M, x0, x1);
+    const Two k = sorted_keys(sh.key, M);
+    unsigned long long x0 = k.x0, x1 = k.x1;
     if (tid == 0) sh.found = x0;
     __syncthreads();
     R.mx = key_logit((uint32_t)(sh.found >> 32));
@@ -644,7 +655,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
       if (keep0) p.probs[row * V + (0xffffffffu - (uint32_t)x0)] = kept_share(m0, inv);
       if (keep1) p.probs[row * V + (0xffffffffu - (uint32_t)x1)] = kept_share(m1, inv);
     }
-    sorted(kept_n, x0, x1);
+    const Two by_index = sorted_keys(sh.key, kept_n);
+    x0 = by_index.x0, x1 = by_index.x1;
     const unsigned long long y0 = x0 ? mass[(uint32_t)x0] : 0ull, y1 = x1 ? mass[(uint32_t)x1] : 0ull;
     const unsigned long long c0 = block_before64(y0 + y1, sh.warp), c1 = c0 + y0;
     if (c0 <= t && t < c0 + y0) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(x0 >> 32));
