@@ -445,9 +445,9 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
  * the attention weights that the rows of sequence b's window give token t (positions below
  * weight_len), summed over the window's rows and the query heads of kv head h: what
  * spec_kv8_evict ranks by.  workspace: spec_kv8_attention_workspace() bytes for the same
- * arguments (-1: a shape the call refuses), as there. */
+ * arguments (0: none needed; -1: a shape the call refuses), as there. */
 int64_t spec_kv8_attention_workspace(int32_t B, int32_t W, int32_t total_rows, int32_t n_heads, int32_t n_kv_heads,
-                                     int32_t head_dim, int32_t max_pages, int32_t with_weight);
+                                     int32_t head_dim, int32_t max_pages, int32_t max_kv_len, int32_t with_weight);
 spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
                                const int32_t* page_table, int32_t max_pages, int32_t num_pages, int32_t n_heads,
                                int32_t n_kv_heads, int32_t head_dim, int32_t dtype, const void* q, int64_t q_stride,

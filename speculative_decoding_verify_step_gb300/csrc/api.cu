@@ -1692,15 +1692,22 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
 }
 
 int64_t spec_kv8_attention_workspace(int32_t B, int32_t W, int32_t total_rows, int32_t n_heads, int32_t n_kv_heads,
-                                     int32_t head_dim, int32_t max_pages, int32_t with_weight) {
+                                     int32_t head_dim, int32_t max_pages, int32_t max_kv_len, int32_t with_weight) {
   // as ragged rows: any number of them
   if (W < 1 || W > kMaxWidth ||
       kv4_check(B, total_rows, W, &max_pages, max_pages, 1, n_kv_heads, head_dim, SPEC_F16) ||
-      kv4_check_window(B, W, n_heads, n_kv_heads, max_pages, 0))
+      kv4_check_window(B, W, n_heads, n_kv_heads, max_pages, max_kv_len))
     return -1;
-  int sms = 0;
-  if (current_sm_count(&sms) != cudaSuccess) return -1;
-  return kv8_attention_workspace(W, n_heads, n_kv_heads, head_dim, total_rows, with_weight != 0, sms);
+  Kv8AttnParams p{};
+  p.B = B;
+  p.W = W;
+  p.total_rows = total_rows;
+  p.Hq = n_heads;
+  p.Hkv = n_kv_heads;
+  p.hd = head_dim;
+  p.kv_len_hint = kv4_len_hint(max_pages, max_kv_len, W);
+  if (current_sm_count(&p.sm_count) != cudaSuccess) return -1;
+  return kv8_attention_workspace(p, with_weight != 0);
 }
 
 spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,
@@ -1727,7 +1734,6 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
   if (spec_status s = kv4_check_ptr(q, "q")) return s;
   if (spec_status s = kv4_check_ptr(out, "out")) return s;
   if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
-  if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
   if (reinterpret_cast<uintptr_t>(weight) & 3u) return fail(SPEC_ERR_INVALID_ARG, "weight must be 4-byte aligned");
   if (spec_status s = kv4_check_stride(q_stride, (long long)n_heads * head_dim, "q_stride")) return s;
   Kv8AttnParams p{};
@@ -1752,8 +1758,13 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
   p.kv_len_hint = kv4_len_hint(max_pages, max_kv_len, W);
   p.weight = weight;
   p.weight_len = weight_len;
+  p.sm_count = 1 << 20;
+  if (kv8_attention_workspace(p, weight != nullptr) > 0)  // needed on any GPU
+    if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
   CUDA_TRY(current_sm_count(&p.sm_count));
-  const long long need = kv8_attention_workspace(W, n_heads, n_kv_heads, head_dim, total_rows, weight != nullptr, p.sm_count);
+  const long long need = kv8_attention_workspace(p, weight != nullptr);
+  if (need > 0)
+    if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
   if (workspace_bytes < need)
     return fail(SPEC_ERR_INVALID_ARG, "workspace_bytes=%lld, %lld needed", (long long)workspace_bytes, need);
   p.workspace = static_cast<float*>(workspace);

@@ -41,15 +41,16 @@ struct Kv8AttnParams {
   int sm_count, kv_len_hint;   // launch shape only
   float scale;                 // of q . k
   uint32_t anc[16];            // window rows that row j sees (bit i)
-  int slots;                   // CTAs resident at once: set by the launcher
+  int slots, cluster;          // CTAs resident at once, CTAs of a cluster: set by the launcher
   float* workspace;            // kv8_attention_workspace bytes: partials, then lse
   float* lse;                  // [total_rows, Hq] log2 of each row's sum of weights, or null: set by the launcher
   float* weight;               // [B, Hkv, weight_len] or null
   long long weight_len;
   int* status;
 };
-// Bytes of workspace: partials of cut groups, and with `weight` the rows' sums.
-long long kv8_attention_workspace(int W, int Hq, int Hkv, int hd, long long total_rows, bool weight, int sm_count);
+// Bytes of workspace of a call of p's shape (B, W, total_rows, Hq, Hkv, hd, sm_count, kv_len_hint):
+// partials of cut groups, and with `weight` the rows' sums.
+long long kv8_attention_workspace(const Kv8AttnParams& p, bool weight);
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t st);
 
 struct Kv8EvictParams {

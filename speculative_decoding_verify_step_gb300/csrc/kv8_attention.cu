@@ -24,7 +24,9 @@
 // takes one piece, a warp every fourth unit of it, with a ring of its own in shared memory
 // (bulk copies of 32 tokens: K, V and exponents are one run of bytes) and accumulators of
 // its own, so the loop has no CTA barrier.  The warps' results are merged at the end, those
-// of a cut group by a second kernel.
+// of a cut group by a second kernel.  Short caches need neither the common target nor the
+// second kernel: the CTAs of a group are one thread-block cluster, and each finishes a share
+// of the rows from all partials, through distributed shared memory.
 #include <math.h>
 
 #include <algorithm>
@@ -44,6 +46,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;             // tokens of a unit
 constexpr int kMinUnits = 4;          // of a piece: one for each warp
 constexpr int kMaxCtas = 3;           // per SM, of any variant
+constexpr int kMaxCluster = 8;
 constexpr float kNoMax = -1e30f;      // running maximum of a row that has seen no token
 constexpr float kSlack = 6.f;         // how far score + b may pass the running maximum
 
@@ -265,11 +268,13 @@ struct Cfg {
   static constexpr int kStages = kStages0 < 6 ? kStages0 : 6; // of a warp
   static constexpr int kSmem = kQ + kWarps * kStages * kStage;
   static_assert(kStages >= 2 && kCtas <= kMaxCtas, "ring");
-  static_assert(NT * 8 * HD * 4 <= kStages * kStage, "a warp's partial reuses its ring");
+  static constexpr int kRec = HD + 4;                         // floats of a row's partial for the cluster: O, maximum, sum
+  static_assert(NT * (8 * HD + 2 * kRec) * 4 <= kStages * kStage, "a warp's partial, and two rows of each tile of the CTA's, reuse its ring");
 };
 
-// grid (pieces, row blocks): rows [y NT 8, (y + 1) NT 8) of the group's.
-template <int HD, int NT>
+// grid (pieces, row blocks): rows [y NT 8, (y + 1) NT 8) of the group's.  CL: the p.cluster CTAs
+// of a group are one cluster, its pieces.
+template <int HD, int NT, bool CL>
 __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
     kv8_attention_kernel(const __grid_constant__ Kv8AttnParams p) {
   using C = Cfg<HD, NT>;
@@ -287,19 +292,31 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
   uint8_t* const ring = smem + C::kQ + warp * D * C::kStage;
 
   pdl_wait();
-  // the merge kernel reads the call's tables before its own wait: they are complete now
-  pdl_launch_dependents();
-  const Seq mine = first_seqs(p);
-  const int target = target_of(p, mine);
-  int before, before_cut;
-  const int b = find_piece(p, mine, target, blockIdx.x, before, before_cut);
-  if (b >= p.B) return;
-  const Seq seq = seq_at(p, mine, b);
-  const int pieces = pieces_of(seq.units, target);
-  const int kvh = (blockIdx.x - before) / pieces, piece = (blockIdx.x - before) % pieces;
-  const int slot = before_cut + (blockIdx.x - before);
+  // The merge kernel reads the call's tables before its own wait: they are complete now.  Clusters
+  // let the next kernel in only as they end: its first CTAs would take places that its other
+  // clusters, if it has any, then lack.
+  if (!CL) pdl_launch_dependents();
+  int b, kvh, piece, pieces, slot = 0;
+  Seq seq;
+  if constexpr (CL) {
+    pieces = p.cluster;
+    piece = blockIdx.x % pieces;
+    kvh = blockIdx.x / pieces % p.Hkv;
+    b = blockIdx.x / pieces / p.Hkv;
+    seq = seq_of(p, b);
+  } else {
+    const Seq mine = first_seqs(p);
+    const int target = target_of(p, mine);
+    int before, before_cut;
+    b = find_piece(p, mine, target, blockIdx.x, before, before_cut);
+    if (b >= p.B) return;
+    seq = seq_at(p, mine, b);
+    pieces = pieces_of(seq.units, target);
+    kvh = (blockIdx.x - before) / pieces, piece = (blockIdx.x - before) % pieces;
+    slot = before_cut + (blockIdx.x - before);
+  }
   const int r0 = blockIdx.y * ROWS, rows = min(seq.Wb * grp - r0, ROWS);  // of this CTA
-  if (rows <= 0) return;
+  if (rows <= 0) return;  // (all CTAs of a cluster alike)
   const int u0 = (int)((long long)seq.units * piece / pieces);
   const int u1 = (int)((long long)seq.units * (piece + 1) / pieces);
   const int L = seq.L, n_keys = seq.n_keys;
@@ -490,8 +507,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
     }
   __syncthreads();
   constexpr int V4 = HD / 4;
-  const bool whole = pieces == 1;
-  float* const ws = partial(p.workspace, (long long)slot * gridDim.y + blockIdx.y, ROWS, HD);
+  const bool whole = !CL && pieces == 1;
+  float* const ws = CL ? nullptr : partial(p.workspace, (long long)slot * gridDim.y + blockIdx.y, ROWS, HD);
+  // row r of the CTA's partial, for the cluster: behind warp r % 4's own
+  const auto record = [&](int r) {
+    return reinterpret_cast<float*>(smem + C::kQ + (r & 3) * D * C::kStage) + ROWS * HD + (r >> 2) * C::kRec;
+  };
   for (int it = threadIdx.x; it < rows * V4; it += kThreads) {
     const int r = it / V4, d4 = it % V4;
     float M = kNoMax, l = 0.f;
@@ -514,12 +535,53 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
       store_row4(p, row, head, HD, d4, o, s_fail ? 1.f : l);
       if (d4 == 0) store_lse(p, row, head, M, l);
     } else {
-      *reinterpret_cast<float4*>(ws + r * HD + d4 * 4) = o;
+      float* const rec = CL ? record(r) : ws + r * HD;
+      *reinterpret_cast<float4*>(rec + d4 * 4) = o;
       if (d4 == 0) {
-        ws[ROWS * HD + r] = M;
-        ws[ROWS * HD + ROWS + r] = l;
+        (CL ? rec + HD : ws + ROWS * HD + r)[0] = M;
+        (CL ? rec + HD + 1 : ws + ROWS * HD + ROWS + r)[0] = l;
       }
     }
+  }
+  if constexpr (CL) {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    // rows piece, piece + pieces, ...: sum_i 2^(m_i - M) o_i over the cluster
+    const int own = (rows - piece + pieces - 1) / pieces;
+    for (int it = threadIdx.x; it < own * V4; it += kThreads) {
+      const int r = piece + it / V4 * pieces, d4 = it % V4;
+      const uint32_t at = smem_u32(record(r));
+      float m[kMaxCluster], s1[kMaxCluster], M = kNoMax, l = 0.f;
+      float4 x[kMaxCluster], o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i)
+        if (i < pieces) {
+          const uint32_t a = mapa_u32(at, i);
+          x[i] = ld_dsmem_f4(a + d4 * 16);
+          m[i] = ld_dsmem_f32(a + HD * 4);
+          s1[i] = ld_dsmem_f32(a + HD * 4 + 4);
+        }
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i)
+        if (i < pieces) M = fmaxf(M, m[i]);
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i)
+        if (i < pieces) {
+          const float a = ex2(m[i] - M);
+          l = fmaf(a, s1[i], l);
+          o.x = fmaf(a, x[i].x, o.x);
+          o.y = fmaf(a, x[i].y, o.y);
+          o.z = fmaf(a, x[i].z, o.z);
+          o.w = fmaf(a, x[i].w, o.w);
+        }
+      const int row = seq.row0 + (r0 + r) / grp, head = kvh * grp + (r0 + r) % grp;
+      store_row4(p, row, head, HD, d4, l == l ? o : make_float4(NAN, NAN, NAN, NAN), l == l ? l : 1.f);
+      if (d4 == 0) store_lse(p, row, head, M, l);
+    }
+    __syncwarp();
+    cluster_arrive_relaxed();  // its reads are done: no CTA leaves before all have
+    cluster_wait();
   }
 }
 
@@ -718,19 +780,34 @@ cudaError_t configure(K kernel, int smem, std::atomic<uint64_t>& done) {
 constexpr int row_blocks(int rows) { return rows > 32 ? 2 : 1; }
 constexpr int row_tiles(int rows) { return ((rows + 7) / 8 + row_blocks(rows) - 1) / row_blocks(rows); }
 
+// CTAs of a group where they are one cluster: short caches, by the hint.  0: not short.
+int cluster_size(int B, int Hkv, int rows, int len_hint, int sm_count) {
+  const long long groups = (long long)B * Hkv * row_blocks(rows), units = (len_hint + kUnit - 1) / kUnit;
+  int cs = 1;
+  while (cs < kMaxCluster && cs * kMinUnits < units && groups * cs * 2 <= 2 * sm_count) cs *= 2;
+  return units <= 16 * cs && groups <= (1 << 27) ? cs : 0;
+}
+
 template <int HD, int NT>
 cudaError_t launch_nt(Kv8AttnParams p, cudaStream_t st) {
   using C = Cfg<HD, NT>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = configure(kv8_attention_kernel<HD, NT>, C::kSmem, done);
-  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> done{0}, done_cl{0};
   const int rows = p.W * (p.Hq / p.Hkv), blocks = row_blocks(rows);
+  if (const int cs = cluster_size(p.B, p.Hkv, rows, p.kv_len_hint, p.sm_count)) {
+    cudaError_t e = configure(kv8_attention_kernel<HD, NT, true>, C::kSmem, done_cl);
+    if (e != cudaSuccess) return e;
+    p.cluster = cs;
+    return launch_k_cluster(kv8_attention_kernel<HD, NT, true>, dim3((unsigned)(p.B * p.Hkv * cs), blocks), dim3(kThreads),
+                            C::kSmem, st, dim3(cs, 1, 1), p);
+  }
+  cudaError_t e = configure(kv8_attention_kernel<HD, NT, false>, C::kSmem, done);
+  if (e != cudaSuccess) return e;
   p.slots = std::max(2, C::kCtas * p.sm_count / blocks);
   // as many CTAs as any lengths can make of it; pieces number groups + units / target at most
   const long long groups = (long long)p.B * p.Hkv;
   const long long ctas = groups + std::max<long long>(p.slots - groups, p.slots / 2);
   if (ctas > 0x7fffffffll) return cudaErrorInvalidValue;
-  e = launch_k(kv8_attention_kernel<HD, NT>, dim3((unsigned)ctas, blocks), dim3(kThreads), C::kSmem, st, p);
+  e = launch_k(kv8_attention_kernel<HD, NT, false>, dim3((unsigned)ctas, blocks), dim3(kThreads), C::kSmem, st, p);
   if (e != cudaSuccess) return e;
   const int n = (int)std::max<long long>(1, p.slots / groups);
   const int at_once = kMergeWarps / merge_split(n) * (128 / HD);
@@ -764,19 +841,21 @@ cudaError_t launch_hd(const Kv8AttnParams& p, cudaStream_t st) {
 }
 
 // Floats of the partials: pieces of cut groups, at most two per slot.
-long long partial_floats(int rows, int hd, int sm_count) {
-  return 2ll * (kMaxCtas * sm_count) * row_tiles(rows) * 8 * row_blocks(rows) * (hd + 2);
+long long partial_floats(const Kv8AttnParams& p) {
+  const int rows = p.W * (p.Hq / p.Hkv);
+  if (cluster_size(p.B, p.Hkv, rows, p.kv_len_hint, p.sm_count)) return 0;
+  return 2ll * (kMaxCtas * p.sm_count) * row_tiles(rows) * 8 * row_blocks(rows) * (p.hd + 2);
 }
 
 }  // namespace
 
-long long kv8_attention_workspace(int W, int Hq, int Hkv, int hd, long long total_rows, bool weight, int sm_count) {
-  return 4 * (partial_floats(W * (Hq / Hkv), hd, sm_count) + (weight ? total_rows * Hq : 0));
+long long kv8_attention_workspace(const Kv8AttnParams& p, bool weight) {
+  return 4 * (partial_floats(p) + (weight ? (long long)p.total_rows * p.Hq : 0));
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnParams& params, cudaStream_t st) {
   Kv8AttnParams p = params;
-  p.lse = p.weight ? p.workspace + partial_floats(p.W * (p.Hq / p.Hkv), p.hd, p.sm_count) : nullptr;
+  p.lse = p.weight ? p.workspace + partial_floats(p) : nullptr;
   return p.hd == 128 ? launch_hd<128>(p, st) : launch_hd<64>(p, st);
 }
 

@@ -104,7 +104,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "spec_kv8_block_bytes": (I64, [I32]),
         "spec_kv8_write": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, I64, I64, P, P]),
         "spec_kv8_read": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, P, P, P, P]),
-        "spec_kv8_attention_workspace": (I64, [I32, I32, I32, I32, I32, I32, I32, I32]),
+        "spec_kv8_attention_workspace": (I64, [I32, I32, I32, I32, I32, I32, I32, I32, I32]),
         "spec_kv8_attention": (I32, [I32, I32, I32, P, P, P, I32, I32, I32, I32, I32, I32, P, I64, P, F32, I32, P, P,
                                      P, I64, P, I64, P]),
         "spec_kv8_evict": (I32, [I32, P, P, I32, P, I32, I32, I32, I32, I32, I32, P, I64, P, P, P, P, I64, P]),
@@ -675,11 +675,13 @@ def spec_kv8_read(pool: torch.Tensor, start: torch.Tensor, page_table: torch.Ten
         raise ValueError("n must not be negative")
     shape = (n, H, hd) if ragged else (B, n, H, hd)
     if outs is None:
-        outs = (torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev))
-    k, v = outs
-    for t in (k, v):
-        if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"outs must be contiguous {dtype} tensors of shape {shape} on {dev}")
+        k = torch.empty(shape, dtype=dtype, device=dev)
+        v = torch.empty_like(k)
+    else:
+        k, v = outs
+        for t in (k, v):
+            if t.dtype != dtype or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"outs must be contiguous {dtype} tensors of shape {shape} on {dev}")
     _kv4_call(dev, lib.spec_kv8_read, B, 0 if ragged else n, n if ragged else B * n,
               row_off.data_ptr() if ragged else None, start.data_ptr(), page_table.data_ptr(), width, P,
               H, hd, _KV4_DTYPE[dtype], pool.data_ptr(), k.data_ptr(), v.data_ptr())
@@ -723,7 +725,7 @@ def spec_kv8_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != q.dtype or out.device != dev or out.shape != q.shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
-    key = (dev.index, B, W, total, Hq, H, hd, width, int(T > 0))
+    key = (dev.index, B, W, total, Hq, H, hd, width, max_kv_len, int(T > 0))
     size = _KV8_WORKSPACE.get(key)
     if size is None:
         if len(_KV8_WORKSPACE) > 4096:
@@ -756,13 +758,16 @@ def spec_kv8_evict(pool: torch.Tensor, weight: torch.Tensor, kv_len: torch.Tenso
     if keep < 1 or not 0 <= recent <= keep:
         raise ValueError("keep must be at least 1 and recent between 0 and keep")
     if outs is None:
-        outs = (torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, H, keep, dtype=torch.int32, device=dev),
-                torch.empty(B, H, max(T, keep), dtype=torch.float32, device=dev))
-    new_len, kept, wout = outs
-    for t, shape, what in ((new_len, (B,), "new_len"), (kept, (B, H, keep), "kept")):
-        if t.dtype is not torch.int32 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape} on {dev}")
-    To = _kv8_weight(wout, "the weights' output", B, H, dev)
+        new_len = torch.empty(B, dtype=torch.int32, device=dev)
+        kept = torch.empty(B, H, keep, dtype=torch.int32, device=dev)
+        wout = torch.empty_like(weight) if T >= keep else torch.empty(B, H, keep, dtype=torch.float32, device=dev)
+        To = max(T, keep)
+    else:
+        new_len, kept, wout = outs
+        for t, shape, what in ((new_len, (B,), "new_len"), (kept, (B, H, keep), "kept")):
+            if t.dtype is not torch.int32 or t.device != dev or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{what} must be a contiguous int32 tensor of shape {shape} on {dev}")
+        To = _kv8_weight(wout, "the weights' output", B, H, dev)
     _kv4_call(dev, lib.spec_kv8_evict, B, kv_len.data_ptr(), page_table.data_ptr(), width, dst_table.data_ptr(),
               dst_table.shape[1], P, H, hd, keep, recent, weight.data_ptr(), T, pool.data_ptr(), new_len.data_ptr(),
               kept.data_ptr(), wout.data_ptr(), To)
@@ -822,14 +827,15 @@ def spec_sample(logits: torch.Tensor, u: Optional[torch.Tensor] = None, temperat
     top_p = _setting(top_p, torch.float32, n, dev, "top_p")
     min_p = _setting(min_p, torch.float32, n, dev, "min_p")
     if outs is None:
-        outs = (torch.empty(lead, dtype=torch.int32, device=dev),
-                torch.empty(shape, dtype=torch.float32, device=dev) if return_probs else None)
-    tokens, probs = outs
-    if tokens.dtype is not torch.int32 or tokens.device != dev or tokens.shape != lead or not tokens.is_contiguous():
-        raise ValueError(f"tokens must be a contiguous int32 tensor of shape {tuple(lead)} on {dev}")
-    if probs is not None and (probs.dtype is not torch.float32 or probs.device != dev or probs.shape != shape
-                              or not probs.is_contiguous()):
-        raise ValueError(f"probs must be a contiguous fp32 tensor of shape {tuple(shape)} on {dev}")
+        tokens = torch.empty(lead, dtype=torch.int32, device=dev)
+        probs = torch.empty(shape, dtype=torch.float32, device=dev) if return_probs else None
+    else:
+        tokens, probs = outs
+        if tokens.dtype is not torch.int32 or tokens.device != dev or tokens.shape != lead or not tokens.is_contiguous():
+            raise ValueError(f"tokens must be a contiguous int32 tensor of shape {tuple(lead)} on {dev}")
+        if probs is not None and (probs.dtype is not torch.float32 or probs.device != dev or probs.shape != shape
+                                  or not probs.is_contiguous()):
+            raise ValueError(f"probs must be a contiguous fp32 tensor of shape {tuple(shape)} on {dev}")
     ptr = [None if t is None else t.data_ptr() for t in (u, temperature, top_k, top_p, min_p, probs)]
     _kv4_call(dev, lib.spec_sample, rows, V, logits.data_ptr(), dtype, stride, ptr[0], t_all, *ptr[1:5],
               rows_per_setting, tokens.data_ptr(), ptr[5])

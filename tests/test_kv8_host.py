@@ -136,7 +136,7 @@ def test_read_refusals(spec, kw):
     (dict(n=0, total=0), 1), (dict(n=17, total=34), 1), (dict(Hq=5), 1), (dict(Hq=0), 1), (dict(q=None), 1),
     (dict(out=None), 1), (dict(q=4104), 1), (dict(out=4104), 1), (dict(qs=248), 1), (dict(qs=260), 1),
     (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(scale=1.2e12), 1), (dict(hint=-1), 1),
-    (dict(ws=None), 1), (dict(ws=4100), 1), (dict(weight=4096, T=0), 1), (dict(weight=4098, T=64), 1),
+    (dict(ws=None, max_pages=4096), 1), (dict(ws=4100, max_pages=4096), 1), (dict(weight=4096, T=0), 1), (dict(weight=4098, T=64), 1),
     (dict(n=9, total=18, Hq=16), 7),                                  # 9 rows x 8 heads of a group
     (dict(H=1 << 14, Hq=1 << 14, max_pages=1 << 16), 7),
     (dict(parent=(ctypes.c_int32 * 3)(0, 0, 1)), 1), (dict(parent=(ctypes.c_int32 * 3)(-1, 1, 0)), 1)])
@@ -152,8 +152,9 @@ def test_no_rows_is_no_work(spec, call):
 
 def test_block_bytes_and_workspace(spec):
     assert [spec._lib.spec_kv8_block_bytes(h) for h in (64, 128, 96, 0)] == [8256, 16448, 0, 0]
-    for bad in ((0, 1, 1, 4, 2, 64, 4, 0), (1, 17, 1, 4, 2, 64, 4, 0), (1, 1, 1, 5, 2, 64, 4, 0), (1, 1, 1, 4, 2, 96, 4, 0),
-                (1, 16, 16, 16, 2, 64, 4, 0), (1, 1, -1, 4, 2, 64, 4, 0)):
+    for bad in ((0, 1, 1, 4, 2, 64, 4, 0, 0), (1, 17, 1, 4, 2, 64, 4, 0, 0), (1, 1, 1, 5, 2, 64, 4, 0, 0),
+                (1, 1, 1, 4, 2, 96, 4, 0, 0), (1, 16, 16, 16, 2, 64, 4, 0, 0), (1, 1, -1, 4, 2, 64, 4, 0, 0),
+                (1, 1, 1, 4, 2, 64, 4, -1, 0)):
         assert spec._lib.spec_kv8_attention_workspace(*bad) == -1
 
 
