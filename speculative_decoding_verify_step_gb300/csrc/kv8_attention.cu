@@ -780,12 +780,17 @@ cudaError_t configure(K kernel, int smem, std::atomic<uint64_t>& done) {
 constexpr int row_blocks(int rows) { return rows > 32 ? 2 : 1; }
 constexpr int row_tiles(int rows) { return ((rows + 7) / 8 + row_blocks(rows) - 1) / row_blocks(rows); }
 
-// CTAs of a group where they are one cluster: short caches, by the hint.  0: not short.
+// CTAs of a group where they are one cluster: short caches, by the hint.  0: not short.  A CTA gets
+// at most 40 units where the clusters fill the SMs, 20 where they leave some idle.  Clusters
+// against pieces, in us (8 kv heads of 128 with 4 query heads; units of a CTA in brackets): decode,
+// 1 x 4096 tokens 8.9, 9.2 (16), 1 x 8192 11.7, 9.9 (32); 4 x 4096 10.0, 12.1 (32), 8 x 2048 9.8, 11.4
+// (32); width 5, 4 x 4096 17.1, 18.1 (32), 16 x 1024 17.9, 19.5 (32); 16 x 5003, 4 heads of 64,
+// width 4 12.0, 12.6 (40).
 int cluster_size(int B, int Hkv, int rows, int len_hint, int sm_count) {
   const long long groups = (long long)B * Hkv * row_blocks(rows), units = (len_hint + kUnit - 1) / kUnit;
   int cs = 1;
   while (cs < kMaxCluster && cs * kMinUnits < units && groups * cs * 2 <= 2 * sm_count) cs *= 2;
-  return units <= 16 * cs && groups <= (1 << 27) ? cs : 0;
+  return units <= (groups * cs > sm_count ? 40 : 20) * cs && groups <= (1 << 27) ? cs : 0;
 }
 
 template <int HD, int NT>
