@@ -8,12 +8,16 @@
 // Two kernels.  The first takes one CTA per (sequence, kv head): its weights, as integers
 // that order like them, come into shared memory once (up to 48 K tokens; of longer ones
 // they are read from L2 again) and a radix select of 11, 11 and 10 bits finds the
-// threshold.  11 bits, because weights spread over exponents: with 8 most lanes of a warp
-// would add to the same counter.  Warps own runs of neighbouring tokens, so the tokens that
-// stay come out in order from two scans of 32 counts.  The second kernel takes one warp per
-// destination sub-block and head.  A token's K is one run of bytes, its V one byte of each
-// word of a run four times as long (four tokens share the words), so V is read up to four
-// times over where neighbours do not stay together.
+// threshold, the last two digits among the few tokens that share the first.  11 bits, because
+// weights spread over exponents: with 8 most lanes of a warp would add to the same counter.
+// Warps own runs of neighbouring tokens, four to a lane, so the tokens that stay come out in
+// order from a scan of the warps' counts.  It is bound by one SM's integer pipe: passes of one
+// token to a lane and step over all tokens took 35 us for 64 heads of 32768 tokens, and
+// clusters of four CTAs, whose barriers cost about 1 us each, 32.
+//
+// The second kernel takes one warp per destination sub-block and head.  A token's K is one run of
+// bytes; its V is one byte of each word of a run of a whole sub-block (four tokens share a
+// word), so where neighbours do not stay together, V is mostly read whole.
 #include <math.h>
 
 #include <algorithm>
@@ -30,7 +34,8 @@ namespace {
 
 constexpr int kPickThreads = 1024;
 constexpr int kPickWarps = kPickThreads / 32;
-constexpr int kPickKeys = 48 * 1024;  // weights held in shared memory
+constexpr int kPickKeys = 48 * 1024;  // weights held in shared memory; whole steps of 128
+constexpr int kPickList = 2048;
 
 // Orders like the weight; NaN lowest, -0 as 0.
 SPEC_DEVICE_INLINE uint32_t weight_key(float w) {
@@ -46,10 +51,11 @@ SPEC_DEVICE_INLINE int seq_tokens(const Kv8EvictParams& p, int b) {
 
 // grid (Hkv, B)
 __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_constant__ Kv8EvictParams p) {
-  extern __shared__ uint32_t keys[];
-  __shared__ unsigned int hist[2048];
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ __align__(8) unsigned int hist[2048];
+  __shared__ int list[kPickList];       // tokens that share the threshold's first digit
   __shared__ unsigned int wsum[kPickWarps], weq[kPickWarps];
-  __shared__ unsigned int s_bin, s_above;
+  __shared__ unsigned int s_bin, s_above, s_list;
   pdl_wait();
   pdl_launch_dependents();
   const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -59,40 +65,66 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
   float* wout = p.weight_out + group * p.weight_out_len;
   const int n = seq_tokens(p, b), m = min(n, p.keep);
   if (h == 0 && tid == 0) p.new_len[b] = m;
-  for (long long i = m + tid; i < p.weight_out_len; i += kPickThreads) wout[i] = 0.f;
   for (int i = m + tid; i < p.keep; i += kPickThreads) kept[i] = -1;
+  const auto zeros = [&] {
+    for (long long i = (long long)m + tid; i < p.weight_out_len; i += kPickThreads) wout[i] = 0.f;
+  };
   if (n == m) {
     for (int i = tid; i < m; i += kPickThreads) {
       kept[i] = i;
       wout[i] = w[i];
     }
+    zeros();
     return;
   }
   const int last = n - min(p.recent, m);   // tokens [last, n) stay anyway
   const unsigned need = (unsigned)(m - (n - last));
   const bool held = n <= kPickKeys;
   const auto key_at = [&](int i) { return held ? keys[i] : weight_key(w[i]); };
-  uint32_t t = 0xffffffffu;                // threshold: keys above it stay, and `eq` of those equal to it
-  unsigned eq = 0;
+  // keys of tokens i .. i + 3 (i a multiple of 4; anything behind the last)
+  const auto keys4 = [&](int i) {
+    if (held) return *reinterpret_cast<const uint4*>(&keys[i]);
+    return make_uint4(weight_key(w[min(i, n - 1)]), weight_key(w[min(i + 1, n - 1)]), weight_key(w[min(i + 2, n - 1)]),
+                      weight_key(w[min(i + 3, n - 1)]));
+  };
+  uint32_t t = 0xffffffffu;                // threshold: keys above it stay, and `eq` of the `ties` equal to it
+  unsigned eq = 0, ties = 0;
   if (need > 0) {
-    if (held)
-      for (int i = tid; i < n; i += kPickThreads) keys[i] = weight_key(w[i]);
-    uint32_t prefix = 0, mask = 0;
+    for (int i = tid; i < 2048; i += kPickThreads) hist[i] = 0;
+    if (tid == 0) s_list = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int i = tid; i < last; i += kPickThreads) {
+      const uint32_t k = weight_key(w[i]);
+      if (held) keys[i] = k;
+      atomicAdd(&hist[k >> 21], 1u);
+    }
+    zeros();  // under the loads' latency
+    uint32_t prefix = 0;
     unsigned left = need;
-#pragma unroll
+    int M = -1;                            // tokens of the list; -1: all
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const uint32_t digit = pass == 2 ? 1023u : 2047u;
-      hist[tid] = hist[tid + kPickThreads] = 0;
-      __syncthreads();
-      for (int i = tid; i < last; i += kPickThreads) {
-        const uint32_t k = key_at(i);
-        if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+      const uint32_t digit = pass == 2 ? 1023u : 2047u, mask = pass == 2 ? ~1023u : ~0u << 21;
+      if (pass > 0) {
+        const auto count = [&](uint32_t k) {
+          if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1u);
+        };
+        if (M >= 0)
+          for (int i = tid; i < M; i += kPickThreads) count(key_at(list[i]));
+        else
+          for (int i = 4 * tid; i < last; i += 4 * kPickThreads) {
+            const uint4 k = keys4(i);
+            count(k.x);
+            if (i + 1 < last) count(k.y);
+            if (i + 2 < last) count(k.z);
+            if (i + 3 < last) count(k.w);
+          }
       }
       __syncthreads();
       // bins from the top: thread i has bins 2047 - 2 i and 2046 - 2 i
-      const unsigned c0 = hist[2047 - 2 * tid], c1 = hist[2046 - 2 * tid];
-      unsigned inc = c0 + c1;
+      const uint2 c = *reinterpret_cast<const uint2*>(&hist[2046 - 2 * tid]);
+      unsigned inc = c.x + c.y;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
@@ -100,57 +132,88 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
       }
       if (lane == 31) wsum[warp] = inc;
       __syncthreads();
-      unsigned before = inc - c0 - c1;
-      for (int i = 0; i < warp; ++i) before += wsum[i];
-      if (before < left && left <= before + c0) {
-        s_bin = 2047 - 2 * tid;
-        s_above = before;
-      } else if (before + c0 < left && left <= before + c0 + c1) {
-        s_bin = 2046 - 2 * tid;
-        s_above = before + c0;
+      const unsigned before = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u) + inc - c.x - c.y;
+      *reinterpret_cast<uint2*>(&hist[2 * tid]) = make_uint2(0u, 0u);  // for the next pass: all have read theirs
+      if (before < left && left <= before + c.y) {
+        s_bin = 2047 - 2 * tid, s_above = before, ties = c.y;
+        weq[0] = c.y;
+      } else if (before + c.y < left && left <= before + c.y + c.x) {
+        s_bin = 2046 - 2 * tid, s_above = before + c.y;
+        weq[0] = c.x;
       }
       __syncthreads();
       prefix |= s_bin << shift;
-      mask |= digit << shift;
       left -= s_above;
+      ties = weq[0];
+      if (pass == 0 && ties <= kPickList) {  // line them up
+        const auto put = [&](uint32_t k, int i) {
+          if ((k >> 21) == s_bin && i < last) list[atomicAdd(&s_list, 1u)] = i;
+        };
+#pragma unroll 2
+        for (int i = 4 * tid; i < last; i += 4 * kPickThreads) {
+          const uint4 k = keys4(i);
+          put(k.x, i), put(k.y, i + 1), put(k.z, i + 2), put(k.w, i + 3);
+        }
+        M = (int)ties;
+      }
+      __syncthreads();
     }
     t = prefix;
     eq = left;
+  } else {
+    zeros();
   }
-  // A warp's run of neighbouring tokens: counts, then places.
-  const int run = ((n + kPickWarps - 1) / kPickWarps + 31) & ~31;
+  // A warp's run of neighbouring tokens, 128 a step: counts, then places.
+  const int run = ((n + kPickWarps - 1) / kPickWarps + 127) & ~127;
   const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
-  // 2: stays whatever the ties, 1: equal to the threshold
-  const auto kind = [&](int i) {
-    if (i >= last) return 2;
-    if (need == 0) return 0;
-    const uint32_t k = key_at(i);
-    return k > t ? 2 : k == t ? 1 : 0;
-  };
-  unsigned gt = 0, ties = 0;
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const int k = i0 + lane < r1 ? kind(i0 + lane) : 0;
-    gt += __popc(__ballot_sync(0xffffffffu, k == 2));
-    ties += __popc(__ballot_sync(0xffffffffu, k == 1));
+  const bool cut = eq < ties;              // not all of the ties stay: the first ones
+  const auto above = [&](uint32_t k, int i) { return i < n && (i >= last || (need > 0 && k > t)); };
+  const auto equal = [&](uint32_t k, int i) { return i < last && need > 0 && k == t; };
+  unsigned gt = 0, tie = 0;
+#pragma unroll 2
+  for (int i = r0 + 4 * lane; i < r1; i += 128) {
+    const uint4 k = keys4(i);
+    gt += above(k.x, i) + above(k.y, i + 1) + above(k.z, i + 2) + above(k.w, i + 3);
+    tie += equal(k.x, i) + equal(k.y, i + 1) + equal(k.z, i + 2) + equal(k.w, i + 3);
   }
+  gt = __reduce_add_sync(0xffffffffu, gt), tie = __reduce_add_sync(0xffffffffu, tie);
+  if (lane == 0) wsum[warp] = gt, weq[warp] = tie;
   __syncthreads();
-  if (lane == 0) wsum[warp] = gt, weq[warp] = ties;
-  __syncthreads();
-  unsigned gt0 = 0, eq0 = 0;
-  for (int i = 0; i < warp; ++i) gt0 += wsum[i], eq0 += weq[i];
-  for (int i0 = r0; i0 < r1; i0 += 32) {
-    const int i = i0 + lane;
-    const int k = i < r1 ? kind(i) : 0;
-    const unsigned bg = __ballot_sync(0xffffffffu, k == 2), be = __ballot_sync(0xffffffffu, k == 1);
-    const unsigned below = (1u << lane) - 1u;
-    const unsigned ge = eq0 + __popc(be & below), gg = gt0 + __popc(bg & below);
-    if (k == 2 || (k == 1 && ge < eq)) {
-      const unsigned at = gg + min(ge, eq);
-      kept[at] = i;
-      wout[at] = w[i];
+  unsigned at0 = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
+  unsigned eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? weq[lane] : 0u);
+  at0 += min(eq0, eq);
+  const unsigned below = (1u << lane) - 1u;
+  for (int i0 = r0; i0 < r1; i0 += 128) {
+    const int i = i0 + 4 * lane;
+    const uint4 k4 = keys4(i);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    bool in[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) in[j] = above(k[j], i + j) || (!cut && equal(k[j], i + j));
+    if (cut) {  // the tokens' ranks among the ties
+      unsigned before = eq0, mine = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned e = __ballot_sync(0xffffffffu, equal(k[j], i + j));
+        before += __popc(e & below), eq0 += __popc(e);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (equal(k[j], i + j)) in[j] = before + mine++ < eq;
     }
-    gt0 += __popc(bg);
-    eq0 += __popc(be);
+    unsigned at = at0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const unsigned f = __ballot_sync(0xffffffffu, in[j]);
+      at += __popc(f & below), at0 += __popc(f);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (in[j]) {
+        kept[at] = i + j;
+        wout[at] = w[i + j];
+        ++at;
+      }
   }
 }
 
@@ -299,7 +362,8 @@ cudaError_t launch_kv8_evict(const Kv8EvictParams& p, cudaStream_t st) {
     done.fetch_or(1ull << (dev & 63), std::memory_order_release);
   }
   const long long most = std::min((long long)p.max_pages * kPage, p.weight_len);
-  const size_t smem = (size_t)std::min<long long>(most, kPickKeys) * 4;
+  // whole steps of 128 tokens: a warp's last step reads past the last one
+  const size_t smem = (size_t)std::min<long long>((most + 127) & ~127ll, kPickKeys) * 4;
   e = launch_k(kv8_pick_kernel, dim3(p.Hkv, p.B), dim3(kPickThreads), smem, st, p);
   if (e != cudaSuccess) return e;
   const long long total = (long long)p.B * p.Hkv * ((p.keep + kSub - 1) / kSub);
