@@ -44,6 +44,10 @@ SPEC_DEVICE_INLINE uint32_t weight_key(float w) {
   return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
+SPEC_DEVICE_INLINE float key_weight(uint32_t k) {
+  return k == 0u ? NAN : __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+}
+
 SPEC_DEVICE_INLINE int seq_tokens(const Kv8EvictParams& p, int b) {
   const long long cap = min((long long)p.max_pages * kPage, p.weight_len);
   return (int)max(0ll, min((long long)p.kv_len[b], cap));
@@ -93,13 +97,12 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
     for (int i = tid; i < 2048; i += kPickThreads) hist[i] = 0;
     if (tid == 0) s_list = 0;
     __syncthreads();
-#pragma unroll 8
-    for (int i = tid; i < last; i += kPickThreads) {
+#pragma unroll 16
+    for (int i = tid; i < n; i += kPickThreads) {
       const uint32_t k = weight_key(w[i]);
       if (held) keys[i] = k;
-      atomicAdd(&hist[k >> 21], 1u);
+      if (i < last) atomicAdd(&hist[k >> 21], 1u);
     }
-    zeros();  // under the loads' latency
     uint32_t prefix = 0;
     unsigned left = need;
     int M = -1;                            // tokens of the list; -1: all
@@ -160,9 +163,8 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
     }
     t = prefix;
     eq = left;
-  } else {
-    zeros();
   }
+  zeros();
   // A warp's run of neighbouring tokens, 128 a step: counts, then places.
   const int run = ((n + kPickWarps - 1) / kPickWarps + 127) & ~127;
   const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
@@ -211,7 +213,7 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
     for (int j = 0; j < 4; ++j)
       if (in[j]) {
         kept[at] = i + j;
-        wout[at] = w[i + j];
+        wout[at] = held && need > 0 ? key_weight(k[j]) : w[i + j];
         ++at;
       }
   }
