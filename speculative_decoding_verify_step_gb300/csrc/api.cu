@@ -1705,6 +1705,7 @@ int64_t spec_kv8_attention_workspace(int32_t B, int32_t W, int32_t total_rows, i
   p.Hq = n_heads;
   p.Hkv = n_kv_heads;
   p.hd = head_dim;
+  p.max_pages = max_pages;
   p.kv_len_hint = kv4_len_hint(max_pages, max_kv_len, W);
   if (current_sm_count(&p.sm_count) != cudaSuccess) return -1;
   return kv8_attention_workspace(p, with_weight != 0);

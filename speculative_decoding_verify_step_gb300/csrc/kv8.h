@@ -44,12 +44,13 @@ struct Kv8AttnParams {
   int slots, cluster;          // CTAs resident at once, CTAs of a cluster: set by the launcher
   float* workspace;            // kv8_attention_workspace bytes: partials, then lse
   float* lse;                  // [total_rows, Hq] log2 of each row's sum of weights, or null: set by the launcher
+  float* scores;               // [B, Hkv, units of 32 tokens, rows, 32] or null: set by the launcher
   float* weight;               // [B, Hkv, weight_len] or null
   long long weight_len;
   int* status;
 };
-// Bytes of workspace of a call of p's shape (B, W, total_rows, Hq, Hkv, hd, sm_count, kv_len_hint):
-// partials of cut groups, and with `weight` the rows' sums.
+// Bytes of workspace of a call of p's shape (B, W, total_rows, Hq, Hkv, hd, max_pages, sm_count,
+// kv_len_hint): partials of cut groups, and with `weight` the rows' sums and perhaps their scores.
 long long kv8_attention_workspace(const Kv8AttnParams& p, bool weight);
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t st);
 

@@ -413,6 +413,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
               }
             }
           }
+          if (NT == 1 && p.scores) {  // for the tokens' weights
+            float* to = p.scores + (((long long)b * p.Hkv + kvh) * p.max_pages * 2 + u) * (p.W * grp * kUnit) + k * kSub + g;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (2 * c + e < rows) __stcs(to + (2 * c + e) * kUnit, x[e]), __stcs(to + (2 * c + e) * kUnit + 8, x[2 + e]);
+          }
           over |= fmaxf(x[0], x[2]) + eb > top[nt][0] + kSlack || fmaxf(x[1], x[3]) + eb > top[nt][1] + kSlack;
         }
       }
@@ -763,6 +769,39 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_kernel(const __g
   }
 }
 
+// The same from the scores that the attention left (few rows): a lane per token.
+__global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_scores_kernel(const __grid_constant__ Kv8AttnParams p) {
+  __shared__ float s_lse[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, kvh = blockIdx.y, grp = p.Hq / p.Hkv;
+  pdl_wait();
+  pdl_launch_dependents();
+  const Seq seq = seq_of(p, b);
+  const int rows = seq.Wb * grp;
+  const int units = (int)min((long long)seq.units, (p.weight_len + kUnit - 1) / kUnit);
+  if ((int)blockIdx.x * kWeightWarps >= units) return;
+  if (threadIdx.x < 8)
+    s_lse[threadIdx.x] = threadIdx.x < rows ? p.lse[(long long)(seq.row0 + threadIdx.x / grp) * p.Hq + kvh * grp + threadIdx.x % grp]
+                                            : INFINITY;
+  __syncthreads();
+  float* const weight = p.weight + ((long long)b * p.Hkv + kvh) * p.weight_len;
+  const float* const scores = p.scores + ((long long)b * p.Hkv + kvh) * p.max_pages * 2 * (p.W * grp * kUnit);
+#pragma unroll 2
+  for (int u = blockIdx.x * kWeightWarps + warp; u < units; u += gridDim.x * kWeightWarps) {
+    const int pg = p.page_table[(long long)b * p.max_pages + (u >> 1)];
+    const int t = u * kUnit + lane;
+    if (pg < 0 || pg >= p.num_pages || t >= seq.n_keys || t >= p.weight_len) continue;
+    const float* x = scores + (long long)u * (p.W * grp * kUnit) + lane;
+    float s[8], w = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s[r] = r < rows ? __ldcs(x + r * kUnit) : 0.f;
+    const float was = weight[t];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) w += ex2(s[r] - s_lse[r]);
+    weight[t] = was + w;
+  }
+}
+
 // Function attributes are per device: one bit per device once they are set there.
 template <typename K>
 cudaError_t configure(K kernel, int smem, std::atomic<uint64_t>& done) {
@@ -820,13 +859,15 @@ cudaError_t launch_nt(Kv8AttnParams p, cudaStream_t st) {
                   p, NT * 8, blocks);
 }
 
+// Four CTAs per SM where there is that much work.
+dim3 weight_grid(const Kv8AttnParams& p) {
+  const long long groups = (long long)p.B * p.Hkv, units = (p.kv_len_hint + kUnit - 1) / kUnit;
+  const long long per = std::max<long long>(1, 4ll * p.sm_count / groups);  // CTAs of a group
+  return dim3((unsigned)std::max<long long>(1, std::min(per, (units + kWeightWarps - 1) / kWeightWarps)), p.Hkv, p.B);
+}
 template <int HD, int NT>
 cudaError_t launch_weight(const Kv8AttnParams& p, cudaStream_t st) {
-  const long long groups = (long long)p.B * p.Hkv;
-  const long long units = (p.kv_len_hint + kUnit - 1) / kUnit;
-  const long long per = std::max<long long>(1, 4ll * p.sm_count / groups);  // CTAs of a group
-  const long long x = std::max<long long>(1, std::min(per, (units + kWeightWarps - 1) / kWeightWarps));
-  return launch_k(kv8_weight_kernel<HD, NT>, dim3((unsigned)x, p.Hkv, p.B), dim3(kWeightWarps * 32), 0, st, p);
+  return launch_k(kv8_weight_kernel<HD, NT>, weight_grid(p), dim3(kWeightWarps * 32), 0, st, p);
 }
 
 template <int HD>
@@ -840,6 +881,10 @@ cudaError_t launch_hd(const Kv8AttnParams& p, cudaStream_t st) {
     case 4: e = launch_nt<HD, 4>(p, st); break;
   }
   if (e != cudaSuccess || !p.weight) return e;
+  if (p.scores) {
+    const dim3 grid = weight_grid(p);
+    return launch_k(kv8_weight_scores_kernel, grid, dim3(kWeightWarps * 32), 0, st, p);
+  }
   const int tiles = (rows + 7) / 8;
   return tiles == 1 ? launch_weight<HD, 1>(p, st) : tiles == 2 ? launch_weight<HD, 2>(p, st)
        : tiles <= 4 ? launch_weight<HD, 4>(p, st) : launch_weight<HD, 8>(p, st);
@@ -852,15 +897,27 @@ long long partial_floats(const Kv8AttnParams& p) {
   return 2ll * (kMaxCtas * p.sm_count) * row_tiles(rows) * 8 * row_blocks(rows) * (p.hd + 2);
 }
 
+// Floats of the scores that are kept for the tokens' weights, or 0: they are worked out again.  Up
+// to 8 rows they are a quarter of K's bytes; writing and reading them takes 62 us where K once more
+// takes 85 (8 x 16384 tokens, 8 kv heads of 128, one row of 4 query heads).  Room for every page
+// of the table: up to 256 MB.
+long long score_floats(const Kv8AttnParams& p) {
+  const long long rows = p.W * (p.Hq / p.Hkv), n = (long long)p.B * p.Hkv * p.max_pages * kPage * rows;
+  return rows <= 8 && n <= (64ll << 20) ? n : 0;
+}
+
 }  // namespace
 
 long long kv8_attention_workspace(const Kv8AttnParams& p, bool weight) {
-  return 4 * (partial_floats(p) + (weight ? (long long)p.total_rows * p.Hq : 0));
+  return 4 * (partial_floats(p) + (weight ? (long long)p.total_rows * p.Hq + score_floats(p) : 0));
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnParams& params, cudaStream_t st) {
   Kv8AttnParams p = params;
-  p.lse = p.weight ? p.workspace + partial_floats(p) : nullptr;
+  if (p.weight) {
+    p.lse = p.workspace + partial_floats(p);
+    if (score_floats(p) > 0) p.scores = p.lse + (long long)p.total_rows * p.Hq;
+  }
   return p.hd == 128 ? launch_hd<128>(p, st) : launch_hd<64>(p, st);
 }
 
