@@ -616,6 +616,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // first nk, to the token and the row's distribution.  counted: sh.tau is top_p's target
   // already.
   auto finish = [&](int M, int nk, bool counted) {
+    if (nk < M && M > 128) {
+      // every CTA's first top_k are there: down to the bin of the row's k-th first, which leaves
+      // fewer to sort (64 rows of 128256 tokens, top_k 50: 38.0 us without, 33.9 with)
+      unsigned long long k[2] = {tid < M ? sh.key[tid] : 0ull, tid + kThreads < M ? sh.key[tid + kThreads] : 0ull};
+      const unsigned most = __reduce_max_sync(0xffffffffu, max((unsigned)(k[0] >> 32), (unsigned)(k[1] >> 32)));
+      if (lane == 0) sh.warp[warp] = most;
+      sh.h.cnt[tid] = 0;
+      __syncthreads();
+      R.mx = key_logit(__reduce_max_sync(0xffffffffu, lane < kWarps ? (unsigned)sh.warp[lane] : 0u));
+      int bin[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        bin[i] = k[i] ? R.bin_of(key_logit((uint32_t)(k[i] >> 32))) : kBins;
+        if (k[i]) atomicAdd(&sh.h.cnt[bin[i]], 1u);
+      }
+      if (tid == 0) sh.picked = 0;
+      __syncthreads();
+      const unsigned here = sh.h.cnt[tid];
+      const unsigned long long above = block_before64(here, sh.warp);
+      if (above < (unsigned long long)nk && (unsigned long long)nk <= above + here) sh.pick = tid;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (bin[i] <= sh.pick) sh.key[atomicAdd(&sh.picked, 1u)] = k[i];
+      __syncthreads();
+      M = (int)sh.picked;
+      __syncthreads();
+    }
     unsigned long long* const mass = reinterpret_cast<unsigned long long*>(&sh.h);  // by rank; the bins are done with
     static_assert(sizeof(Bins) >= kCand * sizeof(unsigned long long), "masses of candidates");
     const Two k = sorted_keys(sh.key, M);

@@ -311,10 +311,35 @@ def test_many_sequences(spec):
     run_attention(spec, c, lens, rows, 4, width=3, qpad=8, weight_len=100)     # weights of the first 100 positions alone
 
 
-def test_windows_before_zero_past_the_table_and_absent_pages(spec):
+@pytest.mark.parametrize("grp", [1, 4])
+def test_windows_before_zero_past_the_table_and_absent_pages(spec, grp):
     lens, rows = [-3, 126, 60, 0], [5, 5, 4, 2]
     c = filled(spec, lens, rows, 1, 64, 2, absent=[(2, 0), (3, 0)])
-    run_attention(spec, c, lens, rows, 4, weight_len=128)
+    run_attention(spec, c, lens, rows, grp, weight_len=128)
+
+
+def test_pool_past_4_gb(spec):
+    """The cells of the last pages of a pool whose byte offsets pass 32 bits."""
+    H, hd, n = 8, 128, 33000
+    pool = spec.spec_kv8_pool(n, H, hd)
+    assert pool.numel() > 2 ** 32
+    c = Cache(spec, 1, H, hd, 3, spare=2)
+    c.table = torch.tensor([[n - 1, 3, n - 2]], dtype=torch.int32, device="cuda")
+    pool[[n - 1, 3, n - 2]] = 255
+    c.pool, c.here[:], c.spare = pool, True, np.array([n - 3, n - 4])
+    c.write([0], [c.values(170)], [c.values(170)])
+    c.check_read([0], [170], "fp16")
+    run_attention(spec, c, [168], [2], 2, weight_len=170)
+    w = torch.rand(1, H, 170, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    dst = i32([[n - 3, n - 4]])
+    _, kept, _ = spec.spec_kv8_evict(pool, w, i32([170]), c.table, dst, 100, 10)
+    k, _ = spec.spec_kv8_read(pool, i32([0]), dst, 100)
+    hk, _ = c.held(0, 170)
+    for h in range(H):
+        stay = O.keep_tokens(w[0, h].cpu().numpy(), 170, 100, 10)
+        assert kept[0, h].tolist() == stay.tolist()
+        assert np.array_equal(k[0, :, h].double().cpu().numpy(), rounded(O.held(hk[stay, h]), "fp16"))
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 3.0])
