@@ -704,8 +704,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const unsigned long long above = block_before64(here, sh.warp);
     if (above < (unsigned long long)K && (unsigned long long)K <= above + here) sh.pick = tid;
     __syncthreads();
-    const float least_l = fmaxf(key_logit(first_key(sh.pick)), -3.402823466e38f);
-    give(mx == INFINITY ? kCand + 1 : send(least_l, [](int, float) { return true; }));
+    const float least_l = mx == INFINITY ? INFINITY : fmaxf(key_logit(first_key(sh.pick)), -3.402823466e38f);
+    const unsigned mine = send(least_l, [](int, float) { return true; });  // by all CTAs: they take turns with cand[]
+    give(mx == INFINITY ? kCand + 1 : mine);
     zero_probs();
     cluster.sync();
     const unsigned long long M = sum_given();

@@ -132,6 +132,19 @@ def test_not_a_number_and_infinities(spec):
     assert tok[4] == 7 and tok[6] == 4321
 
 
+@pytest.mark.parametrize("rows,V", [(1, 128256), (3, 50257)])
+def test_infinities_of_one_slice(spec, rows, V):
+    """+infinity in one CTA's slice of a row, the first one's among them, with a small top_k."""
+    x, u = logits_of(rows, V, "fp32", 12)
+    for at in ([0], [7, 11], [V // 2], [V // 3, V // 3 + 1], [V - 1]):
+        y = x.clone()
+        y[:, at] = float("inf")
+        for k in (1, 2, 5):
+            tok, q = check(spec, y, u, 1.0, k=k)
+            assert all(int(t) in at for t in tok)
+            check(spec, y, u, 0.7, k=k, p=0.9)
+
+
 def test_greedy(spec):
     x, u = logits_of(6, 20011, "bf16", 3)
     tok, q = check(spec, x, u, 0.0, k=5, p=0.5)
