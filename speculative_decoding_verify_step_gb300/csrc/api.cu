@@ -1759,8 +1759,7 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
   p.kv_len_hint = kv4_len_hint(max_pages, max_kv_len, W);
   p.weight = weight;
   p.weight_len = weight_len;
-  p.sm_count = 1 << 20;
-  if (kv8_attention_workspace(p, weight != nullptr) > 0)  // needed on any GPU
+  if (kv8_attention_needs_workspace(p, weight != nullptr))  // on any GPU
     if (spec_status s = kv4_check_ptr(workspace, "workspace")) return s;
   CUDA_TRY(current_sm_count(&p.sm_count));
   const long long need = kv8_attention_workspace(p, weight != nullptr);

@@ -52,6 +52,8 @@ struct Kv8AttnParams {
 // Bytes of workspace of a call of p's shape (B, W, total_rows, Hq, Hkv, hd, max_pages, sm_count,
 // kv_len_hint): partials of cut groups, and with `weight` the rows' sums and perhaps their scores.
 long long kv8_attention_workspace(const Kv8AttnParams& p, bool weight);
+// Whether that is more than none whatever the GPU.
+bool kv8_attention_needs_workspace(const Kv8AttnParams& p, bool weight);
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t st);
 
 struct Kv8EvictParams {

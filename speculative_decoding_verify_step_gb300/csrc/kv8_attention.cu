@@ -47,6 +47,7 @@ constexpr int kUnit = 32;             // tokens of a unit
 constexpr int kMinUnits = 4;          // of a piece: one for each warp
 constexpr int kMaxCtas = 3;           // per SM, of any variant
 constexpr int kMaxCluster = 8;
+constexpr int kClusterUnits = 40;     // of a cluster's CTA, at most
 constexpr float kNoMax = -1e30f;      // running maximum of a row that has seen no token
 constexpr float kSlack = 6.f;         // how far score + b may pass the running maximum
 
@@ -829,7 +830,7 @@ int cluster_size(int B, int Hkv, int rows, int len_hint, int sm_count) {
   const long long groups = (long long)B * Hkv * row_blocks(rows), units = (len_hint + kUnit - 1) / kUnit;
   int cs = 1;
   while (cs < kMaxCluster && cs * kMinUnits < units && groups * cs * 2 <= 2 * sm_count) cs *= 2;
-  return units <= (groups * cs > sm_count ? 40 : 20) * cs && groups <= (1 << 27) ? cs : 0;
+  return units <= (groups * cs > sm_count ? kClusterUnits : kClusterUnits / 2) * cs && groups <= (1 << 27) ? cs : 0;
 }
 
 template <int HD, int NT>
@@ -910,6 +911,10 @@ long long score_floats(const Kv8AttnParams& p) {
 
 long long kv8_attention_workspace(const Kv8AttnParams& p, bool weight) {
   return 4 * (partial_floats(p) + (weight ? (long long)p.total_rows * p.Hq + score_floats(p) : 0));
+}
+
+bool kv8_attention_needs_workspace(const Kv8AttnParams& p, bool weight) {
+  return weight || (p.kv_len_hint + kUnit - 1) / kUnit > kMaxCluster * kClusterUnits;
 }
 
 cudaError_t launch_kv8_attention(const Kv8AttnParams& params, cudaStream_t st) {

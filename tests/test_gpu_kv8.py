@@ -296,6 +296,15 @@ def test_long_caches_are_cut_and_merged(spec, W, grp):
         assert torch.equal(x, y)                            # one order of the sums
 
 
+@pytest.mark.parametrize("B,H,pages", [(3, 8, 150), (5, 4, 83), (19, 2, 158), (1, 24, 100)])
+def test_clusters_of_middling_lengths_need_no_workspace(spec, B, H, pages):
+    """20 to 38 groups of 5 to 10 thousand tokens: one cluster each on some GPUs, pieces on others."""
+    lens, rows = [pages * 64 - 1] + [300 * b + 5 for b in range(1, B)], [1] * B
+    c = filled(spec, lens, rows, H, 64, pages, seed=B)
+    run_attention(spec, c, lens, rows, 2)
+    run_attention(spec, c, lens, rows, 1, weight_len=pages * 64)
+
+
 def test_longest_cache(spec):
     lens, rows = [65520], [3]
     c = filled(spec, lens, rows, 1, 64, 1024)
