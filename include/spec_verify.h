@@ -444,7 +444,7 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
  * weight (may be NULL): device [B, n_kv_heads, weight_len] fp32; weight[b, h, t] grows by
  * the attention weights that the rows of sequence b's window give token t (positions below
  * weight_len), summed over the window's rows and the query heads of kv head h: what
- * spec_kv8_evict ranks by.  workspace: spec_kv8_attention_workspace() bytes for the same
+ * spec_kv8_evict ranks by; out must not overlap q then.  workspace: spec_kv8_attention_workspace() bytes for the same
  * arguments (0: none needed; -1: a shape the call refuses), as there. */
 int64_t spec_kv8_attention_workspace(int32_t B, int32_t W, int32_t total_rows, int32_t n_heads, int32_t n_kv_heads,
                                      int32_t head_dim, int32_t max_pages, int32_t max_kv_len, int32_t with_weight);
@@ -460,7 +460,8 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
  * and of the others those of the largest weight[b, h, .] (equal ones: the earlier token; NaN
  * counts as the smallest).  Outputs: new_len [B] = m; kept [B, n_kv_heads, keep] = their
  * positions, rising, -1 behind the last; weight_out [B, n_kv_heads, weight_out_len] = their
- * weights, zeros behind (weight_out_len >= keep); and their K and V in cells 0..m-1 of
+ * weights, zeros behind (weight_out_len >= keep; neither it nor new_len may overlap its
+ * input); and their K and V in cells 0..m-1 of
  * dst_table [B, dst_pages] (64 * dst_pages >= keep), as if the held values were written
  * there in one call.  The pages of dst_table are pages of the same pool, named once, that
  * page_table does not name in this call (a page shared with another sequence stays as it is;

@@ -1635,6 +1635,12 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
 }  // extern "C"
 
 // ------------------------------------------------------------ 8-bit paged KV cache
+namespace {
+bool overlap(const void* a, long long a_bytes, const void* b, long long b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+}  // namespace
 extern "C" {
 
 int64_t spec_kv8_block_bytes(int32_t head_dim) {
@@ -1737,6 +1743,10 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
   if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
   if (reinterpret_cast<uintptr_t>(weight) & 3u) return fail(SPEC_ERR_INVALID_ARG, "weight must be 4-byte aligned");
   if (spec_status s = kv4_check_stride(q_stride, (long long)n_heads * head_dim, "q_stride")) return s;
+  // the weights may need q again, after out
+  if (weight && overlap(q, ((total_rows - 1) * q_stride + (long long)n_heads * head_dim) * 2, out,
+                        (long long)total_rows * n_heads * head_dim * 2))
+    return fail(SPEC_ERR_INVALID_ARG, "out overlaps q, in a call with weight");
   Kv8AttnParams p{};
   p.q = q;
   p.q_row_stride = q_stride;
@@ -1792,8 +1802,9 @@ spec_status spec_kv8_evict(int32_t B, const int32_t* kv_len, const int32_t* page
   if ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(weight_out)) & 3u)
     return fail(SPEC_ERR_INVALID_ARG, "weight and weight_out must be 4-byte aligned");
   const long long groups = (long long)B * n_kv_heads;
-  if (weight < weight_out + groups * weight_out_len && weight_out < weight + groups * weight_len)
+  if (overlap(weight, groups * weight_len * 4, weight_out, groups * weight_out_len * 4))
     return fail(SPEC_ERR_INVALID_ARG, "weight_out overlaps weight");
+  if (overlap(kv_len, 4ll * B, new_len, 4ll * B)) return fail(SPEC_ERR_INVALID_ARG, "new_len overlaps kv_len");
   Kv8EvictParams p{};
   p.pool = static_cast<uint8_t*>(pool);
   p.kv_len = kv_len;

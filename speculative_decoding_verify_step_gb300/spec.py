@@ -703,7 +703,8 @@ def spec_kv8_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
                        out: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Attention of verify windows over the 8-bit cache: spec_kv4_attention's arguments and
     rules.  weight [B, n_kv_heads, tokens] fp32: grows by the attention weight that each token
-    gets, summed over the window's rows and the query heads of a kv head (for spec_kv8_evict)."""
+    gets, summed over the window's rows and the query heads of a kv head (for spec_kv8_evict); out
+    must not be q then."""
     lib = _lib or load_library()
     P, H, hd, B, width = _kv8_geometry(pool, kv_len, page_table, row_off)
     dev, ragged = pool.device, row_off is not None
@@ -747,7 +748,7 @@ def spec_kv8_evict(pool: torch.Tensor, weight: torch.Tensor, kv_len: torch.Tenso
     move, in order, to the pages of dst_table (pages of the same pool that page_table does not
     name).  Returns (new_len [B], kept positions [B, n_kv_heads, keep] with -1 behind the last,
     their weights with zeros behind, as many tokens as weight has or `keep`); `outs`:
-    preallocated."""
+    preallocated, not kv_len or weight themselves."""
     lib = _lib or load_library()
     P, H, hd, B, width = _kv8_geometry(pool, kv_len, page_table, None)
     dev, keep, recent = pool.device, int(keep), int(recent)

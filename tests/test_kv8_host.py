@@ -85,7 +85,7 @@ def _attend(spec, **kw):
 
 def _evict(spec, **kw):
     a = dict(B=2, start=4096, table=4096, max_pages=4, dst=4096, dst_pages=2, num_pages=8, H=2, hd=64, keep=100, recent=10,
-             weight=1 << 20, T=256, pool=4096, new_len=4096, kept=4096, wout=1 << 30, To=256)
+             weight=1 << 20, T=256, pool=4096, new_len=1 << 16, kept=4096, wout=1 << 30, To=256)
     a.update(kw)
     return spec._lib.spec_kv8_evict(a["B"], a["start"], a["table"], a["max_pages"], a["dst"], a["dst_pages"], a["num_pages"],
                                     a["H"], a["hd"], a["keep"], a["recent"], a["weight"], a["T"], a["pool"], a["new_len"],
@@ -119,6 +119,19 @@ def test_evict_common_refusals(spec, kw, status):
     dict(wout=(1 << 20) + 2 * 2 * 256 * 4 - 4)])
 def test_evict_refusals(spec, kw):
     assert _evict(spec, **kw) == 1
+
+
+@pytest.mark.parametrize("at", [4096, 4100, 4092])
+def test_evict_new_len_is_not_kv_len(spec, at):
+    assert _evict(spec, new_len=at) == 1
+    assert b"new_len overlaps kv_len" in spec._lib.spec_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(out=4096 + 6 * 512 - 16), dict(q=4096 + 6 * 512 - 16),
+                                dict(qs=512, out=4096 + 5 * 1024 + 496)])
+def test_attention_with_weights_is_not_in_place(spec, kw):
+    assert _attend(spec, weight=1 << 20, T=64, **kw) == 1
+    assert b"out overlaps q" in spec._lib.spec_last_error()
 
 
 @pytest.mark.parametrize("kw", [dict(k=None), dict(v=None), dict(k=4104), dict(v=4098), dict(ks=120), dict(vs=120),
