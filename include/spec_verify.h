@@ -488,7 +488,7 @@ spec_status spec_kv8_evict(int32_t B, const int32_t* kv_len, const int32_t* page
  * fp32, R_v / Z of kept tokens, else 0.  temperature 0: the first of the largest logits;
  * u is not read.  A NaN logit counts as -infinity; several +infinity share the mass.  A
  * row without a logit above -infinity, or whose setting or u is out of range
- * (temperature below 0, in (0, 1e-6), infinite or NaN; top_k < 0; top_p outside (0, 1];
+ * (temperature not 0 and outside 1e-6..1e30; top_k < 0; top_p outside (0, 1];
  * min_p outside [0, 1]; u outside [0, 1)), gets token -1 and a row of zeros.
  * No call allocates or keeps state.  V <= 393216, rows <= 2^24.  u may be NULL where
  * temperature is NULL and temperature_all 0. */

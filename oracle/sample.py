@@ -26,7 +26,7 @@ def masses(l, temperature):
 
 
 def valid(u, temperature, top_k=0, top_p=1.0, min_p=0.0):
-    t_ok = temperature == 0 or (np.float32(1e-6) <= temperature < np.inf)
+    t_ok = temperature == 0 or (np.float32(1e-6) <= temperature <= np.float32(1e30))
     return bool(t_ok and top_k >= 0 and 0 < top_p <= 1 and 0 <= min_p <= 1 and (temperature == 0 or 0 <= u < 1))
 
 

@@ -1839,8 +1839,8 @@ spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dty
     return fail(SPEC_ERR_INVALID_ARG, "dtype must be SPEC_F16, SPEC_BF16 or SPEC_F32");
   if (row_stride < V) return fail(SPEC_ERR_INVALID_ARG, "row_stride=%lld is below V=%d", (long long)row_stride, V);
   if (rows_per_setting < 1) return fail(SPEC_ERR_INVALID_ARG, "rows_per_setting must be at least 1");
-  if (!temperature && !(temperature_all == 0.f || (temperature_all >= 1e-6f && std::isfinite(temperature_all))))
-    return fail(SPEC_ERR_INVALID_ARG, "temperature must be 0 or a finite number from 1e-6 on");
+  if (!temperature && !sample_temperature_ok(temperature_all))
+    return fail(SPEC_ERR_INVALID_ARG, "temperature must be 0 or in 1e-6..1e30");
   if (rows == 0) return SPEC_OK;
   if (!logits || !tokens) return fail(SPEC_ERR_INVALID_ARG, "NULL argument");
   if (!u && (temperature || temperature_all != 0.f)) return fail(SPEC_ERR_INVALID_ARG, "sampling needs uniforms u");

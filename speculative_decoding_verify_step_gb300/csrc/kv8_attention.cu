@@ -27,6 +27,11 @@
 // of a cut group by a second kernel.  Short caches need neither the common target nor the
 // second kernel: the CTAs of a group are one thread-block cluster, and each finishes a share
 // of the rows from all partials, through distributed shared memory.
+//
+// What bounds it (8 kv heads of 128 with 4 query heads).  Two tiles of query rows: the cache's bytes,
+// 8 x 32768 tokens at width 4 in 93 us, 0.85 of the copy rate (a decode step of the same 86, 0.91).  Three
+// and four: latencies, since 242 registers leave two warps per SM quarter: 64 x 512..2048 at
+// width 5 in 63 us, 0.41.  Short caches: one chain of latencies, 1 x 1024 tokens in 6.5 us.
 #include <math.h>
 
 #include <algorithm>
@@ -118,7 +123,8 @@ SPEC_DEVICE_INLINE int pieces_of(int units, int target) { return (units + target
 
 // Units of a piece, at most.  Pieces number at most groups + units / target: with few groups
 // as many as there are slots (CTAs that the GPU holds at once), with many up to half again
-// as many.
+// as many.  With 1.5 times the slots always, 32 x 512..8192 tokens at width 4 took 62 us instead of 74,
+// but 8 x 32768 103 instead of 93 and 64 x 512..2048 at width 5 75 instead of 63.
 SPEC_DEVICE_INLINE int target_of(const Kv8AttnParams& p, const Seq& mine) {
   const int lane = threadIdx.x & 31;
   unsigned n = mine.units;

@@ -21,6 +21,7 @@ struct SampleParams {
   float* probs;              // [rows, V] or null
   int sm_count;              // launch shape only
 };
+bool sample_temperature_ok(float t);
 int sample_max_vocab();
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st);
 

@@ -800,7 +800,7 @@ def spec_sample(logits: torch.Tensor, u: Optional[torch.Tensor] = None, temperat
     uniforms u [...] in [0, 1), and with return_probs the distribution q it was drawn from: a
     drafter's x and q of spec_verify_step.  temperature (0: the largest logit; u may be None),
     top_k, top_p, min_p: a number for all rows, or one for each rows_per_setting rows (None:
-    off).  Returns (tokens int32 [...], probs fp32 [..., V] or None); a row without a logit
+    off); lists are copied from the host, so a call inside a graph capture takes tensors.  Returns (tokens int32 [...], probs fp32 [..., V] or None); a row without a logit
     above -infinity, or with a setting or u out of range, gives -1 and zeros.  `outs`:
     preallocated (tokens, probs or None)."""
     lib = _lib or load_library()

@@ -167,6 +167,15 @@ def test_settings_out_of_range(spec):
     assert (tok[1:] == -1).all() and (q[1:] == 0).all() and tok[0] >= 0
 
 
+def test_temperatures_at_their_ends(spec):
+    x, u = logits_of(6, 3000, "fp32", 5)
+    x[1:3] *= 1e30
+    x[3:] *= 1e-6
+    check(spec, x, u, [1e-6, 1e30, 3e30, 1e-6, 2e-6, 1e-4], p=0.9)
+    check(spec, x, u, 1e30)
+    check(spec, x, u, 1e-6, k=7)
+
+
 def test_uniforms_at_their_ends(spec):
     x, _ = logits_of(4, 9000, "fp32", 8)
     x[:, 0] = x[:, -1] = x.max() + 1                      # so that neither end is a decision near another

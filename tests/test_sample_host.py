@@ -62,7 +62,7 @@ def _call(spec, **kw):
 
 @pytest.mark.parametrize("kw", [
     dict(rows=-1), dict(rows=(1 << 24) + 1), dict(V=0), dict(V=393217, stride=393217), dict(dtype=3), dict(dtype=-1),
-    dict(stride=99), dict(per=0), dict(t_all=-1.0), dict(t_all=float("nan")), dict(t_all=float("inf")), dict(t_all=1e-7),
+    dict(stride=99), dict(per=0), dict(t_all=-1.0), dict(t_all=float("nan")), dict(t_all=float("inf")), dict(t_all=1e-7), dict(t_all=1.1e30),
     dict(logits=None), dict(tokens=None), dict(u=None), dict(u=None, t_all=0.0, t=4096), dict(logits=4098),
     dict(logits=4097, dtype=1)])
 def test_refusals(spec, kw):
