@@ -65,6 +65,7 @@ constexpr float kBinsPerUnit = 16.f;     // bins of x in the first histogram
 constexpr int kBatch = 4;                // tokens of a thread under way at once
 constexpr int kCand = 1024;              // candidates that one CTA sorts
 constexpr int kCandK = kCand / 2;        // largest top_k that is tried so
+constexpr int kFew = kThreads / 4;       // candidates that are ranked by comparing each with each
 
 // Temperatures for which log2(e) / T is a pair of normal floats, and T's steps are fp32's.
 constexpr float kMinTemp = 1e-6f, kMaxTemp = 1e30f;
@@ -246,6 +247,31 @@ __device__ __noinline__ Two sorted_keys(unsigned long long* key, int M) {
   return Two{x0, x1};
 }
 
+// Among M <= kFew keys with measures m, four threads to one key x: how many are larger, their
+// measures' sum, and that of all.  (Sorting 64 keys takes 2.5 K cycles, this 0.5 K.)
+struct Ranked {
+  unsigned long long before, total;
+  int above;
+};
+__device__ __noinline__ Ranked ranked(const unsigned long long* key, const unsigned long long* m, int M, unsigned long long x) {
+  Ranked r{0ull, 0ull, 0};
+#pragma unroll 4
+  for (int j = threadIdx.x & 3; j < M; j += 4) {
+    const unsigned long long v = m[j];
+    const bool more = key[j] > x;
+    r.total += v;
+    r.before += more ? v : 0ull;
+    r.above += more;
+  }
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    r.total += __shfl_xor_sync(0xffffffffu, r.total, o);
+    r.before += __shfl_xor_sync(0xffffffffu, r.before, o);
+    r.above += __shfl_xor_sync(0xffffffffu, r.above, o);
+  }
+  return r;
+}
+
 // What is kept: logits above the threshold, and of those equal to it the tokens up to cut.
 struct Kept {
   float t;
@@ -327,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       }
   }
 
-  // f(i, logit of i) for the slice's tokens from least_l on, read in 16-byte pieces.
-  const auto each_from = [&](float least_l, auto f) {
+  // f(i, logit of i) for the slice's tokens from least_l to most_l, read in 16-byte pieces.
+  const auto each_in = [&](float least_l, float most_l, auto f) {
     const auto one = [&](int i, unsigned hits) {  // tokens i + the places of the bits of hits
 #pragma unroll 1
       for (; hits; hits &= hits - 1) {
@@ -338,14 +364,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     };
     // what lies around the pieces: the first threads before, the last ones behind them
     const int i = tid < kThreads / 2 ? tid : tail0 + (kThreads - 1 - tid);
-    one(i, (tid < head || (tid >= kThreads / 2 && i < n)) && logit(i) >= least_l ? 1u : 0u);
+    one(i, (tid < head || (tid >= kThreads / 2 && i < n)) && logit(i) >= least_l && logit(i) <= most_l ? 1u : 0u);
 #pragma unroll 1
     for (int j = tid; j < vecs; j += kThreads) {
       const uint4 w = reinterpret_cast<const uint4*>(val + head)[j];
       const T* e = reinterpret_cast<const T*>(&w);
       unsigned m = 0;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) m |= to_f32(e[k]) >= least_l ? 1u << k : 0u;
+      for (int k = 0; k < PER; ++k) {
+        const float l = fmaxf(to_f32(e[k]), -INFINITY);
+        m |= l >= least_l && l <= most_l ? 1u << k : 0u;
+      }
       one(head + j * PER, m);
     }
   };
@@ -493,18 +522,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     hi = b > 0 ? first_key(b - 1) - 1u : order_key(R.mx);
   };
 
+  // Below every logit of the bins up to b, and above every one of the bins from b on: the bins'
+  // bounds, by more than bin_of's roundings.
+  auto bin_floor = [&](int b) {
+    const float d = (float)(b + 1) / R.bin;
+    return b < kBins - 1 ? R.mx - d - (fabsf(R.mx) + d) * 0x1p-20f : -INFINITY;
+  };
+  auto bin_ceil = [&](int b) {
+    const float d = (float)b / R.bin;
+    return R.mx - d + (fabsf(R.mx) + d) * 0x1p-20f;
+  };
+
   Shared* const first = cluster.map_shared_rank(&sh, 0);
-  // The keys of this CTA's tokens from least_l on that `is` picks (order of the logit, then the
+  // The keys of this CTA's tokens from least_l to most_l that `is` picks (order of the logit, then the
   // lower index first) into the first CTA's list, in any order, as far as it and this CTA's own list, in the
   // bins' place, go; how many there were.
   unsigned long long* const local = reinterpret_cast<unsigned long long*>(&sh.h);
   static_assert(sizeof(Bins) >= kCand * sizeof(unsigned long long), "lists in the bins' place");
   int sent = 0;
-  auto send = [&](float least_l, auto is) {
+  auto send = [&](float least_l, float most_l, auto is) {
     __syncthreads();  // the bins have been read
     if (tid == 0) sh.picked = 0, sh.cand[(sent + 1) & 1] = 0;
     __syncthreads();
-    each_from(least_l, [&](int i, float x) {
+    each_in(least_l, most_l, [&](int i, float x) {
       if (is(i, x)) {
         const unsigned at = atomicAdd(&sh.picked, 1u);
         if (at < kCand) local[at] = (unsigned long long)order_key(x) << 32 | (0xffffffffu - (unsigned)(s0 + i));
@@ -522,49 +562,114 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return mine;
   };
   // All CTAs' such tokens: how many there were, and, if at most kCand, all their keys.
-  auto gather = [&](float least_l, auto is) {
-    give(send(least_l, is));
+  auto gather = [&](float least_l, float most_l, auto is) {
+    give(send(least_l, most_l, is));
     cluster.sync();
     return sum_given();
+  };
+  unsigned long long* const mass = reinterpret_cast<unsigned long long*>(&sh.h);  // the first CTA's, in the bins' place
+  static_assert(sizeof(Bins) >= (kCand + 2 * kFew) * sizeof(unsigned long long), "masses of candidates");
+  // The candidate (its key) among the M in the first CTA whose measure, `before` lying ahead of them all,
+  // completes target; to all CTAs' sh.found.
+  auto last_kept = [&](bool by_mass, unsigned long long target, unsigned long long before, int M) {
+    const auto measure = [&](unsigned long long key) {
+      return key == 0ull ? 0ull : by_mass ? R.mass(key_logit((uint32_t)(key >> 32))) : 1ull;
+    };
+    const auto tell = [&](unsigned long long key, unsigned long long b, unsigned long long m) {
+      if (b < target && target <= b + m)
+        for (int r = 0; r < cs; ++r) cluster.map_shared_rank(&sh, r)->found = key;
+    };
+    if (M > kFew) {  // only those of a finer bin
+      const unsigned long long k[2] = {tid < M ? sh.key[tid] : 0ull, tid + kThreads < M ? sh.key[tid + kThreads] : 0ull};
+      const unsigned h0 = (unsigned)(k[0] >> 32), h1 = (unsigned)(k[1] >> 32);
+      const unsigned most = __reduce_max_sync(0xffffffffu, max(h0, h1));
+      const unsigned fell = __reduce_max_sync(0xffffffffu, max(k[0] ? ~h0 : 0u, k[1] ? ~h1 : 0u));
+      if (lane == 0) sh.warp[warp] = (unsigned long long)most << 32 | fell;
+      sh.h.cnt[tid] = sh.h.m0[tid] = sh.h.m1[tid] = sh.h.m2[tid] = 0;
+      if (tid == 0) sh.picked = 0;
+      __syncthreads();
+      const unsigned long long w = lane < kWarps ? sh.warp[lane] : 0ull;
+      const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(w >> 32)), lo = ~__reduce_max_sync(0xffffffffu, (unsigned)w);
+      const int sft = max(0, 32 - __clz(hi - lo) - 9);
+      int bin[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        bin[i] = k[i] ? (int)((hi - (i ? h1 : h0)) >> sft) : -1;
+        if (!k[i]) continue;
+        if (by_mass) {
+          int a, b;
+          R.mass_parts(key_logit(i ? h1 : h0), a, b);
+          const Parts q(a, b);
+          atomicAdd(&sh.h.m0[bin[i]], q.lo);
+          atomicAdd(&sh.h.m1[bin[i]], q.mid);
+          atomicAdd(&sh.h.m2[bin[i]], q.hi);
+        } else {
+          atomicAdd(&sh.h.m0[bin[i]], 1u);
+        }
+      }
+      __syncthreads();
+      const unsigned long long here = joined(sh.h.m0[tid], sh.h.m1[tid], sh.h.m2[tid]);
+      const unsigned long long ahead = before + block_before64(here, sh.warp);
+      if (ahead < target && target <= ahead + here) sh.pick = tid, sh.found = ahead;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (bin[i] == sh.pick) sh.key[atomicAdd(&sh.picked, 1u)] = k[i];
+      before = sh.found;
+      __syncthreads();
+      M = (int)sh.picked;
+    }
+    if (M <= kFew) {
+      const unsigned long long x = tid / 4 < M ? sh.key[tid / 4] : 0ull, m = measure(x);
+      if (tid % 4 == 0 && x) mass[tid / 4] = m;
+      __syncthreads();
+      const Ranked r = ranked(sh.key, mass, M, x);
+      if (tid % 4 == 0) tell(x, before + r.before, m);
+      return;
+    }
+    const Two k = sorted_keys(sh.key, M);
+    const unsigned long long m0 = measure(k.x0), m1 = measure(k.x1);
+    before += block_before64(m0 + m1, sh.warp);
+    tell(k.x0, before, m0);
+    tell(k.x1, before + m0, m1);
   };
   // The shortest prefix (by rank) of the tokens of `in` whose measure reaches target, from the
   // bin of their first histogram that holds its end.
   auto select = [&](bool by_mass, unsigned long long target, const Kept& in, Found f) -> Kept {
-    uint32_t lo, hi;
-    bin_bounds(f.bin, lo, hi);
+    const int coarse = f.bin;
+    uint32_t lo = 0, hi = 0;  // the bin's keys, once they are needed
+    bool known = false;
+    const auto bounds = [&] {
+      if (!known) bin_bounds(coarse, lo, hi);
+      known = true;
+    };
     while (true) {
-      if (f.above + f.size == target) return key_logit(lo) > in.t ? Kept{key_logit(lo), V} : in;  // all of the bin
+      if (f.above + f.size == target) {  // all of the bin
+        bounds();
+        return key_logit(lo) > in.t ? Kept{key_logit(lo), V} : in;
+      }
+      const bool exact = known;
       const uint32_t l = lo, h = hi;
       // by keys: as floats, 0 would lie in a range that ends at -0
       const auto inside = [&](int i, float x) {
         const uint32_t key = order_key(x);
-        return key >= l && key <= h && in.has(x, s0 + i);
+        return (exact ? key >= l && key <= h : R.bin_of(x) == coarse) && in.has(x, s0 + i);
       };
       if (f.count <= kCand) {
-        const unsigned long long M = gather(key_logit(lo), inside);  // (top_p's bins leave out tokens of no mass, which lie inside too)
+        // (top_p's bins leave out tokens of no mass, which lie inside too)
+        const unsigned long long M =
+            gather(exact ? key_logit(l) : bin_floor(coarse), exact ? key_logit(h) : bin_ceil(coarse), inside);
         if (M <= kCand) {
-          if (rank == 0) {
-            unsigned long long x[2], m[2], before;
-            const Two k = sorted_keys(sh.key, (int)M);
-            x[0] = k.x0, x[1] = k.x1;
-            const auto measure = [&](unsigned long long key) {
-              return key == 0ull ? 0ull : by_mass ? R.mass(key_logit((uint32_t)(key >> 32))) : 1ull;
-            };
-            m[0] = measure(x[0]), m[1] = measure(x[1]);
-            before = f.above + block_before64(m[0] + m[1], sh.warp);
-            // the candidate whose measure completes the target is the last one kept
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (before < target && target <= before + m[i])
-                for (int r = 0; r < cs; ++r) cluster.map_shared_rank(&sh, r)->found = x[i];
-              before += m[i];
-            }
-          }
+          if (rank == 0) last_kept(by_mass, target, f.above, (int)M);
           cluster.sync();
           const unsigned long long end = sh.found;
           __syncthreads();
           return Kept{key_logit((uint32_t)(end >> 32)), (int)(0xffffffffu - (uint32_t)end)};
         }
+      }
+      if (!exact) {
+        bounds();
+        continue;
       }
       if (l == h) break;
       const int sft = max(0, 32 - __clz(h - l) - 9);  // (h - l) >> sft < 512
@@ -628,56 +733,79 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // first nk, to the token and the row's distribution.  counted: sh.tau is top_p's target
   // already.
   auto finish = [&](int M, int nk, bool counted) {
-    if (nk < M && M > 128) {
-      // every CTA's first top_k are there: down to the bin of the row's k-th first, which leaves
-      // fewer to sort (64 rows of 128256 tokens, top_k 50: 38.0 us without, 33.9 with)
-      unsigned long long k[2] = {tid < M ? sh.key[tid] : 0ull, tid + kThreads < M ? sh.key[tid + kThreads] : 0ull};
-      const unsigned most = __reduce_max_sync(0xffffffffu, max((unsigned)(k[0] >> 32), (unsigned)(k[1] >> 32)));
-      if (lane == 0) sh.warp[warp] = most;
-      sh.h.cnt[tid] = 0;
-      __syncthreads();
-      R.mx = key_logit(__reduce_max_sync(0xffffffffu, lane < kWarps ? (unsigned)sh.warp[lane] : 0u));
-      int bin[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        bin[i] = k[i] ? R.bin_of(key_logit((uint32_t)(k[i] >> 32))) : kBins;
-        if (k[i]) atomicAdd(&sh.h.cnt[bin[i]], 1u);
-      }
-      if (tid == 0) sh.picked = 0;
-      __syncthreads();
-      const unsigned here = sh.h.cnt[tid];
-      const unsigned long long above = block_before64(here, sh.warp);
-      if (above < (unsigned long long)nk && (unsigned long long)nk <= above + here) sh.pick = tid;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (bin[i] <= sh.pick) sh.key[atomicAdd(&sh.picked, 1u)] = k[i];
-      __syncthreads();
-      M = (int)sh.picked;
-      __syncthreads();
-    }
-    unsigned long long* const mass = reinterpret_cast<unsigned long long*>(&sh.h);  // by rank; the bins are done with
-    static_assert(sizeof(Bins) >= kCand * sizeof(unsigned long long), "masses of candidates");
-    const Two k = sorted_keys(sh.key, M);
-    unsigned long long x0 = k.x0, x1 = k.x1;
-    if (tid == 0) sh.found = x0;
-    __syncthreads();
-    R.mx = key_logit((uint32_t)(sh.found >> 32));
     if (M == 0) {  // no logit above -infinity
       if (tid == 0) p.tokens[row] = -1;
       return;
     }
+    {
+      const unsigned long long k[2] = {tid < M ? sh.key[tid] : 0ull, tid + kThreads < M ? sh.key[tid + kThreads] : 0ull};
+      const unsigned most = __reduce_max_sync(0xffffffffu, max((unsigned)(k[0] >> 32), (unsigned)(k[1] >> 32)));
+      if (lane == 0) sh.warp[warp] = most;
+      sh.h.cnt[tid] = 0;
+      if (tid == 0) sh.picked = 0;
+      __syncthreads();
+      R.mx = key_logit(__reduce_max_sync(0xffffffffu, lane < kWarps ? (unsigned)sh.warp[lane] : 0u));
+      if (nk < M && M > kFew) {
+        // every CTA's first top_k are there: down to the bin of the row's k-th first, which leaves
+        // fewer to rank (64 rows of 128256 tokens, top_k 50: 38.0 us without, 33.9 with)
+        int bin[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          bin[i] = k[i] ? R.bin_of(key_logit((uint32_t)(k[i] >> 32))) : kBins;
+          if (k[i]) atomicAdd(&sh.h.cnt[bin[i]], 1u);
+        }
+        __syncthreads();
+        const unsigned here = sh.h.cnt[tid];
+        const unsigned long long above = block_before64(here, sh.warp);
+        if (above < (unsigned long long)nk && (unsigned long long)nk <= above + here) sh.pick = tid;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (bin[i] <= sh.pick) sh.key[atomicAdd(&sh.picked, 1u)] = k[i];
+        __syncthreads();
+        M = (int)sh.picked;
+      }
+      __syncthreads();
+    }
+    // top_p's target, from the sum of the first nk
+    const auto target = [&](bool last, unsigned long long sum) {
+      if (p_on && !counted) {
+        if (last) sh.found = sum;
+        __syncthreads();
+        set_tau(sh.found);
+      }
+      return p_on ? sh.tau : ~0ull;
+    };
+    if (M <= kFew) {
+      const int i = tid / 4;
+      const bool lead = tid % 4 == 0;
+      const unsigned long long x = i < M ? sh.key[i] : 0ull, m = x ? R.mass(key_logit((uint32_t)(x >> 32))) : 0ull;
+      if (lead && x) mass[i] = m;
+      __syncthreads();
+      const Ranked r = ranked(sh.key, mass, M, x);
+      const unsigned long long tau = target(lead && x && r.above == nk - 1, r.before + m);
+      const bool keep = x && r.above < nk && r.before < tau && m >= least;
+      // now by index (the low halves of the keys fall as it rises)
+      const unsigned long long y = keep ? x << 32 | 1u : 0ull;
+      unsigned long long* const by = mass + kCand;
+      if (lead) by[i] = y, by[kFew + i] = keep ? m : 0ull;
+      __syncthreads();
+      const Ranked q = ranked(by, by + kFew, M, y);
+      const unsigned long long t = draw_target(q.total);
+      const int v = (int)(0xffffffffu - (uint32_t)x);
+      if (lead && keep) {
+        if (q.before <= t && t < q.before + m) p.tokens[row] = v;
+        if (p.probs) p.probs[row * V + v] = kept_share(m, 1.f / (float)q.total);
+      }
+      return;
+    }
+    const Two k = sorted_keys(sh.key, M);
+    unsigned long long x0 = k.x0, x1 = k.x1;
     const int i0 = 2 * tid, i1 = 2 * tid + 1;
     const unsigned long long m0 = x0 ? R.mass(key_logit((uint32_t)(x0 >> 32))) : 0ull;
     const unsigned long long m1 = x1 ? R.mass(key_logit((uint32_t)(x1 >> 32))) : 0ull;
     const unsigned long long b0 = block_before64(m0 + m1, sh.warp), b1 = b0 + m0;
-    if (p_on && !counted) {
-      if (i0 == nk - 1) sh.found = b0 + m0;
-      if (i1 == nk - 1) sh.found = b1 + m1;
-      __syncthreads();
-      set_tau(sh.found);
-    }
-    const unsigned long long tau = p_on ? sh.tau : ~0ull;
+    const unsigned long long tau = target(i0 == nk - 1 || i1 == nk - 1, i0 == nk - 1 ? b0 + m0 : b1 + m1);
     // a rank is kept if it is among the top_k, what lies before it falls short of tau, and its mass suffices
     const bool keep0 = i0 < nk && b0 < tau && m0 >= least, keep1 = i1 < nk && b1 < tau && m1 >= least;
     const int kept_n = __syncthreads_count(keep0) + __syncthreads_count(keep1);
@@ -716,8 +844,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const unsigned long long above = block_before64(here, sh.warp);
     if (above < (unsigned long long)K && (unsigned long long)K <= above + here) sh.pick = tid;
     __syncthreads();
-    const float least_l = mx == INFINITY ? INFINITY : fmaxf(key_logit(first_key(sh.pick)), -3.402823466e38f);
-    const unsigned mine = send(least_l, [](int, float) { return true; });  // by all CTAs: they take turns with cand[]
+    const int bin = sh.pick;
+    const float least_l = mx == INFINITY ? INFINITY : fmaxf(bin_floor(bin), -3.402823466e38f);
+    const unsigned mine =  // by all CTAs: they take turns with cand[]
+        send(least_l, INFINITY, [&](int, float x) { return R.bin_of(x) <= bin; });
     give(mx == INFINITY ? kCand + 1 : mine);
     zero_probs();
     cluster.sync();
@@ -817,7 +947,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     last_bin = min(last_bin, (int)fminf(-logf(MP) * kBinsPerUnit + 1.f, (float)(kBins - 1)));
   if (last_bin < kBins) {
     const Kept in = kept;
-    const unsigned long long M = gather(key_logit(first_key(last_bin)), [&](int i, float x) { return in.has(x, s0 + i); });
+    const unsigned long long M = gather(bin_floor(last_bin), INFINITY, [&](int i, float x) {
+      return R.bin_of(x) <= last_bin && in.has(x, s0 + i);
+    });
     if (M <= kCand) {
       zero_probs();
       cluster.sync();  // the zeros lie before the kept tokens' shares

@@ -132,6 +132,27 @@ def test_not_a_number_and_infinities(spec):
     assert tok[4] == 7 and tok[6] == 4321
 
 
+@pytest.mark.parametrize("dt", ["fp32", "fp16"])
+@pytest.mark.parametrize("none", [float("nan"), -float("inf")])
+def test_top_k_that_ends_among_tokens_without_mass(spec, none, dt):
+    x, u = logits_of(2, 5000, dt, 14)
+    x[0, 4590:4990] = none
+    x[1, torch.randperm(5000, generator=torch.Generator().manual_seed(2))[:700]] = none
+    for k in (4299, 4300, 4301, 4599, 4600, 4601, 4800, 4999):
+        check(spec, x, u, 1.0, k=k)
+        check(spec, x, u, 2.0, k=k, p=0.99)
+
+
+@pytest.mark.parametrize("spread", [0.01, 0.3, 5.0])
+def test_limits_among_neighbours(spec, spread):
+    """Where the limits end in bins of few, of many and of a thousand tokens."""
+    x, u = logits_of(3, 20000, "fp32", 15)
+    x = x.clamp(max=3.0) * spread
+    for kw in (dict(k=40), dict(k=120), dict(k=130), dict(k=300), dict(k=513), dict(k=900), dict(p=0.002), dict(p=0.05), dict(p=0.5),
+               dict(k=200, p=0.3), dict(k=1500, p=0.6), dict(k=60, p=0.9, m=0.3)):
+        check(spec, x, u, 1.0, **kw)
+
+
 @pytest.mark.parametrize("rows,V", [(1, 128256), (3, 50257)])
 def test_infinities_of_one_slice(spec, rows, V):
     """+infinity in one CTA's slice of a row, the first one's among them, with a small top_k."""
