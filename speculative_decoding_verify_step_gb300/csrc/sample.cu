@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   };
   if (tid < head) put(tid);
   if (tid < n - tail0) put(tail0 + tid);
-  constexpr int UN = 4;  // loads in flight
+  constexpr int UN = 4;  // pieces at once
   for (int j0 = tid; j0 < vecs; j0 += UN * kThreads) {
     uint4 w[UN];
 #pragma unroll
@@ -355,28 +355,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
 
   // f(i, logit of i) for the slice's tokens from least_l to most_l, read in 16-byte pieces.
   const auto each_in = [&](float least_l, float most_l, auto f) {
-    const auto one = [&](int i, unsigned hits) {  // tokens i + the places of the bits of hits
+    const auto is = [&](T e) {
+      const float l = fmaxf(to_f32(e), -INFINITY);
+      return l >= least_l && l <= most_l;
+    };
+    // tokens of the pieces j, j + kThreads, ..: a bit each
+    const auto each = [&](int j, unsigned hits) {
 #pragma unroll 1
       for (; hits; hits &= hits - 1) {
-        const int at = i + __ffs(hits) - 1;
+        const int b = __ffs(hits) - 1, at = head + (j + b / PER * kThreads) * PER + b % PER;
         f(at, logit(at));
       }
     };
-    // what lies around the pieces: the first threads before, the last ones behind them
-    const int i = tid < kThreads / 2 ? tid : tail0 + (kThreads - 1 - tid);
-    one(i, (tid < head || (tid >= kThreads / 2 && i < n)) && logit(i) >= least_l && logit(i) <= most_l ? 1u : 0u);
 #pragma unroll 1
-    for (int j = tid; j < vecs; j += kThreads) {
-      const uint4 w = reinterpret_cast<const uint4*>(val + head)[j];
-      const T* e = reinterpret_cast<const T*>(&w);
+    for (int j = tid; j < vecs; j += UN * kThreads) {
       unsigned m = 0;
 #pragma unroll
-      for (int k = 0; k < PER; ++k) {
-        const float l = fmaxf(to_f32(e[k]), -INFINITY);
-        m |= l >= least_l && l <= most_l ? 1u << k : 0u;
-      }
-      one(head + j * PER, m);
+      for (int k = 0; k < UN; ++k)
+        if (j + k * kThreads < vecs) {
+          const uint4 w = reinterpret_cast<const uint4*>(val + head)[j + k * kThreads];
+          const T* e = reinterpret_cast<const T*>(&w);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) m |= is(e[i]) ? 1u << (k * PER + i) : 0u;
+        }
+      each(j, m);
     }
+    // what lies around the pieces: the first threads before, the last ones behind them
+    const int i = tid < kThreads / 2 ? tid : tail0 + (kThreads - 1 - tid);
+    if ((tid < head || (tid >= kThreads / 2 && i < n)) && is(val[i])) f(i, logit(i));
   };
 
   // Exchange number xchg: one 64-bit value of every CTA, read after a cluster barrier.  A
@@ -724,9 +730,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     return (__umul64hi(m24, Z) << 40) | ((m24 * Z) >> 24);
   };
 
-  // tau = ceil(top_p * sum) into sh.tau, by one thread: fp64 is slow here.
+  // tau = ceil(top_p * sum) into sh.tau, of top_p = m 2^-e, 2^23 <= m < 2^24 (fp64 is slow here).
   auto set_tau = [&](unsigned long long sum) {
-    if (tid == 0) sh.tau = max(1ull, (unsigned long long)ceil(__dmul_rn((double)TP, (double)sum)));
+    if (tid == 0) {
+      const unsigned b = __float_as_uint(TP), m = (b & 0x7fffffu) | 0x800000u;
+      const int e = 150 - (int)(b >> 23);  // 24 or more
+      const unsigned long long lo = m * sum, hi = __umul64hi(m, sum);
+      unsigned long long q = 0, rest = 1;  // (a top_p below 2^-39: the largest mass alone reaches it)
+      if (e < 64) q = hi << (64 - e) | lo >> e, rest = lo << (64 - e);
+      sh.tau = q + (rest != 0);
+    }
     __syncthreads();
   };
   // In the first CTA: M <= kCand candidates, all that can be kept, of which top_k leaves the
@@ -823,6 +836,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (keep0) p.probs[row * V + (0xffffffffu - (uint32_t)x0)] = kept_share(m0, inv);
       if (keep1) p.probs[row * V + (0xffffffffu - (uint32_t)x1)] = kept_share(m1, inv);
     }
+    if (kept_n <= kFew) {
+      const unsigned long long y = tid / 4 < kept_n ? sh.key[tid / 4] : 0ull;
+      const Ranked q = ranked(sh.key, mass, kept_n, y);
+      if (tid % 4 == 0 && y && q.before <= t && t < q.before + mass[tid / 4]) p.tokens[row] = (int)(0xffffffffu - (uint32_t)(y >> 32));
+      return;
+    }
     const Two by_index = sorted_keys(sh.key, kept_n);
     x0 = by_index.x0, x1 = by_index.x1;
     const unsigned long long y0 = x0 ? mass[(uint32_t)x0] : 0ull, y1 = x1 ? mass[(uint32_t)x1] : 0ull;
@@ -836,6 +855,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   // before they are sent.  (Tokens at -infinity have no mass and are left out; a row with
   // +infinity goes the long way.)
   if (!bad && temp > 0.f && k_on && 2 * K <= kThreads && K * cs <= kCand * 5 / 8) {
+    zero_probs();  // now, so that the barrier below does not wait for them
     sh.h.cnt[tid] = 0;
     __syncthreads();
     atomicAdd(&sh.h.cnt[R.bin_of(own)], 1u);
@@ -849,7 +869,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     const unsigned mine =  // by all CTAs: they take turns with cand[]
         send(least_l, INFINITY, [&](int, float x) { return R.bin_of(x) <= bin; });
     give(mx == INFINITY ? kCand + 1 : mine);
-    zero_probs();
     cluster.sync();
     const unsigned long long M = sum_given();
     if (M <= kCand) {
