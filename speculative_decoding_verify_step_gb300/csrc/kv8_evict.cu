@@ -71,8 +71,12 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
   const int n = seq_tokens(p, b), m = min(n, p.keep);
   if (h == 0 && tid == 0) p.new_len[b] = m;
   for (int i = m + tid; i < p.keep; i += kPickThreads) kept[i] = -1;
-  const auto zeros = [&] {
-    for (long long i = (long long)m + tid; i < p.weight_out_len; i += kPickThreads) wout[i] = 0.f;
+  const auto zeros = [&] {  // of 16 bytes where they can be
+    const long long a = m + ((16 - (reinterpret_cast<uintptr_t>(wout + m) & 15)) & 15) / 4, e = p.weight_out_len;
+    for (long long i = a + 4 * tid; i + 4 <= e; i += 4 * kPickThreads) *reinterpret_cast<float4*>(wout + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m + tid < min(a, e)) wout[m + tid] = 0.f;
+    const long long z = e - 1 - tid;  // behind the last 16 bytes
+    if (tid < 3 && z >= a + (e - a) / 4 * 4) wout[z] = 0.f;
   };
   if (n == m) {
     for (int i = tid; i < m; i += kPickThreads) {
@@ -170,14 +174,24 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
   const int run = ((n + kPickWarps - 1) / kPickWarps + 127) & ~127;
   const int r0 = min(n, warp * run), r1 = min(n, r0 + run);
   const bool cut = eq < ties;              // not all of the ties stay: the first ones
-  const auto above = [&](uint32_t k, int i) { return i < n && (i >= last || (need > 0 && k > t)); };
-  const auto equal = [&](uint32_t k, int i) { return i < last && need > 0 && k == t; };
+  const uint32_t from = cut ? t + 1u : t;  // keys from here on stay
+  // which of tokens i .. i + 3 stay anyway, a bit each, and which are the cut ties
+  const auto staying = [&](uint4 k, int i) {
+    unsigned f = (k.x >= from) | (k.y >= from) << 1 | (k.z >= from) << 2 | (k.w >= from) << 3;
+    if (need == 0) f = 0;                  // (the keys were not read)
+    if (i + 4 > last) f = ((i < last ? f & ((1u << (last - i)) - 1u) : 0u) | 15u << max(last - i, 0)) & ((1u << min(max(n - i, 0), 4)) - 1u);
+    return f;
+  };
+  const auto tied = [&](uint4 k, int i) {
+    const unsigned f = (k.x == t) | (k.y == t) << 1 | (k.z == t) << 2 | (k.w == t) << 3;
+    return i < last ? f & ((1u << min(last - i, 4)) - 1u) : 0u;
+  };
   unsigned gt = 0, tie = 0;
 #pragma unroll 2
   for (int i = r0 + 4 * lane; i < r1; i += 128) {
     const uint4 k = keys4(i);
-    gt += above(k.x, i) + above(k.y, i + 1) + above(k.z, i + 2) + above(k.w, i + 3);
-    tie += equal(k.x, i) + equal(k.y, i + 1) + equal(k.z, i + 2) + equal(k.w, i + 3);
+    gt += __popc(staying(k, i));
+    if (cut) tie += __popc(tied(k, i));
   }
   gt = __reduce_add_sync(0xffffffffu, gt), tie = __reduce_add_sync(0xffffffffu, tie);
   if (lane == 0) wsum[warp] = gt, weq[warp] = tie;
@@ -185,38 +199,30 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
   unsigned at0 = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
   unsigned eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? weq[lane] : 0u);
   at0 += min(eq0, eq);
+  // Sum over the lanes before this one of counts up to 4, and (added to `all`) over all lanes.
   const unsigned below = (1u << lane) - 1u;
+  const auto ahead = [&](unsigned c, unsigned& all) {
+    unsigned sum = all;
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+      const unsigned f = __ballot_sync(0xffffffffu, (c >> b) & 1u);
+      sum += __popc(f & below) << b, all += __popc(f) << b;
+    }
+    return sum;
+  };
   for (int i0 = r0; i0 < r1; i0 += 128) {
     const int i = i0 + 4 * lane;
     const uint4 k4 = keys4(i);
-    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-    bool in[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) in[j] = above(k[j], i + j) || (!cut && equal(k[j], i + j));
-    if (cut) {  // the tokens' ranks among the ties
-      unsigned before = eq0, mine = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned e = __ballot_sync(0xffffffffu, equal(k[j], i + j));
-        before += __popc(e & below), eq0 += __popc(e);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (equal(k[j], i + j)) in[j] = before + mine++ < eq;
+    unsigned f = staying(k4, i);
+    if (cut) {  // the first of the ties, by their ranks
+      unsigned e = tied(k4, i);
+      for (unsigned before = ahead(__popc(e), eq0); e && before < eq; e &= e - 1u, ++before) f |= e & -e;
     }
-    unsigned at = at0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const unsigned f = __ballot_sync(0xffffffffu, in[j]);
-      at += __popc(f & below), at0 += __popc(f);
+    for (unsigned at = ahead(__popc(f), at0); f; f &= f - 1u, ++at) {
+      const int j = __ffs(f) - 1;
+      kept[at] = i + j;
+      wout[at] = held && need > 0 ? key_weight(keys[i + j]) : w[i + j];
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (in[j]) {
-        kept[at] = i + j;
-        wout[at] = held && need > 0 ? key_weight(k[j]) : w[i + j];
-        ++at;
-      }
   }
 }
 
