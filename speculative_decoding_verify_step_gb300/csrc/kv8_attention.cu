@@ -29,7 +29,7 @@
 // of the rows from all partials, through distributed shared memory.
 //
 // What bounds it (8 kv heads of 128 with 4 query heads).  Two tiles of query rows: the cache's bytes,
-// 8 x 32768 tokens at width 4 in 93 us, 0.85 of the copy rate (a decode step of the same 86, 0.91).  Three
+// 8 x 32768 tokens at width 4 in 92 us, 0.86 of the copy rate (a decode step of the same 87, 0.91).  Three
 // and four: latencies, since 242 registers leave two warps per SM quarter: 64 x 512..2048 at
 // width 5 in 63 us, 0.41.  Short caches: one chain of latencies, 1 x 1024 tokens in 6.5 us.
 #include <math.h>
@@ -123,8 +123,9 @@ SPEC_DEVICE_INLINE int pieces_of(int units, int target) { return (units + target
 
 // Units of a piece, at most.  Pieces number at most groups + units / target: with few groups
 // as many as there are slots (CTAs that the GPU holds at once), with many up to half again
-// as many.  With 1.5 times the slots always, 32 x 512..8192 tokens at width 4 took 62 us instead of 74,
-// but 8 x 32768 103 instead of 93 and 64 x 512..2048 at width 5 75 instead of 63.
+// as many.  With 1.5 times the slots always, 37 x 64..8000 tokens at width 4 took 66 us instead of 69,
+// but 8 x 32768 104 instead of 92 and 64 x 512..2048 at width 5 67 instead of 63.  (Equal runs of units
+// over group bounds, a CTA taking several groups one behind another: 118, 98 and 75.)
 SPEC_DEVICE_INLINE int target_of(const Kv8AttnParams& p, const Seq& mine) {
   const int lane = threadIdx.x & 31;
   unsigned n = mine.units;
@@ -268,7 +269,9 @@ SPEC_DEVICE_INLINE bool sees(uint32_t anc, int w) { return w < 0 || (w < 16 && (
 template <int HD, int NT>
 struct Cfg {
   static constexpr int kStage = kUnit / kSub * kv8_sub_bytes(HD);
-  static constexpr int kCtas = NT == 1 ? 3 : 2;               // CTAs per SM, by registers
+  // CTAs per SM, by registers.  Two tiles in 168 registers instead of 186: 32 x 512..8192 tokens at
+  // width 4 64.5 us instead of 73.5; three tiles spill then (64 x 512..2048 at width 5 70 instead of 63).
+  static constexpr int kCtas = NT <= 2 ? 3 : 2;
   static constexpr int kQ = NT * (HD / 32) * 512;             // query fragments
   static constexpr int kStatic = NT * 8 * 4 * (1 + 2 * kWarps) + 1024;
   static constexpr int kStages0 = (233472 / kCtas - 1024 - kStatic - kQ) / (kWarps * kStage);
