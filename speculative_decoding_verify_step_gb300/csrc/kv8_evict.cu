@@ -5,20 +5,20 @@
 // order, to cells 0..m-1 of the destination table's pages; a destination sub-block gets the
 // least exponents that hold its tokens, as if the held values were written there.
 //
-// Two kernels.  The first takes one CTA per (sequence, kv head): its weights, as integers
+// Two kernels.  The first takes a CTA or two per (sequence, kv head): its weights, as integers
 // that order like them, come into shared memory once (up to 48 K tokens; of longer ones
 // they are read from L2 again) and a radix select of 11, 11 and 10 bits finds the
 // threshold, the last two digits among the few tokens that share the first.  11 bits, because
 // weights spread over exponents: with 8 most lanes of a warp would add to the same counter.
 // Warps own runs of neighbouring tokens, four to a lane, so the tokens that stay come out in
-// order from a scan of the warps' counts.  It is bound by one SM's integer pipe: passes of one
-// token to a lane and step over all tokens took 35 us for 64 heads of 32768 tokens, and
-// clusters of four CTAs, whose barriers cost about 1 us each, 32.
+// order from a scan of the warps' counts.  It is bound by one SM's integer pipe and shared-memory
+// atomics: 19 us for 64 heads of 32768 tokens.  (Passes of one token to a lane and step over all
+// tokens took 35, and clusters of four CTAs, whose barriers cost about 1 us each, 32.)
 //
 // The second kernel takes one warp per destination sub-block and head.  A token's K is one run of
-// bytes; its V is one byte of each word of a run of a whole sub-block (four tokens share a
-// word), so where neighbours do not stay together, V is mostly read whole: 8 x 32768 tokens to 2048, 8
-// heads of 128, move in 42 us, 198 MB of reads; the selection before it takes 25.
+// bytes; its V one byte of each word of a quarter of its sub-block (four tokens share a word), so
+// where neighbours do not stay together, V is read four times over: 8 x 32768 tokens to 2048, 8
+// heads of 128, move in 32 us, the selection before it takes 19.
 #include <math.h>
 
 #include <algorithm>
@@ -54,7 +54,7 @@ SPEC_DEVICE_INLINE int seq_tokens(const Kv8EvictParams& p, int b) {
   return (int)max(0ll, min((long long)p.kv_len[b], cap));
 }
 
-// grid (Hkv, B)
+// grid (Hkv, B, shares): CTAs of a head find the same threshold, and each writes a share of what comes out.
 __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_constant__ Kv8EvictParams p) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ __align__(8) unsigned int hist[2048];
@@ -69,17 +69,18 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
   int32_t* kept = p.kept + group * p.keep;
   float* wout = p.weight_out + group * p.weight_out_len;
   const int n = seq_tokens(p, b), m = min(n, p.keep);
-  if (h == 0 && tid == 0) p.new_len[b] = m;
-  for (int i = m + tid; i < p.keep; i += kPickThreads) kept[i] = -1;
+  const int share = blockIdx.z, shares = gridDim.z, me = share * kPickThreads + tid, step = shares * kPickThreads;
+  if (h == 0 && me == 0) p.new_len[b] = m;
+  for (int i = m + me; i < p.keep; i += step) kept[i] = -1;
   const auto zeros = [&] {  // of 16 bytes where they can be
     const long long a = m + ((16 - (reinterpret_cast<uintptr_t>(wout + m) & 15)) & 15) / 4, e = p.weight_out_len;
-    for (long long i = a + 4 * tid; i + 4 <= e; i += 4 * kPickThreads) *reinterpret_cast<float4*>(wout + i) = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m + tid < min(a, e)) wout[m + tid] = 0.f;
-    const long long z = e - 1 - tid;  // behind the last 16 bytes
-    if (tid < 3 && z >= a + (e - a) / 4 * 4) wout[z] = 0.f;
+    for (long long i = a + 4 * me; i + 4 <= e; i += 4 * step) *reinterpret_cast<float4*>(wout + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m + me < min(a, e)) wout[m + me] = 0.f;
+    const long long z = e - 1 - me;  // behind the last 16 bytes
+    if (me < 3 && z >= a + (e - a) / 4 * 4) wout[z] = 0.f;
   };
   if (n == m) {
-    for (int i = tid; i < m; i += kPickThreads) {
+    for (int i = me; i < m; i += step) {
       kept[i] = i;
       wout[i] = w[i];
     }
@@ -186,18 +187,22 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
     const unsigned f = (k.x == t) | (k.y == t) << 1 | (k.z == t) << 2 | (k.w == t) << 3;
     return i < last ? f & ((1u << min(last - i, 4)) - 1u) : 0u;
   };
-  unsigned gt = 0, tie = 0;
+  // this CTA's steps: tokens [a0, a1) of the run
+  const int part = ((r1 - r0 + shares - 1) / shares + 127) & ~127, a0 = min(r1, r0 + share * part), a1 = min(r1, a0 + part);
+  unsigned gt = 0, tie = 0, gt0 = 0, tie0 = 0;
 #pragma unroll 2
   for (int i = r0 + 4 * lane; i < r1; i += 128) {
     const uint4 k = keys4(i);
-    gt += __popc(staying(k, i));
-    if (cut) tie += __popc(tied(k, i));
+    const unsigned c = __popc(staying(k, i)), e = cut ? __popc(tied(k, i)) : 0u;
+    gt += c, tie += e;
+    if (i < a0) gt0 += c, tie0 += e;
   }
   gt = __reduce_add_sync(0xffffffffu, gt), tie = __reduce_add_sync(0xffffffffu, tie);
   if (lane == 0) wsum[warp] = gt, weq[warp] = tie;
   __syncthreads();
   unsigned at0 = __reduce_add_sync(0xffffffffu, lane < warp ? wsum[lane] : 0u);
   unsigned eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? weq[lane] : 0u);
+  at0 += __reduce_add_sync(0xffffffffu, gt0), eq0 += __reduce_add_sync(0xffffffffu, tie0);
   at0 += min(eq0, eq);
   // Sum over the lanes before this one of counts up to 4, and (added to `all`) over all lanes.
   const unsigned below = (1u << lane) - 1u;
@@ -210,7 +215,7 @@ __global__ void __launch_bounds__(kPickThreads) kv8_pick_kernel(const __grid_con
     }
     return sum;
   };
-  for (int i0 = r0; i0 < r1; i0 += 128) {
+  for (int i0 = a0; i0 < a1; i0 += 128) {
     const int i = i0 + 4 * lane;
     const uint4 k4 = keys4(i);
     unsigned f = staying(k4, i);
@@ -373,7 +378,13 @@ cudaError_t launch_kv8_evict(const Kv8EvictParams& p, cudaStream_t st) {
   const long long most = std::min((long long)p.max_pages * kPage, p.weight_len);
   // whole steps of 128 tokens: a warp's last step reads past the last one
   const size_t smem = (size_t)std::min<long long>((most + 127) & ~127ll, kPickKeys) * 4;
-  e = launch_k(kv8_pick_kernel, dim3(p.Hkv, p.B), dim3(kPickThreads), smem, st, p);
+  int sms = 0;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  // two CTAs to a head of many tokens where that leaves none waiting (64 heads of 32768 tokens to 2048
+  // 49.5 us, with one each 51.9; nothing is won where few tokens come out)
+  const int shares = most > 8192 && (long long)p.Hkv * p.B * 2 <= sms ? 2 : 1;
+  e = launch_k(kv8_pick_kernel, dim3(p.Hkv, p.B, shares), dim3(kPickThreads), smem, st, p);
   if (e != cudaSuccess) return e;
   const long long total = (long long)p.B * p.Hkv * ((p.keep + kSub - 1) / kSub);
   const long long ctas = (total + kMoveWarps - 1) / kMoveWarps;
