@@ -16,9 +16,8 @@
 // fp16 numbers.  K: lane (g, c) takes chunks c and c + 4 of tokens g and g + 8; the
 // halves of odd tokens' rows are exchanged (head_dim 128), so that the eight lanes of a
 // shared-memory phase hit all banks.  V: lane (g, c) takes dims g hd/8 .. of tokens 2c,
-// 2c + 1, 2c + 8 and 2c + 9; a word is one dim of the four, a chunk four dims.  The chunks of
-// the eight lanes of one c are a line of 128 bytes, so that a token alone is read with three
-// others' bytes only; their order in it gives all banks to the lanes of a phase.
+// 2c + 1, 2c + 8 and 2c + 9; a word is one dim of the four, a chunk four dims, and the 32
+// lanes' chunks are adjacent.
 #pragma once
 
 #include "common.cuh"
@@ -38,8 +37,7 @@ SPEC_DEVICE_INLINE int kv8_k_chunk(int t, int j) {
 // Byte offset of V's chunk j (dims 4 j .. of the lane's) for lane (g, c) = g * 4 + c.
 template <int HD>
 SPEC_DEVICE_INLINE int kv8_v_chunk(int j, int lane) {
-  const int g = lane >> 2, c = lane & 3;
-  return kSub * HD + j * 512 + c * 128 + ((g ^ (c << 1)) << 4);
+  return kSub * HD + j * 512 + lane * 16;
 }
 
 constexpr int kKv8MinExp = -15, kKv8MaxExp = 8;
