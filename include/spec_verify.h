@@ -424,7 +424,11 @@ spec_status spec_kv4_attention(int32_t B, int32_t W, int32_t total_rows, const i
  * from the bytes there: 0 in zeroed memory.)
  * Rows, positions, row_off, start, page_table, dtype, strides, streams and positions
  * without a cell are as in spec_kv4_write.  Codes that were never written may be
- * anything: they have no effect on tokens that were. */
+ * anything: they have no effect on tokens that were.
+ * A block is its four sub-blocks, each 32 * head_dim + 16 bytes.  Token u, dim d: K's code at
+ * u * head_dim + 16 * J + d % 16, J = d / 16, at head_dim 128 xor 4 for odd u; V's, with
+ * w = head_dim / 8, at 16 * head_dim + d % w / 4 * 512 + (d / w * 4 + u % 8 / 2) * 16
+ * + d % 4 * 4 + u / 8 * 2 + u % 2; then at 32 * head_dim the exponents of K and V (signed). */
 int64_t spec_kv8_block_bytes(int32_t head_dim);
 
 /* Quantise rows k, v [total_rows, n_kv_heads, head_dim] into their cells. */

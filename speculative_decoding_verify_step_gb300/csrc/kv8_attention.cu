@@ -869,15 +869,15 @@ cudaError_t launch_nt(Kv8AttnParams p, cudaStream_t st) {
                   p, NT * 8, blocks);
 }
 
-// Four CTAs per SM where there is that much work.
-dim3 weight_grid(const Kv8AttnParams& p) {
+// CTAs of the weights' kernels: `ctas` per SM where there is that much work.
+dim3 weight_grid(const Kv8AttnParams& p, int ctas) {
   const long long groups = (long long)p.B * p.Hkv, units = (p.kv_len_hint + kUnit - 1) / kUnit;
-  const long long per = std::max<long long>(1, 4ll * p.sm_count / groups);  // CTAs of a group
+  const long long per = std::max<long long>(1, (long long)ctas * p.sm_count / groups);  // CTAs of a group
   return dim3((unsigned)std::max<long long>(1, std::min(per, (units + kWeightWarps - 1) / kWeightWarps)), p.Hkv, p.B);
 }
 template <int HD, int NT>
 cudaError_t launch_weight(const Kv8AttnParams& p, cudaStream_t st) {
-  return launch_k(kv8_weight_kernel<HD, NT>, weight_grid(p), dim3(kWeightWarps * 32), 0, st, p);
+  return launch_k(kv8_weight_kernel<HD, NT>, weight_grid(p, 4), dim3(kWeightWarps * 32), 0, st, p);
 }
 
 template <int HD>
@@ -891,10 +891,7 @@ cudaError_t launch_hd(const Kv8AttnParams& p, cudaStream_t st) {
     case 4: e = launch_nt<HD, 4>(p, st); break;
   }
   if (e != cudaSuccess || !p.weight) return e;
-  if (p.scores) {
-    const dim3 grid = weight_grid(p);
-    return launch_k(kv8_weight_scores_kernel, grid, dim3(kWeightWarps * 32), 0, st, p);
-  }
+  if (p.scores) return launch_k(kv8_weight_scores_kernel, weight_grid(p, 8), dim3(kWeightWarps * 32), 0, st, p);
   const int tiles = (rows + 7) / 8;
   return tiles == 1 ? launch_weight<HD, 1>(p, st) : tiles == 2 ? launch_weight<HD, 2>(p, st)
        : tiles <= 4 ? launch_weight<HD, 4>(p, st) : launch_weight<HD, 8>(p, st);

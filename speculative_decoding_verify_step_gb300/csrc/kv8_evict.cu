@@ -16,9 +16,9 @@
 // tokens took 35, and clusters of four CTAs, whose barriers cost about 1 us each, 32.)
 //
 // The second kernel takes one warp per destination sub-block and head.  A token's K is one run of
-// bytes; its V one byte of each word of a quarter of its sub-block (four tokens share a word), so
-// where neighbours do not stay together, V is read four times over: 8 x 32768 tokens to 2048, 8
-// heads of 128, move in 32 us, the selection before it takes 19.
+// bytes; its V one byte of each word of a quarter of its sub-block (four tokens share a word), in 16-byte
+// pieces, so where neighbours do not stay together, V is mostly read whole: 8 x 32768 tokens to 2048, 8
+// heads of 128, move in 40 us, the selection before it takes 19.
 #include <math.h>
 
 #include <algorithm>
@@ -382,7 +382,7 @@ cudaError_t launch_kv8_evict(const Kv8EvictParams& p, cudaStream_t st) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   // two CTAs to a head of many tokens where that leaves none waiting (64 heads of 32768 tokens to 2048
-  // 49.5 us, with one each 51.9; nothing is won where few tokens come out)
+  // 59.0 us, with one each 61.3; nothing is won where few tokens come out)
   const int shares = most > 8192 && (long long)p.Hkv * p.B * 2 <= sms ? 2 : 1;
   e = launch_k(kv8_pick_kernel, dim3(p.Hkv, p.B, shares), dim3(kPickThreads), smem, st, p);
   if (e != cudaSuccess) return e;

@@ -34,11 +34,14 @@
 // A small top_k needs no more than each CTA's own maxima: its tokens down to the bin of its own
 // k-th largest go to the first CTA at once, after one barrier.
 //
+// Up to 128 candidates are ranked by comparing each with each; more are sorted, or first cut down
+// by a histogram of the candidates alone.
+//
 // What bounds it: chains of short steps (cluster barriers of 0.8 us, instructions fetched once per
-// row), not bytes.  GPU us against the bytes at the copy rate: 1 x 128256 fp32 with top_p 27.6 (0.08),
-// 64 x 128256 fp32 with top_k, top_p and q 33.7 (9.7), 256 x 50257 bf16, settings per row, 88 (3.8): there
-// the masses of rows without top_k.  Decisions by histograms of all CTAs alone, without candidates,
-// took 41, 111 and 340.
+// row), not bytes.  GPU us against the bytes at the copy rate: 1 x 128256 fp32 with top_p 22.6 (0.08),
+// 64 x 128256 fp32 with top_k, top_p and q 28.2 (9.7), 256 x 50257 bf16, settings per row, 73.5 (3.8):
+// there the masses of rows without top_k.  Decisions by histograms of all CTAs alone, without
+// candidates, took 41, 111 and 340; sorting every list of candidates 27.6, 33.7 and 88.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

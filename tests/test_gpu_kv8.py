@@ -116,6 +116,27 @@ def test_writes_in_any_split_bit_for_bit(spec, hd, H, B, dt):
         c.check_read([a - 3 for a in at], [3] * B, dt, ragged=False)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+def test_bytes_of_a_block(spec, hd):
+    """Where each code lies, which pools that a caller lays out have to hold to."""
+    codes = torch.randint(0, 256, (2, 64, 2, hd), generator=torch.Generator().manual_seed(hd), dtype=torch.uint8)
+    codes[(codes & 127) == 127] = 1                         # no NaN
+    codes[:, ::16] = 126                                    # 448: exponent 0 in every sub-block
+    k, v = codes.view(torch.float8_e4m3fn).half()
+    pool = spec.spec_kv8_pool(2, 2, hd)
+    z = torch.zeros(1, dtype=torch.int32, device="cuda")
+    spec.spec_kv8_write(k[None].cuda(), v[None].cuda(), z, z.view(1, 1) + 1, pool)
+    want = torch.zeros(2, 4, 32 * hd + 16, dtype=torch.uint8)
+    for t in range(64):
+        u, (c, i) = t % 16, (t % 8 // 2, t % 16 // 8 * 2 + t % 2)
+        for d in range(hd):
+            j, g, n = d // 16, d // (hd // 8), d % (hd // 8)
+            at_k = u * hd + ((j ^ (4 * (u % 2))) if hd == 128 else j) * 16 + d % 16
+            at_v = 16 * hd + n // 4 * 512 + (4 * g + c) * 16 + n % 4 * 4 + i
+            want[:, t // 16, at_k], want[:, t // 16, at_v] = codes[0, t, :, d], codes[1, t, :, d]
+    assert torch.equal(pool[1].cpu().view(2, 4, -1), want) and (pool[0] == 0).all()
+
+
 def test_uniform_rows_overwrite_and_start_anew(spec):
     c = Cache(spec, 2, 2, 128, 2)
     c.write([0, 0], [c.values(60, 50.0)] * 2, [c.values(60, 50.0)] * 2, ragged=False)
