@@ -11,13 +11,16 @@
 // turns the weights into the B operand of the second product.
 //
 // Rounding.  q is scaled per row by a power of two into fp16's range (bf16 queries keep
-// all their bits); the weights times 2^b are rounded to fp16: by 2^-11 of themselves, or
-// 2^-25 where they are subnormal.  Everything else is fp32.  The running maximum of a row
-// is that of score + b over the tokens it sees, so the largest weight times 2^b is near
-// one whatever the exponents of tokens that the row does not see or hardly weighs; the sum
-// takes the weights without 2^b.  Score and maximum are numbers of one float grid (the
-// product with the scale is rounded before the difference is taken), so scores past 2^24
-// keep all weight on the largest.
+// all their bits); the weights times 2^b are rounded to fp16.  Everything else is fp32.  The
+// running maximum of a row is that of score + b over the tokens it sees, so the largest
+// weight times 2^b is near one whatever the exponents of tokens that the row does not see
+// or hardly weighs; the sum takes the weights without 2^b.  They are rounded as multiples
+// of 2^-11, which takes the largest next to the end of fp16's range: a weight times 2^b is off
+// by 2^-11 of itself down to 2^-25 of the largest, and below by 2^-36 of the largest at most.
+// So 2^20 light tokens beside a heavy one keep their share to 2^-16, and dims where a
+// sub-block of large exponent has zeros keep the others' values, as long as those weigh that much.  Score and maximum
+// are numbers of one float grid (the product with the scale is rounded before the difference
+// is taken), so scores past 2^24 keep all weight on the largest.
 //
 // Work split.  A group is a sequence and a kv head, a unit 32 of its tokens.  Groups longer
 // than a common target are cut into pieces of at most that many units; a CTA of four warps
@@ -54,7 +57,12 @@ constexpr int kMaxCtas = 3;           // per SM, of any variant
 constexpr int kMaxCluster = 8;
 constexpr int kClusterUnits = 40;     // of a cluster's CTA, at most
 constexpr float kNoMax = -1e30f;      // running maximum of a row that has seen no token
-constexpr float kSlack = 6.f;         // how far score + b may pass the running maximum
+// How far score + b may pass the running maximum: 64 x 512..2048 tokens at width 5 take 65.0 us with
+// 2, 63.3 with 4 and 62.5 with 6, but the weights' unit rises with it.
+constexpr float kSlack = 4.f;
+// Unit of the weights times 2^b as fp16: they are at most 2^kSlack, or, where maxima are 2^25 or
+// more (float steps of 4 or more, to which score + b is rounded down), 2^8.
+constexpr float kLift = 2048.f, kLiftHuge = 128.f, kHuge = 33554432.f;
 
 SPEC_DEVICE_INLINE float ex2(float x) {
   float y;
@@ -378,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
   }
 
   int s = 0;
+  float lift = kLift;
   bool failed = false;
   for (int u = u0 + warp; u < u1; u += kWarps) {
     if ((there >> s) & 1u) {
@@ -402,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
         const uint32_t par = *reinterpret_cast<const uint32_t*>(st + k * SUB + 2 * kSub * HD);
         const float ka = kv8_pow2(kv8_exp(par, 0));
         ev[k] = kv8_exp(par, 1);
-        const float eb = (float)ev[k];
+        const float room = kSlack - (float)ev[k];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float2 f = *reinterpret_cast<const float2*>(&s_f[nt * 8 + 2 * c]);
@@ -429,10 +438,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
             for (int e = 0; e < 2; ++e)
               if (2 * c + e < rows) __stcs(to + (2 * c + e) * kUnit, x[e]), __stcs(to + (2 * c + e) * kUnit + 8, x[2 + e]);
           }
-          over |= fmaxf(x[0], x[2]) + eb > top[nt][0] + kSlack || fmaxf(x[1], x[3]) + eb > top[nt][1] + kSlack;
+          over |= fmaxf(x[0], x[2]) - top[nt][0] > room || fmaxf(x[1], x[3]) - top[nt][1] > room;
         }
       }
       if (__any_sync(0xffffffffu, over)) {  // raise the maxima and rescale what is summed up
+        bool huge = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -447,16 +457,26 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             m = fmaxf(m, top[nt][e]);
+            huge |= m > kNoMax && fabsf(m) >= kHuge;
             const float a = ex2(top[nt][e] - m);
             top[nt][e] = m;
             sum[nt][e] *= a;
 #pragma unroll
             for (int t = 0; t < MT; ++t) acc[nt][t][e] *= a, acc[nt][t][2 + e] *= a;
           }
+        if (lift != kLiftHuge && __any_sync(0xffffffffu, huge)) {
+          lift = kLiftHuge;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[nt][t][i] *= kLiftHuge / kLift;
+        }
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const float vb = kv8_pow2(ev[k]);
+        const float vb = kv8_pow2(ev[k]) * lift;
         uint32_t pb[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -505,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
   __syncwarp();
 
   // The warp's partial in its ring's place: [ROWS][HD].
+  const float unit = 1.f / lift;
   float* const part = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -519,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
 #pragma unroll
       for (int t = 0; t < MT; t += 2)
         *reinterpret_cast<float4*>(part + r * HD + g * (HD / 8) + 2 * t) =
-            make_float4(acc[nt][t][e], acc[nt][t][2 + e], acc[nt][t + 1][e], acc[nt][t + 1][2 + e]);
+            make_float4(acc[nt][t][e] * unit, acc[nt][t][2 + e] * unit, acc[nt][t + 1][e] * unit, acc[nt][t + 1][2 + e] * unit);
     }
   __syncthreads();
   constexpr int V4 = HD / 4;
