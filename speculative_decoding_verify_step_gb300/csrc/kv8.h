@@ -42,8 +42,8 @@ struct Kv8AttnParams {
   float scale;                 // of q . k
   uint32_t anc[16];            // window rows that row j sees (bit i)
   int slots, cluster;          // CTAs resident at once, CTAs of a cluster: set by the launcher
-  float* workspace;            // kv8_attention_workspace bytes: partials, then lse
-  float* lse;                  // [total_rows, Hq] log2 of each row's sum of weights, or null: set by the launcher
+  float* workspace;            // kv8_attention_workspace bytes: partials, then norm and scores
+  float2* norm;                // [total_rows, Hq] each row's maximum and inverse sum, or null: set by the launcher
   float* scores;               // [B, Hkv, units of 32 tokens, rows, 32] or null: set by the launcher
   float* weight;               // [B, Hkv, weight_len] or null
   long long weight_len;

@@ -192,9 +192,10 @@ SPEC_DEVICE_INLINE void store_row4(const Kv8AttnParams& p, long long row, int he
   }
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row * p.Hq + head) * hd + d4 * 4) = w;
 }
-// log2 of a row's sum of weights; a row that sees no token gives nobody any.
-SPEC_DEVICE_INLINE void store_lse(const Kv8AttnParams& p, long long row, int head, float m, float l) {
-  if (p.lse) p.lse[row * p.Hq + head] = l > 0.f ? m + __log2f(l) : l == l ? INFINITY : NAN;
+// What turns a row's scores into weights, 2^(score - m) / l: m and 1 / l apart, since from m = 2^24 on
+// m + log2(l) would lose l.  A row that sees no token gives nobody any.
+SPEC_DEVICE_INLINE void store_norm(const Kv8AttnParams& p, long long row, int head, float m, float l) {
+  if (p.norm) p.norm[row * p.Hq + head] = l > 0.f ? make_float2(m, 1.f / l) : l == l ? make_float2(INFINITY, 0.f) : make_float2(NAN, NAN);
 }
 
 // Rows [r0, r0 + 8 NT) of a group's query rows (`rows` in all; window at flat row row0, kv head
@@ -570,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
     if (whole) {
       const int row = seq.row0 + (r0 + r) / grp, head = kvh * grp + (r0 + r) % grp;
       store_row4(p, row, head, HD, d4, o, s_fail ? 1.f : l);
-      if (d4 == 0) store_lse(p, row, head, M, l);
+      if (d4 == 0) store_norm(p, row, head, M, l);
     } else {
       float* const rec = CL ? record(r) : ws + r * HD;
       *reinterpret_cast<float4*>(rec + d4 * 4) = o;
@@ -614,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<HD, NT>::kCtas))
         }
       const int row = seq.row0 + (r0 + r) / grp, head = kvh * grp + (r0 + r) % grp;
       store_row4(p, row, head, HD, d4, l == l ? o : make_float4(NAN, NAN, NAN, NAN), l == l ? l : 1.f);
-      if (d4 == 0) store_lse(p, row, head, M, l);
+      if (d4 == 0) store_norm(p, row, head, M, l);
     }
     __syncwarp();
     cluster_arrive_relaxed();  // its reads are done: no CTA leaves before all have
@@ -650,7 +651,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     for (int it = blockIdx.x * kMergeWarps * 32 + threadIdx.x; it < rows * V4; it += gridDim.x * kMergeWarps * 32) {
       const int r = it / V4;
       store_row4(p, seq.row0 + r / grp, kvh * grp + r % grp, HD, it % V4, make_float4(0.f, 0.f, 0.f, 0.f), 0.f);
-      if (it % V4 == 0) store_lse(p, seq.row0 + r / grp, kvh * grp + r % grp, 0.f, 0.f);
+      if (it % V4 == 0) store_norm(p, seq.row0 + r / grp, kvh * grp + r % grp, 0.f, 0.f);
     }
     return;
   }
@@ -726,12 +727,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     if (part == 0 && r < rows) {
       const int row = seq.row0 + r / grp, head = kvh * grp + r % grp;
       store_row4(p, row, head, HD, d4, l == l ? o : make_float4(NAN, NAN, NAN, NAN), l == l ? l : 1.f);
-      if (d4 == 0) store_lse(p, row, head, M, l);
+      if (d4 == 0) store_norm(p, row, head, M, l);
     }
   }
 }
 
-// weight[b, h, t] += sum over the group's rows of 2^(score - lse): the scores once more, from K
+// weight[b, h, t] += sum over the group's rows of 2^(score - m) / l: the scores once more, from K
 // alone.  grid (CTAs of a group, Hkv, B); a unit of 32 tokens is one warp's, which alone touches
 // their weights.
 constexpr int kWeightWarps = 8;
@@ -739,7 +740,8 @@ template <int HD, int NT>
 __global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_kernel(const __grid_constant__ Kv8AttnParams p) {
   constexpr int ROWS = NT * 8, SUB = kv8_sub_bytes(HD);
   __shared__ __align__(16) uint8_t qfrag[NT * (HD / 32) * 512];
-  __shared__ float s_f[ROWS], s_lse[ROWS];
+  __shared__ float s_f[ROWS];
+  __shared__ float2 s_norm[ROWS];
   __shared__ uint32_t s_anc[16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int b = blockIdx.z, kvh = blockIdx.y, grp = p.Hq / p.Hkv;
@@ -752,7 +754,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_kernel(const __g
   load_queries<HD, NT, kWeightWarps * 32>(p, seq.row0, kvh, 0, rows, qfrag, s_f);
   if (threadIdx.x < 16) s_anc[threadIdx.x] = p.anc[threadIdx.x];
   for (int r = threadIdx.x; r < ROWS; r += kWeightWarps * 32)
-    s_lse[r] = r < rows ? p.lse[(long long)(seq.row0 + r / grp) * p.Hq + kvh * grp + r % grp] : INFINITY;
+    s_norm[r] = r < rows ? p.norm[(long long)(seq.row0 + r / grp) * p.Hq + kvh * grp + r % grp] : make_float2(INFINITY, 0.f);
   __syncthreads();
   float* const weight = p.weight + ((long long)b * p.Hkv + kvh) * p.weight_len;
   for (int u = blockIdx.x * kWeightWarps + warp; u < units; u += gridDim.x * kWeightWarps) {
@@ -779,14 +781,15 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_kernel(const __g
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int r = nt * 8 + 2 * c + e;
-          const float f = s_f[r] * ka, lse = s_lse[r];
+          const float f = s_f[r] * ka;
+          const float2 norm = s_norm[r];
           uint32_t anc = 0xffffffffu;
           if (masked) anc = r < rows ? s_anc[r / grp] & ((1u << seq.Wb) - 1u) : 0u;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float w = ex2(__fmul_rn(sc[nt][2 * h + e], f) - lse);
+            const float w = ex2(__fmul_rn(sc[nt][2 * h + e], f) - norm.x);
             const int key = u * kUnit + k * kSub + g + 8 * h;
-            if (!masked || (key < seq.n_keys && sees(anc, key - seq.L))) add[2 * k + h] += w;
+            if (!masked || (key < seq.n_keys && sees(anc, key - seq.L))) add[2 * k + h] = fmaf(w, norm.y, add[2 * k + h]);
           }
         }
     }
@@ -800,9 +803,9 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_kernel(const __g
   }
 }
 
-// The same from the scores that the attention left (few rows): a lane per token.
-__global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_scores_kernel(const __grid_constant__ Kv8AttnParams p) {
-  __shared__ float s_lse[8];
+// The same from the scores that the attention left (few rows): a lane per token, eight CTAs per SM.
+__global__ void __launch_bounds__(kWeightWarps * 32, 8) kv8_weight_scores_kernel(const __grid_constant__ Kv8AttnParams p) {
+  __shared__ float2 s_norm[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.z, kvh = blockIdx.y, grp = p.Hq / p.Hkv;
   pdl_wait();
@@ -812,12 +815,12 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_scores_kernel(co
   const int units = (int)min((long long)seq.units, (p.weight_len + kUnit - 1) / kUnit);
   if ((int)blockIdx.x * kWeightWarps >= units) return;
   if (threadIdx.x < 8)
-    s_lse[threadIdx.x] = threadIdx.x < rows ? p.lse[(long long)(seq.row0 + threadIdx.x / grp) * p.Hq + kvh * grp + threadIdx.x % grp]
-                                            : INFINITY;
+    s_norm[threadIdx.x] = threadIdx.x < rows ? p.norm[(long long)(seq.row0 + threadIdx.x / grp) * p.Hq + kvh * grp + threadIdx.x % grp]
+                                             : make_float2(INFINITY, 0.f);
   __syncthreads();
   float* const weight = p.weight + ((long long)b * p.Hkv + kvh) * p.weight_len;
   const float* const scores = p.scores + ((long long)b * p.Hkv + kvh) * p.max_pages * 2 * (p.W * grp * kUnit);
-#pragma unroll 2
+#pragma unroll 1
   for (int u = blockIdx.x * kWeightWarps + warp; u < units; u += gridDim.x * kWeightWarps) {
     const int pg = p.page_table[(long long)b * p.max_pages + (u >> 1)];
     const int t = u * kUnit + lane;
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(kWeightWarps * 32) kv8_weight_scores_kernel(co
     for (int r = 0; r < 8; ++r) s[r] = r < rows ? __ldcs(x + r * kUnit) : 0.f;
     const float was = weight[t];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) w += ex2(s[r] - s_lse[r]);
+    for (int r = 0; r < 8; ++r) w = fmaf(ex2(s[r] - s_norm[r].x), s_norm[r].y, w);
     weight[t] = was + w;
   }
 }
@@ -937,7 +940,7 @@ long long score_floats(const Kv8AttnParams& p) {
 }  // namespace
 
 long long kv8_attention_workspace(const Kv8AttnParams& p, bool weight) {
-  return 4 * (partial_floats(p) + (weight ? (long long)p.total_rows * p.Hq + score_floats(p) : 0));
+  return 4 * (partial_floats(p) + (weight ? 2ll * p.total_rows * p.Hq + score_floats(p) : 0));
 }
 
 bool kv8_attention_needs_workspace(const Kv8AttnParams& p, bool weight) {
@@ -947,8 +950,9 @@ bool kv8_attention_needs_workspace(const Kv8AttnParams& p, bool weight) {
 cudaError_t launch_kv8_attention(const Kv8AttnParams& params, cudaStream_t st) {
   Kv8AttnParams p = params;
   if (p.weight) {
-    p.lse = p.workspace + partial_floats(p);
-    if (score_floats(p) > 0) p.scores = p.lse + (long long)p.total_rows * p.Hq;
+    float* const norm = p.workspace + partial_floats(p);  // (a whole number of row pairs)
+    p.norm = reinterpret_cast<float2*>(norm);
+    if (score_floats(p) > 0) p.scores = norm + 2ll * p.total_rows * p.Hq;
   }
   return p.hd == 128 ? launch_hd<128>(p, st) : launch_hd<64>(p, st);
 }
