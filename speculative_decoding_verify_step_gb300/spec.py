@@ -8,6 +8,7 @@ the library has not been built -- there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Iterable, Optional, Sequence, Tuple
 
@@ -794,6 +795,16 @@ def _setting(t, dtype, n: int, dev, what: str):
     return t
 
 
+def _uniforms(u, n: int, dev):
+    """None, or uniforms as a contiguous fp32 [n] tensor on dev.  The draw takes floor(2^24 u): of other
+    types that much is kept, so that what is below one stays so."""
+    if isinstance(u, (int, float)):
+        u = math.floor(u * 2 ** 24) / 2 ** 24 if abs(u) < 1 else u
+    elif u is not None and not (isinstance(u, torch.Tensor) and u.dtype in (torch.float32, torch.float16, torch.bfloat16)):
+        u = torch.floor(torch.as_tensor(u, dtype=torch.float64) * 2 ** 24) / 2 ** 24
+    return _setting(u, torch.float32, n, dev, "u")
+
+
 def spec_sample(logits: torch.Tensor, u: Optional[torch.Tensor] = None, temperature=1.0, top_k=None, top_p=None,
                 min_p=None, rows_per_setting: int = 1, return_probs: bool = False, outs=None):
     """One token per row of logits [..., V] (fp32, bf16 or fp16; [rows, V] may be strided) from
@@ -823,7 +834,7 @@ def spec_sample(logits: torch.Tensor, u: Optional[torch.Tensor] = None, temperat
         t_all, temperature = float(temperature), None
     else:
         temperature = _setting(temperature, torch.float32, n, dev, "temperature")
-    u = _setting(u, torch.float32, rows, dev, "u")
+    u = _uniforms(u, rows, dev)
     top_k = _setting(top_k, torch.int32, n, dev, "top_k")
     top_p = _setting(top_p, torch.float32, n, dev, "top_p")
     min_p = _setting(min_p, torch.float32, n, dev, "min_p")
