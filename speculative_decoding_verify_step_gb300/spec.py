@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import numbers
 import os
 from typing import Iterable, Optional, Sequence, Tuple
 
@@ -780,14 +781,31 @@ def spec_kv8_evict(pool: torch.Tensor, weight: torch.Tensor, kv_len: torch.Tenso
 _SAMPLE_DTYPE = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 
 
+_INT_MAX, _FP32_LEAST = 2 ** 31 - 1, 2.0 ** -149
+
+
+def _fp32_number(x) -> float:
+    """x, but not zero where fp32 would make it zero, and infinite past its largest."""
+    x = float(x)
+    return math.copysign(_FP32_LEAST, x) if 0 < abs(x) < _FP32_LEAST else math.copysign(math.inf, x) if abs(x) > 3.4e38 else x
+
+
 def _setting(t, dtype, n: int, dev, what: str):
-    """None, or a contiguous [n] tensor of `dtype` on dev (a number counts for all)."""
+    """None, or a contiguous [n] tensor of `dtype` on dev (a number counts for all).  What the type cannot
+    hold stays on its side of the range: whole numbers saturate (not a number: -1), others do not become 0."""
     if t is None:
         return None
-    if isinstance(t, (int, float)):
-        return torch.full((n,), t, dtype=dtype, device=dev)  # no copy from the host: calls can be captured
+    whole = dtype is torch.int32
+    if isinstance(t, numbers.Real):
+        if whole:
+            t = math.floor(max(-1, min(t, _INT_MAX))) if t == t else -1
+        return torch.full((n,), t if whole else _fp32_number(t), dtype=dtype, device=dev)  # no copy from the host: calls can be captured
     if not isinstance(t, torch.Tensor):
-        t = torch.as_tensor(t)
+        t = torch.as_tensor(t) if whole else torch.as_tensor(t, dtype=torch.float64)
+    if t.dtype is not dtype and whole:
+        t = (torch.nan_to_num(t.floor(), nan=-1.0).double() if t.is_floating_point() else t).clamp(-1, _INT_MAX)
+    elif t.dtype is torch.float64 and dtype is torch.float32:
+        t = torch.where((t != 0) & (t.abs() < _FP32_LEAST), torch.copysign(torch.full_like(t, _FP32_LEAST), t), t)
     if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
         t = t.to(device=dev, dtype=dtype).contiguous()
     if t.numel() != n:
@@ -798,7 +816,7 @@ def _setting(t, dtype, n: int, dev, what: str):
 def _uniforms(u, n: int, dev):
     """None, or uniforms as a contiguous fp32 [n] tensor on dev.  The draw takes floor(2^24 u): of other
     types that much is kept, so that what is below one stays so."""
-    if isinstance(u, (int, float)):
+    if isinstance(u, numbers.Real):
         u = math.floor(u * 2 ** 24) / 2 ** 24 if abs(u) < 1 else u
     elif u is not None and not (isinstance(u, torch.Tensor) and u.dtype in (torch.float32, torch.float16, torch.bfloat16)):
         u = torch.floor(torch.as_tensor(u, dtype=torch.float64) * 2 ** 24) / 2 ** 24
@@ -830,8 +848,8 @@ def spec_sample(logits: torch.Tensor, u: Optional[torch.Tensor] = None, temperat
         raise ValueError("rows_per_setting must be at least 1")
     n = -(-rows // rows_per_setting)
     t_all = 0.0
-    if isinstance(temperature, (int, float)):
-        t_all, temperature = float(temperature), None
+    if isinstance(temperature, numbers.Real):
+        t_all, temperature = _fp32_number(temperature), None
     else:
         temperature = _setting(temperature, torch.float32, n, dev, "temperature")
     u = _uniforms(u, rows, dev)
