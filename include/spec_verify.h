@@ -464,8 +464,8 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
  * and of the others those of the largest weight[b, h, .] (equal ones: the earlier token; NaN
  * counts as the smallest).  Outputs: new_len [B] = m; kept [B, n_kv_heads, keep] = their
  * positions, rising, -1 behind the last; weight_out [B, n_kv_heads, weight_out_len] = their
- * weights, zeros behind (weight_out_len >= keep; neither it nor new_len may overlap its
- * input); and their K and V in cells 0..m-1 of
+ * weights, zeros behind (weight_out_len >= keep; none of these may overlap another one or
+ * what the call reads); and their K and V in cells 0..m-1 of
  * dst_table [B, dst_pages] (64 * dst_pages >= keep), as if the held values were written
  * there in one call.  The pages of dst_table are pages of the same pool, named once, that
  * page_table does not name in this call (a page shared with another sequence stays as it is;

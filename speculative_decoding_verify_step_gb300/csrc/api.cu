@@ -1805,6 +1805,23 @@ spec_status spec_kv8_evict(int32_t B, const int32_t* kv_len, const int32_t* page
   if (overlap(weight, groups * weight_len * 4, weight_out, groups * weight_out_len * 4))
     return fail(SPEC_ERR_INVALID_ARG, "weight_out overlaps weight");
   if (overlap(kv_len, 4ll * B, new_len, 4ll * B)) return fail(SPEC_ERR_INVALID_ARG, "new_len overlaps kv_len");
+  // what one kernel writes the other takes positions and pages from
+  const struct {
+    const void* p;
+    long long bytes;
+    const char* name;
+  } span[] = {{new_len, 4ll * B, "new_len"},
+              {kept, groups * keep * 4, "kept"},
+              {weight_out, groups * weight_out_len * 4, "weight_out"},
+              {kv_len, 4ll * B, "kv_len"},
+              {page_table, 4ll * B * max_pages, "page_table"},
+              {dst_table, 4ll * B * dst_pages, "dst_table"},
+              {weight, groups * weight_len * 4, "weight"},
+              {pool, (long long)num_pages * n_kv_heads * kv8_block_bytes(head_dim), "pool"}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (overlap(span[i].p, span[i].bytes, span[j].p, span[j].bytes))
+        return fail(SPEC_ERR_INVALID_ARG, "%s overlaps %s", span[i].name, span[j].name);
   Kv8EvictParams p{};
   p.pool = static_cast<uint8_t*>(pool);
   p.kv_len = kv_len;

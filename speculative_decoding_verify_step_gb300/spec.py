@@ -750,7 +750,7 @@ def spec_kv8_evict(pool: torch.Tensor, weight: torch.Tensor, kv_len: torch.Tenso
     move, in order, to the pages of dst_table (pages of the same pool that page_table does not
     name).  Returns (new_len [B], kept positions [B, n_kv_heads, keep] with -1 behind the last,
     their weights with zeros behind, as many tokens as weight has or `keep`); `outs`:
-    preallocated, not kv_len or weight themselves."""
+    preallocated, apart from each other and from the inputs."""
     lib = _lib or load_library()
     P, H, hd, B, width = _kv8_geometry(pool, kv_len, page_table, None)
     dev, keep, recent = pool.device, int(keep), int(recent)
