@@ -1640,6 +1640,17 @@ bool overlap(const void* a, long long a_bytes, const void* b, long long b_bytes)
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
+// Arrays of 4-byte numbers; any may be NULL.
+struct Words {
+  const void* p;
+  const char* name;
+};
+template <size_t N>
+spec_status check_words(const Words (&words)[N]) {
+  for (const Words& w : words)
+    if (reinterpret_cast<uintptr_t>(w.p) & 3u) return fail(SPEC_ERR_INVALID_ARG, "%s must be 4-byte aligned", w.name);
+  return SPEC_OK;
+}
 }  // namespace
 extern "C" {
 
@@ -1655,6 +1666,7 @@ spec_status spec_kv8_write(int32_t B, int32_t rows_per_seq, int32_t total_rows, 
     return s;
   if (total_rows == 0) return SPEC_OK;
   if (!start || !page_table) return fail(SPEC_ERR_INVALID_ARG, "start or page_table is NULL");
+  if (spec_status s = check_words({{row_off, "row_off"}, {start, "start"}, {page_table, "page_table"}})) return s;
   if (spec_status s = kv4_check_ptr(k, "k")) return s;
   if (spec_status s = kv4_check_ptr(v, "v")) return s;
   if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
@@ -1682,6 +1694,7 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
     return s;
   if (total_rows == 0) return SPEC_OK;
   if (!start || !page_table) return fail(SPEC_ERR_INVALID_ARG, "start or page_table is NULL");
+  if (spec_status s = check_words({{row_off, "row_off"}, {start, "start"}, {page_table, "page_table"}})) return s;
   if (spec_status s = kv4_check_ptr(k, "k")) return s;
   if (spec_status s = kv4_check_ptr(v, "v")) return s;
   if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
@@ -1738,10 +1751,10 @@ spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const i
   }
   if (total_rows == 0) return SPEC_OK;
   if (!kv_len || !page_table) return fail(SPEC_ERR_INVALID_ARG, "kv_len or page_table is NULL");
+  if (spec_status s = check_words({{row_off, "row_off"}, {kv_len, "kv_len"}, {page_table, "page_table"}, {weight, "weight"}})) return s;
   if (spec_status s = kv4_check_ptr(q, "q")) return s;
   if (spec_status s = kv4_check_ptr(out, "out")) return s;
   if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
-  if (reinterpret_cast<uintptr_t>(weight) & 3u) return fail(SPEC_ERR_INVALID_ARG, "weight must be 4-byte aligned");
   if (spec_status s = kv4_check_stride(q_stride, (long long)n_heads * head_dim, "q_stride")) return s;
   // the weights may need q again, after out
   if (weight && overlap(q, ((total_rows - 1) * q_stride + (long long)n_heads * head_dim) * 2, out,
@@ -1799,8 +1812,9 @@ spec_status spec_kv8_evict(int32_t B, const int32_t* kv_len, const int32_t* page
   if (!kv_len || !page_table || !dst_table || !weight || !new_len || !kept || !weight_out)
     return fail(SPEC_ERR_INVALID_ARG, "NULL argument");
   if (spec_status s = kv4_check_ptr(pool, "pool")) return s;
-  if ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(weight_out)) & 3u)
-    return fail(SPEC_ERR_INVALID_ARG, "weight and weight_out must be 4-byte aligned");
+  if (spec_status s = check_words({{kv_len, "kv_len"}, {page_table, "page_table"}, {dst_table, "dst_table"}, {weight, "weight"},
+                                   {new_len, "new_len"}, {kept, "kept"}, {weight_out, "weight_out"}}))
+    return s;
   const long long groups = (long long)B * n_kv_heads;
   if (overlap(weight, groups * weight_len * 4, weight_out, groups * weight_out_len * 4))
     return fail(SPEC_ERR_INVALID_ARG, "weight_out overlaps weight");
@@ -1863,6 +1877,9 @@ spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dty
   if (!u && (temperature || temperature_all != 0.f)) return fail(SPEC_ERR_INVALID_ARG, "sampling needs uniforms u");
   if (reinterpret_cast<uintptr_t>(logits) & (dtype == SPEC_F32 ? 3u : 1u))
     return fail(SPEC_ERR_INVALID_ARG, "logits are not aligned to their type");
+  if (spec_status s = check_words({{u, "u"}, {temperature, "temperature"}, {top_k, "top_k"}, {top_p, "top_p"}, {min_p, "min_p"},
+                                   {tokens, "tokens"}, {probs, "probs"}}))
+    return s;
   SampleParams p{};
   p.logits = logits;
   p.row_stride = row_stride;
