@@ -495,7 +495,8 @@ spec_status spec_kv8_evict(int32_t B, const int32_t* kv_len, const int32_t* page
  * (temperature not 0 and outside 1e-6..1e30; top_k < 0; top_p outside (0, 1];
  * min_p outside [0, 1]; u outside [0, 1)), gets token -1 and a row of zeros.
  * No call allocates or keeps state.  V <= 393216, rows <= 2^24.  u may be NULL where
- * temperature is NULL and temperature_all 0. */
+ * temperature is NULL and temperature_all 0.  Neither output may overlap the other or an
+ * input, but probs may be the logits themselves (fp32, row_stride V). */
 spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dtype, int64_t row_stride, const float* u,
                         float temperature_all, const float* temperature, const int32_t* top_k, const float* top_p,
                         const float* min_p, int32_t rows_per_setting, int32_t* tokens, float* probs, void* stream);

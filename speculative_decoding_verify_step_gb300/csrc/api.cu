@@ -1880,6 +1880,26 @@ spec_status spec_sample(int32_t rows, int32_t V, const void* logits, int32_t dty
   if (spec_status s = check_words({{u, "u"}, {temperature, "temperature"}, {top_k, "top_k"}, {top_p, "top_p"}, {min_p, "min_p"},
                                    {tokens, "tokens"}, {probs, "probs"}}))
     return s;
+  // a row's outputs are written while others are read; q in its own logits' place is what a row alone reads
+  const long long row_bytes = rows * 4ll, set_bytes = ((long long)rows + rows_per_setting - 1) / rows_per_setting * 4;
+  const long long logit_bytes = ((rows - 1) * row_stride + V) * (dtype == SPEC_F32 ? 4 : 2);
+  const struct {
+    const void* p;
+    long long bytes;
+    const char* name;
+  } span[] = {{tokens, row_bytes, "tokens"},
+              {probs, row_bytes * V, "probs"},
+              {logits, logit_bytes, "logits"},
+              {u, row_bytes, "u"},
+              {temperature, set_bytes, "temperature"},
+              {top_k, set_bytes, "top_k"},
+              {top_p, set_bytes, "top_p"},
+              {min_p, set_bytes, "min_p"}};
+  const bool in_place = probs == logits && dtype == SPEC_F32 && (row_stride == V || rows == 1);
+  for (int i = 0; i < 2; ++i)
+    for (int j = i + 1; j < 8; ++j)
+      if (span[i].p && span[j].p && !(i == 1 && j == 2 && in_place) && overlap(span[i].p, span[i].bytes, span[j].p, span[j].bytes))
+        return fail(SPEC_ERR_INVALID_ARG, "%s overlaps %s", span[i].name, span[j].name);
   SampleParams p{};
   p.logits = logits;
   p.row_stride = row_stride;

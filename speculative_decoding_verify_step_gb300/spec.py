@@ -829,9 +829,11 @@ def spec_sample(logits: torch.Tensor, u: Optional[torch.Tensor] = None, temperat
     uniforms u [...] in [0, 1), and with return_probs the distribution q it was drawn from: a
     drafter's x and q of spec_verify_step.  temperature (0: the largest logit; u may be None),
     top_k, top_p, min_p: a number for all rows, or one for each rows_per_setting rows (None:
-    off); lists are copied from the host, so a call inside a graph capture takes tensors.  Returns (tokens int32 [...], probs fp32 [..., V] or None); a row without a logit
-    above -infinity, or with a setting or u out of range, gives -1 and zeros.  `outs`:
-    preallocated (tokens, probs or None)."""
+    off; top_k of V or more too); lists are copied from the host, so a call inside a graph
+    capture takes tensors.  Returns (tokens int32 [...], probs fp32 [..., V] or None); a row
+    without a logit above -infinity, or with a setting or u out of range, gives -1 and zeros.
+    `outs`: preallocated (tokens, probs or None), apart from each other and the inputs, but
+    probs may be contiguous fp32 logits themselves."""
     lib = _lib or load_library()
     dtype, shape, dev = _SAMPLE_DTYPE.get(logits.dtype), logits.shape, logits.device
     if dtype is None or not logits.is_cuda or len(shape) < 1 or shape[-1] < 1:
