@@ -448,8 +448,14 @@ spec_status spec_kv8_read(int32_t B, int32_t rows_per_seq, int32_t total_rows, c
  * weight (may be NULL): device [B, n_kv_heads, weight_len] fp32; weight[b, h, t] grows by
  * the attention weights that the rows of sequence b's window give token t (positions below
  * weight_len), summed over the window's rows and the query heads of kv head h: what
- * spec_kv8_evict ranks by; out must not overlap q then.  workspace: spec_kv8_attention_workspace() bytes for the same
- * arguments (0: none needed; -1: a shape the call refuses), as there. */
+ * spec_kv8_evict ranks by; out must not overlap q then.  A call only adds, for every row and
+ * token of the window.  Where drafts are rejected, so that kv_len falls, the caller clears
+ * weight[b, :, kv_len ..] before other tokens are written there; the rejected rows' shares
+ * on the tokens that stay are gone only if a copy from before those rows is put back (or
+ * weight is passed for accepted rows alone).  In the cache a rejected token leaves the
+ * exponent that it raised, until a write starts the sub-block anew.
+ * workspace: spec_kv8_attention_workspace() bytes for the same arguments (0: none needed;
+ * -1: a shape the call refuses), as there. */
 int64_t spec_kv8_attention_workspace(int32_t B, int32_t W, int32_t total_rows, int32_t n_heads, int32_t n_kv_heads,
                                      int32_t head_dim, int32_t max_pages, int32_t max_kv_len, int32_t with_weight);
 spec_status spec_kv8_attention(int32_t B, int32_t W, int32_t total_rows, const int32_t* row_off, const int32_t* kv_len,

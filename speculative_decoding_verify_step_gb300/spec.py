@@ -706,7 +706,8 @@ def spec_kv8_attention(q: torch.Tensor, pool: torch.Tensor, kv_len: torch.Tensor
     """Attention of verify windows over the 8-bit cache: spec_kv4_attention's arguments and
     rules.  weight [B, n_kv_heads, tokens] fp32: grows by the attention weight that each token
     gets, summed over the window's rows and the query heads of a kv head (for spec_kv8_evict); out
-    must not be q then."""
+    must not be q then.  After rejected drafts clear weight[b, :, kv_len:] (and put a copy from before
+    them back, if their shares on other tokens shall not count)."""
     lib = _lib or load_library()
     P, H, hd, B, width = _kv8_geometry(pool, kv_len, page_table, row_off)
     dev, ragged = pool.device, row_off is not None
