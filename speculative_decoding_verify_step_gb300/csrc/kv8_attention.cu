@@ -32,8 +32,8 @@
 // of the rows from all partials, through distributed shared memory.
 //
 // What bounds it (8 kv heads of 128 with 4 query heads).  Two tiles of query rows: the cache's bytes,
-// 8 x 32768 tokens at width 4 in 92 us, 0.86 of the copy rate (a decode step of the same 87, 0.91).  Three
-// and four: latencies, since 242 registers leave two warps per SM quarter: 64 x 512..2048 at
+// 8 x 32768 tokens at width 4 in 92.5 us, 0.86 of the copy rate (a decode step of the same 87, 0.91).  Three
+// and four: latencies, since 243 registers leave two warps per SM quarter: 64 x 512..2048 at
 // width 5 in 63 us, 0.41.  Short caches: one chain of latencies, 1 x 1024 tokens in 6.5 us.
 #include <math.h>
 
@@ -858,7 +858,7 @@ constexpr int row_tiles(int rows) { return ((rows + 7) / 8 + row_blocks(rows) - 
 // against pieces, in us (8 kv heads of 128 with 4 query heads; units of a CTA in brackets): decode,
 // 1 x 4096 tokens 8.9, 9.2 (16), 1 x 8192 11.7, 9.9 (32); 4 x 4096 10.0, 12.1 (32), 8 x 2048 9.8, 11.4
 // (32); width 5, 4 x 4096 17.1, 18.1 (32), 16 x 1024 17.9, 19.5 (32); 16 x 5003, 4 heads of 64,
-// width 4 12.0, 12.6 (40).
+// width 4 12.0, 12.6 (40), and 16 x 0..5003 at widths 1 to 7 11.7, 12.7 (40).
 int cluster_size(int B, int Hkv, int rows, int len_hint, int sm_count) {
   const long long groups = (long long)B * Hkv * row_blocks(rows), units = (len_hint + kUnit - 1) / kUnit;
   int cs = 1;

@@ -39,8 +39,10 @@
 //
 // What bounds it: chains of short steps (cluster barriers of 0.8 us, instructions fetched once per
 // row), not bytes.  GPU us against the bytes at the copy rate: 1 x 128256 fp32 with top_p 22.6 (0.08),
-// 64 x 128256 fp32 with top_k, top_p and q 28.2 (9.7), 256 x 50257 bf16, settings per row, 73.5 (3.8):
-// there the masses of rows without top_k.  Decisions by histograms of all CTAs alone, without
+// 64 x 128256 fp32 with top_k, top_p and q 28.2 (9.7), 256 x 50257 bf16, settings per row, 73 (3.8): there
+// the 51 rows without top_k, a mass and four shared atomics per token on two CTAs each, which run on when
+// the others have ended (the 51 alone take 45, the 205 others alone 38; with the 51 first the batch takes
+// 61).  Decisions by histograms of all CTAs alone, without
 // candidates, took 41, 111 and 340; sorting every list of candidates 27.6, 33.7 and 88.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
