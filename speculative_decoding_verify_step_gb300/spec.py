@@ -804,7 +804,7 @@ def _setting(t, dtype, n: int, dev, what: str):
     if not isinstance(t, torch.Tensor):
         t = torch.as_tensor(t) if whole else torch.as_tensor(t, dtype=torch.float64)
     if t.dtype is not dtype and whole:
-        t = (torch.nan_to_num(t.floor(), nan=-1.0).double() if t.is_floating_point() else t).clamp(-1, _INT_MAX)
+        t = (torch.nan_to_num(t.double().floor(), nan=-1.0) if t.is_floating_point() else t.long()).clamp(-1, _INT_MAX)
     elif t.dtype is torch.float64 and dtype is torch.float32:
         t = torch.where((t != 0) & (t.abs() < _FP32_LEAST), torch.copysign(torch.full_like(t, _FP32_LEAST), t), t)
     if t.dtype is not dtype or t.device != dev or not t.is_contiguous():
